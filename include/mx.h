@@ -257,6 +257,84 @@ mx_status mx_quantize_2d_blocks(const void* x, int32_t dtype, int64_t rows, int6
 mx_status mx_scale_mismatch_map(const void* x, int32_t dtype, int64_t rows, int64_t cols,
                                 int64_t ld, int32_t scale_rule, int8_t* map, void* stream);
 
+/* RMS norm with the residual's addition, row by row over x [rows][cols]:
+ *   s = x + residual (in fp32, rounded to dtype; s = x when residual is NULL),
+ *   rho = 1 / sqrt(mean(s^2) + eps),   y = s * rho * gamma.
+ * x, residual, sum and y have type dtype (MX_BF16 or MX_F32) and leading dimensions ldx, ldr, lds
+ * and ldy in elements; gamma [cols] has type gamma_dtype. sum receives s, the new residual stream;
+ * rstd [rows] (fp32) receives rho, which mx_rmsnorm_backward reads. residual, sum and rstd may be
+ * NULL (ldr and lds are then ignored). The norm takes the rounded s, so it can be recomputed from
+ * the stored sum. The sum of squares, rho and y are formed in 64 bits and every output is rounded
+ * once, to the nearest value, so a row's outputs depend on that row alone (not on how many rows
+ * share the call). A row that holds an infinity or a NaN gives NaNs (or zeros beside an infinity),
+ * as the formula does. sum and y may each be x or residual itself (same leading dimension).
+ * cols is a multiple of 32 and at most 32768 (MX_ERR_UNSUPPORTED beyond); pointers to rows and
+ * gamma 16-byte aligned, rstd 4-byte, every leading dimension * element size a multiple of 16
+ * bytes. Errors (nothing is launched): MX_ERR_NULL for a NULL x, gamma or y; MX_ERR_SHAPE for
+ * negative sizes, a leading dimension below cols or the multiple-of rules; MX_ERR_ARG for a bad
+ * type, a misaligned pointer or an eps that is negative or not finite. rows == 0 or cols == 0 is a
+ * no-op. */
+mx_status mx_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t dtype,
+                     int64_t rows, int64_t cols, const void* gamma, int32_t gamma_dtype, float eps,
+                     void* sum, int64_t lds, void* y, int64_t ldy, float* rstd, void* stream);
+
+/* mx_rmsnorm with y quantized in 1x32 blocks along the row, MXFP4 or MXFP8: codes, scales, opts
+ * and fmt as for mx_quantize (axis = 1) and mx_quantize_mxfp8 (axis = 1), stochastic-rounding
+ * index r * cols + c. The values that are quantized are the unrounded y: with opts->hadamard the
+ * signs and the 32-point transform are applied in 64 bits, and each value is rounded once, to its
+ * code. y is optional here (NULL: only the codes are written; ldy ignored). Alignment of codes:
+ * 16 bytes (MXFP4), 8 bytes (MXFP8). Errors as for mx_rmsnorm, plus those of the quantizers for
+ * opts, fmt, codes and scales. */
+mx_status mx_rmsnorm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                           int32_t dtype, int64_t rows, int64_t cols, const void* gamma,
+                           int32_t gamma_dtype, float eps, void* sum, int64_t lds, void* y,
+                           int64_t ldy, float* rstd, const mx_quant_opts* opts, uint8_t* codes,
+                           uint8_t* scales, void* stream);
+mx_status mx_rmsnorm_quant_mxfp8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                 int32_t dtype, int64_t rows, int64_t cols, const void* gamma,
+                                 int32_t gamma_dtype, float eps, void* sum, int64_t lds, void* y,
+                                 int64_t ldy, float* rstd, int32_t fmt, const mx_quant_opts* opts,
+                                 uint8_t* codes, uint8_t* scales, void* stream);
+
+/* Backward pass of mx_rmsnorm (the quantizers are the identity, straight-through). From dy (the
+ * gradient of y), dsum (the gradient that reaches the stored sum from further on; may be NULL), s
+ * (the stored sum) and rstd:  u = dy * gamma, z = s * rstd, c = mean over the row of u * z,
+ *   dx = rstd * (u - z * c) + dsum     (the gradient of x and of residual alike),
+ *   dgamma[j] = sum over the rows of dy * z   (fp32; may be NULL).
+ * fp32 throughout, dx rounded to dtype at the end; the order of every sum is fixed by the sizes.
+ * dx may be dy or dsum itself (same leading dimension). With dgamma, workspace holds at least
+ * mx_rmsnorm_backward_workspace(rows, cols) bytes, 16-byte aligned; its contents are scratch, and
+ * calls that may run at the same time need one each. Sizes, alignment and errors as for
+ * mx_rmsnorm; MX_ERR_ARG also for a workspace that is too small. rows == 0 writes a zero dgamma. */
+int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
+mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, int64_t ldds,
+                              const void* s, int64_t lds, int32_t dtype, int64_t rows,
+                              int64_t cols, const void* gamma, int32_t gamma_dtype,
+                              const float* rstd, void* dx, int64_t lddx, float* dgamma,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Product of a few tokens with MXFP4 weights, the activations not quantized (decoding):
+ *   y[t][n] = 2^alpha_exp * sum_k x'[t][k] * W[n][k]
+ * x: [T][ldx], dtype MX_BF16 or MX_F32; W: codes wq [N][K/2] and scales ws of granularity gw (1,
+ * 32 or 64), as for mx_gemm_fprop; y: [T][ldy], out_dtype. With hadamard = 1 every 32-block of x
+ * is rotated like mx_quantize rotates it (signs of sign_mask, then the transform, in fp32), for
+ * weights that were quantized rotated; alpha_exp = -5 then undoes the factor 32. T and N are
+ * arbitrary (N a multiple of gw), K a multiple of 32. x and its rows (ldx * element size) 16-byte
+ * aligned, wq 16-byte aligned, y aligned to its elements, ldy >= N. The weights are read once for
+ * every 64 tokens; many more tokens are the GEMMs' work.
+ * Accuracy: fp32 accumulation. The products are exact, sums of 128 of them are formed by the
+ * matrix core, which drops what lies below 2^-24 of a sum's largest term, and joined in fp32:
+ * |y - exact| <= 2^-16 * sum_k |x'_k W_k| before the rounding to bf16 (K <= 65536). A weight
+ * beyond bf16's range, 2^128 or more (scale bytes 253 and 254), counts as infinity; scale byte
+ * 255 is NaN.
+ * Errors (nothing is launched): MX_ERR_SHAPE, MX_ERR_ARG (types, granularity, hadamard, alpha_exp
+ * outside [-126, 127], alignment), MX_ERR_NULL, MX_ERR_LAUNCH (N above 2^26 or T above 2^19 rows).
+ * T == 0 or N == 0 is a no-op; K == 0 writes zeros. */
+mx_status mx_gemv(const void* x, int32_t dtype, int64_t ldx, const uint8_t* wq, const uint8_t* ws,
+                  int32_t gw, int64_t T, int64_t N, int64_t K, int32_t hadamard,
+                  uint32_t sign_mask, int32_t alpha_exp, int32_t out_dtype, void* y, int64_t ldy,
+                  void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* mx_status_string(int32_t status);
 

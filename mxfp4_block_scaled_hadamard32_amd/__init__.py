@@ -14,6 +14,10 @@ in the library's HIP kernels.
   mx_scale_mismatch_map   per-element scale exponent of the row block minus the column block
   mx_quantize_mxfp8 / mx_gemm_mxfp8   MXFP8 (E4M3 / E5M2 elements, the same E8M0 block scales)
                   quantize and block-scaled GEMM, for the query / key projections
+  mx_rmsnorm / mx_rmsnorm_quant / mx_rmsnorm_quant_mxfp8   RMS norm with the residual's addition,
+                  its result in the input's type and / or quantized in 1x32 blocks
+  mx_rmsnorm_backward   gradients of the norm's input and weight
+  mx_gemv         product of a few tokens (bf16 / fp32, not quantized) with MXFP4 weights
 """
 from __future__ import annotations
 
@@ -27,7 +31,8 @@ from ._lib import (MX_BF16, MX_E4M3, MX_E5M2, MX_F32, MX_ROUND_RNE, MX_ROUND_SR,
 
 __all__ = ["mx_quantize", "mx_quantize_2d", "mx_dequantize", "mx_gemm_fprop", "mx_gemm_dgrad",
            "mx_gemm_wgrad", "mx_gemm_fprop_quant", "mx_quantize_mxfp8", "mx_gemm_mxfp8", "mx_quantize_2d_blocks",
-           "mx_scale_mismatch_map", "MxError",
+           "mx_scale_mismatch_map", "mx_rmsnorm", "mx_rmsnorm_quant", "mx_rmsnorm_quant_mxfp8",
+           "mx_rmsnorm_backward", "mx_gemv", "MxError",
            "MX_SCALE_FLOOR", "MX_SCALE_CEIL", "MX_ROUND_RNE", "MX_ROUND_SR", "MX_E4M3", "MX_E5M2",
            "lib"]
 
@@ -290,4 +295,174 @@ def mx_scale_mismatch_map(x: torch.Tensor, scale_rule: int = MX_SCALE_FLOOR, out
     _buf(out, "out", (rows, cols), (torch.int8,), x.device)
     check(lib().mx_scale_mismatch_map(_ptr(x), _dtype_code(x), rows, cols, ld, int(scale_rule),
                                       _ptr(out), _stream(stream)), "mx_scale_mismatch_map")
+    return out
+
+
+def _launch(name, device, stream, *args):
+    """One library call on `stream` (None: the device's current stream), with the tensors' device
+    current during the call."""
+    fn = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        check(fn(*args, _stream(stream)), name)
+    else:
+        with torch.cuda.device(device):
+            check(fn(*args, _stream(stream)), name)
+
+
+def _rows(t, name: str):
+    """A 2-D CUDA tensor of bf16 or fp32 with contiguous rows; returns (rows, cols, ld). The
+    stride of a single row says nothing, so its leading dimension is its length."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be bfloat16 or float32")
+    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D CUDA tensor with contiguous rows")
+    rows, cols = t.shape
+    return rows, cols, t.stride(0) if rows > 1 else cols
+
+
+def _rows_like(t, name: str, x):
+    """Another [rows][cols] operand of x's shape, type and device; returns its ld."""
+    if _rows(t, name)[:2] != tuple(x.shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
+    if t.dtype != x.dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {x.dtype}")
+    if t.device != x.device:
+        raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
+
+
+_CODE = {torch.bfloat16: MX_BF16, torch.float32: MX_F32}
+_FLOATS = (torch.bfloat16, torch.float32)
+_F32 = (torch.float32,)
+
+
+def _norm_args(x, gamma, residual, eps, sum, y, with_y, rstd):
+    """Checks the norm's tensors and allocates the outputs that are not given; returns the leading
+    arguments of the C calls and (y, s, rstd)."""
+    rows, cols, ldx = _rows(x, "x")
+    dev = x.device
+    _buf(gamma, "gamma", (cols,), _FLOATS, dev)
+    ldr = lds = ldy = 0
+    s = x
+    if residual is not None:
+        ldr = _rows_like(residual, "residual", x)
+        if sum is None:
+            sum = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+        s = sum
+    if sum is not None:
+        lds = _rows_like(sum, "sum", x)
+    if y is None and with_y:
+        y = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+    if y is not None:
+        ldy = _rows_like(y, "y", x)
+    if rstd is None:
+        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+    else:
+        _buf(rstd, "rstd", (rows,), _F32, dev)
+    args = (x.data_ptr(), ldx, _data(residual), ldr, _CODE[x.dtype], rows, cols, gamma.data_ptr(),
+            _CODE[gamma.dtype], float(eps), _data(sum), lds, _data(y), ldy, rstd.data_ptr())
+    return args, (y, s, rstd)
+
+
+def mx_rmsnorm(x, gamma, residual=None, eps: float = 1e-5, sum=None, y=None, rstd=None,
+               stream=None):
+    """RMS norm of s = x + residual by rows: y = s / sqrt(mean(s^2) + eps) * gamma.
+    x, residual [rows][cols] bf16 or fp32 (cols a multiple of 32, at most 32768), gamma [cols]
+    bf16 or fp32 -> (y, s, rstd [rows] fp32); s is x itself without a residual."""
+    args, out = _norm_args(x, gamma, residual, eps, sum, y, True, rstd)
+    _launch("mx_rmsnorm", x.device, stream, *args)
+    return out
+
+
+def mx_rmsnorm_quant(x, gamma, residual=None, eps: float = 1e-5, scale_rule: int = MX_SCALE_FLOOR,
+                     round: int = MX_ROUND_RNE, hadamard: int = 0, sign_mask: int = 0,
+                     seed: int = 0, with_y: bool = False, codes=None, scales=None, sum=None,
+                     y=None, rstd=None, stream=None):
+    """mx_rmsnorm with its result in MXFP4, 1x32 blocks along the row -> (codes [rows][cols/2],
+    scales [rows][cols/32], y or None, s, rstd). y is written with with_y or when a buffer is
+    given."""
+    args, out = _norm_args(x, gamma, residual, eps, sum, y, with_y, rstd)
+    rows, cols = x.shape
+    codes = _codes_out(codes, "codes", (rows, cols // 2), x.device)
+    scales = _codes_out(scales, "scales", (rows, cols // 32), x.device)
+    o = _opts(scale_rule, round, hadamard, sign_mask, seed)
+    _launch("mx_rmsnorm_quant", x.device, stream, *args, ctypes.byref(o), codes.data_ptr(),
+            scales.data_ptr())
+    return (codes, scales) + out
+
+
+def mx_rmsnorm_quant_mxfp8(x, gamma, residual=None, eps: float = 1e-5, fmt: int = MX_E4M3,
+                           scale_rule: int = MX_SCALE_FLOOR, round: int = MX_ROUND_RNE,
+                           hadamard: int = 0, sign_mask: int = 0, seed: int = 0,
+                           with_y: bool = False, codes=None, scales=None, sum=None, y=None,
+                           rstd=None, stream=None):
+    """mx_rmsnorm with its result in MXFP8 (fmt MX_E4M3 or MX_E5M2), 1x32 blocks along the row ->
+    (codes [rows][cols], scales [rows][cols/32], y or None, s, rstd)."""
+    args, out = _norm_args(x, gamma, residual, eps, sum, y, with_y, rstd)
+    rows, cols = x.shape
+    codes = _codes_out(codes, "codes", (rows, cols), x.device)
+    scales = _codes_out(scales, "scales", (rows, cols // 32), x.device)
+    o = _opts(scale_rule, round, hadamard, sign_mask, seed)
+    _launch("mx_rmsnorm_quant_mxfp8", x.device, stream, *args, int(fmt), ctypes.byref(o),
+            codes.data_ptr(), scales.data_ptr())
+    return (codes, scales) + out
+
+
+def mx_rmsnorm_backward(dy, s, gamma, rstd, dsum=None, with_dgamma: bool = True, dx=None,
+                        dgamma=None, workspace=None, stream=None):
+    """Gradients of mx_rmsnorm from dy, the stored sum s, rstd and (optionally) the gradient dsum
+    that reaches the sum from further on -> (dx, of x and of residual alike; dgamma [cols] fp32,
+    None without with_dgamma). workspace: a uint8 buffer of at least
+    lib().mx_rmsnorm_backward_workspace(rows, cols) bytes, allocated per call when None."""
+    rows, cols, lds = _rows(s, "s")
+    dev = s.device
+    lddy = _rows_like(dy, "dy", s)
+    ldds = 0 if dsum is None else _rows_like(dsum, "dsum", s)
+    _buf(gamma, "gamma", (cols,), _FLOATS, dev)
+    _buf(rstd, "rstd", (rows,), _F32, dev)
+    if dx is None:
+        dx = torch.empty((rows, cols), dtype=s.dtype, device=dev)
+    lddx = _rows_like(dx, "dx", s)
+    size = 0
+    if with_dgamma:
+        if dgamma is None:
+            dgamma = torch.empty((cols,), dtype=torch.float32, device=dev)
+        else:
+            _buf(dgamma, "dgamma", (cols,), _F32, dev)
+        if workspace is None:
+            size = lib().mx_rmsnorm_backward_workspace(rows, cols)
+            # from the pool of the stream that uses it: a later allocation there comes after it
+            with torch.cuda.stream(stream):
+                workspace = torch.empty((size,), dtype=torch.uint8, device=dev)
+        else:
+            size = workspace.numel()
+            _buf(workspace, "workspace", (size,), _U8, dev)
+    else:
+        dgamma = workspace = None
+    _launch("mx_rmsnorm_backward", dev, stream, dy.data_ptr(), lddy, _data(dsum), ldds,
+            s.data_ptr(), lds, _CODE[s.dtype], rows, cols, gamma.data_ptr(), _CODE[gamma.dtype],
+            rstd.data_ptr(), dx.data_ptr(), lddx, _data(dgamma), _data(workspace), size)
+    return dx, dgamma
+
+
+def mx_gemv(x, wq, ws, gw: int = 1, hadamard: int = 0, sign_mask: int = 0, alpha_exp: int = 0,
+            out_dtype=torch.bfloat16, out=None, stream=None):
+    """y[T][N] = 2^alpha x W^T for a few tokens x [T][K] (bf16 or fp32, not quantized) and MXFP4
+    weights wq [N][K/2], ws [N/gw][K/32]; hadamard = 1 rotates x as mx_quantize does (for weights
+    quantized rotated, with alpha_exp = -5)."""
+    T, K, ldx = _rows(x, "x")
+    N, Kw = _operand(wq, ws, gw, "W")
+    if Kw != K or wq.device != x.device:
+        raise ValueError("operands disagree on the reduction length or the device")
+    out, code = _out(out, T, N, out_dtype, x.device)
+    ldy = out.stride(0) if T > 1 else N
+    _launch("mx_gemv", x.device, stream, x.data_ptr(), _CODE[x.dtype], ldx, wq.data_ptr(),
+            ws.data_ptr(), int(gw), T, N, K, int(hadamard), int(sign_mask) & 0xFFFFFFFF,
+            int(alpha_exp), code, out.data_ptr(), ldy)
     return out

@@ -58,9 +58,22 @@ def lib() -> ctypes.CDLL:
     L.mx_quantize_2d_blocks.argtypes = [vp, i32, i64, i64, i64, i32, ctypes.POINTER(mx_quant_opts),
                                         vp, vp, vp, vp, vp]
     L.mx_scale_mismatch_map.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp]
+    opts = ctypes.POINTER(mx_quant_opts)
+    f32 = ctypes.c_float
+    norm_args = [vp, i64, vp, i64, i32, i64, i64, vp, i32, f32, vp, i64, vp, i64, vp]
+    L.mx_rmsnorm.argtypes = norm_args + [vp]
+    L.mx_rmsnorm_quant.argtypes = norm_args + [opts, vp, vp, vp]
+    L.mx_rmsnorm_quant_mxfp8.argtypes = norm_args + [i32, opts, vp, vp, vp]
+    L.mx_rmsnorm_backward.argtypes = [vp, i64, vp, i64, vp, i64, i32, i64, i64, vp, i32, vp, vp,
+                                      i64, vp, vp, i64, vp]
+    L.mx_rmsnorm_backward_workspace.argtypes = [i64, i64]
+    L.mx_rmsnorm_backward_workspace.restype = i64
+    L.mx_gemv.argtypes = [vp, i32, i64, vp, vp, i32, i64, i64, i64, i32, u32, i32, i32, vp, i64,
+                          vp]
     for name in ("mx_quantize", "mx_quantize_2d", "mx_dequantize", "mx_gemm_fprop",
                  "mx_gemm_dgrad", "mx_gemm_wgrad", "mx_gemm_fprop_quant", "mx_quantize_mxfp8",
-                 "mx_gemm_mxfp8", "mx_quantize_2d_blocks", "mx_scale_mismatch_map"):
+                 "mx_gemm_mxfp8", "mx_quantize_2d_blocks", "mx_scale_mismatch_map", "mx_rmsnorm",
+                 "mx_rmsnorm_quant", "mx_rmsnorm_quant_mxfp8", "mx_rmsnorm_backward", "mx_gemv"):
         getattr(L, name).restype = ctypes.c_int
     L.mx_status_string.argtypes = [i32]
     L.mx_status_string.restype = ctypes.c_char_p

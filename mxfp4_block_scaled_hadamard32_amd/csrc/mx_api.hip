@@ -5,7 +5,7 @@
 
 namespace {
 
-constexpr int32_t kVersion = 100;  // 0.1.0
+constexpr int32_t kVersion = 200;  // 0.2.0
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -51,6 +51,68 @@ mx_status gemm(const uint8_t* a, const uint8_t* as, int32_t ga, const uint8_t* b
   }
   GemmArgs g{a, as, ga, b, bs, gb, M, N, K, alpha_exp, out_dtype == MX_BF16, c, ldc, stream};
   return launch_status(mx_launch_gemm(g));
+}
+
+// rows of a norm operand: type-sized leading dimension and 16-byte rows
+mx_status check_rows(const void* p, int64_t ld, int64_t cols, int32_t dtype) {
+  const int64_t esize = dtype == MX_BF16 ? 2 : 4;
+  if (ld < cols || (ld * esize) % 16 != 0) return MX_ERR_SHAPE;
+  return aligned(p, 16) ? MX_OK : MX_ERR_ARG;
+}
+
+mx_status check_norm_sizes(int32_t dtype, int64_t rows, int64_t cols, int32_t gamma_dtype) {
+  if (dtype != MX_F32 && dtype != MX_BF16) return MX_ERR_ARG;
+  if (gamma_dtype != MX_F32 && gamma_dtype != MX_BF16) return MX_ERR_ARG;
+  if (rows < 0 || cols < 0 || cols % 32 != 0) return MX_ERR_SHAPE;
+  return cols > kNormMaxCols ? MX_ERR_UNSUPPORTED : MX_OK;
+}
+
+// fmt 0: y only (required); 1, 2, 3: E2M1, E4M3, E5M2 codes, y optional
+mx_status rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t dtype,
+                  int64_t rows, int64_t cols, const void* gamma, int32_t gamma_dtype, float eps,
+                  void* sum, int64_t lds, void* y, int64_t ldy, float* rstd, int fmt,
+                  const mx_quant_opts* opts, uint8_t* codes, uint8_t* scales, void* stream) {
+  mx_status s;
+  if (fmt != 0 && (s = check_opts(opts)) != MX_OK) return s;
+  if ((s = check_norm_sizes(dtype, rows, cols, gamma_dtype)) != MX_OK) return s;
+  if (!(eps >= 0.0f) || eps > 3.402823466e+38f) return MX_ERR_ARG;
+  if ((s = check_rows(x, ldx, cols, dtype)) != MX_OK) return s;
+  if (residual && (s = check_rows(residual, ldr, cols, dtype)) != MX_OK) return s;
+  if (sum && (s = check_rows(sum, lds, cols, dtype)) != MX_OK) return s;
+  if ((y || fmt == 0) && (s = check_rows(y, ldy, cols, dtype)) != MX_OK) return s;
+  if (!aligned(gamma, 16) || !aligned(rstd, 4) || !aligned(codes, fmt == 1 ? 16 : 8))
+    return MX_ERR_ARG;
+  if (rows == 0 || cols == 0) return MX_OK;
+  if (!x || !gamma) return MX_ERR_NULL;
+  if (fmt == 0 ? !y : (!codes || !scales)) return MX_ERR_NULL;
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.gamma = gamma;
+  a.sum = sum;
+  a.y = y;
+  a.rstd = rstd;
+  a.codes = codes;
+  a.scales = scales;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.lds = lds;
+  a.ldy = ldy;
+  a.eps = eps;
+  a.fmt = fmt;
+  a.bf16 = dtype == MX_BF16;
+  a.gamma_bf16 = gamma_dtype == MX_BF16;
+  if (fmt != 0) {
+    a.seed = opts->seed;
+    a.sign_mask = opts->sign_mask;
+    a.ceil = opts->scale_rule == MX_SCALE_CEIL;
+    a.sr = opts->round == MX_ROUND_SR;
+    a.hadamard = opts->hadamard == 1;
+  }
+  a.stream = stream;
+  return launch_status(mx_launch_rmsnorm(a));
 }
 
 }  // namespace
@@ -221,6 +283,82 @@ mx_status mx_scale_mismatch_map(const void* x, int32_t dtype, int64_t rows, int6
   if (!aligned(map, 8)) return MX_ERR_ARG;
   return launch_status(mx_launch_scale_mismatch(x, dtype == MX_BF16, rows, cols, ld,
                                                 scale_rule == MX_SCALE_CEIL, map, stream));
+}
+
+mx_status mx_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t dtype,
+                     int64_t rows, int64_t cols, const void* gamma, int32_t gamma_dtype, float eps,
+                     void* sum, int64_t lds, void* y, int64_t ldy, float* rstd, void* stream) {
+  return rmsnorm(x, ldx, residual, ldr, dtype, rows, cols, gamma, gamma_dtype, eps, sum, lds, y,
+                 ldy, rstd, 0, nullptr, nullptr, nullptr, stream);
+}
+
+mx_status mx_rmsnorm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                           int32_t dtype, int64_t rows, int64_t cols, const void* gamma,
+                           int32_t gamma_dtype, float eps, void* sum, int64_t lds, void* y,
+                           int64_t ldy, float* rstd, const mx_quant_opts* opts, uint8_t* codes,
+                           uint8_t* scales, void* stream) {
+  return rmsnorm(x, ldx, residual, ldr, dtype, rows, cols, gamma, gamma_dtype, eps, sum, lds, y,
+                 ldy, rstd, 1, opts, codes, scales, stream);
+}
+
+mx_status mx_rmsnorm_quant_mxfp8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                                 int32_t dtype, int64_t rows, int64_t cols, const void* gamma,
+                                 int32_t gamma_dtype, float eps, void* sum, int64_t lds, void* y,
+                                 int64_t ldy, float* rstd, int32_t fmt, const mx_quant_opts* opts,
+                                 uint8_t* codes, uint8_t* scales, void* stream) {
+  if (fmt != MX_E4M3 && fmt != MX_E5M2) return MX_ERR_ARG;
+  return rmsnorm(x, ldx, residual, ldr, dtype, rows, cols, gamma, gamma_dtype, eps, sum, lds, y,
+                 ldy, rstd, 2 + fmt, opts, codes, scales, stream);
+}
+
+int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || cols % 32 != 0 || cols > kNormMaxCols) return 0;
+  return mx_norm_backward_blocks(rows, cols) * cols * (int64_t)sizeof(float);
+}
+
+mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, int64_t ldds,
+                              const void* s, int64_t lds, int32_t dtype, int64_t rows,
+                              int64_t cols, const void* gamma, int32_t gamma_dtype,
+                              const float* rstd, void* dx, int64_t lddx, float* dgamma,
+                              void* workspace, int64_t workspace_bytes, void* stream) {
+  mx_status st = check_norm_sizes(dtype, rows, cols, gamma_dtype);
+  if (st != MX_OK) return st;
+  if ((st = check_rows(dy, lddy, cols, dtype)) != MX_OK) return st;
+  if (dsum && (st = check_rows(dsum, ldds, cols, dtype)) != MX_OK) return st;
+  if ((st = check_rows(s, lds, cols, dtype)) != MX_OK) return st;
+  if ((st = check_rows(dx, lddx, cols, dtype)) != MX_OK) return st;
+  if (!aligned(gamma, 16) || !aligned(rstd, 4) || !aligned(dgamma, 4) || !aligned(workspace, 16))
+    return MX_ERR_ARG;
+  if (cols == 0 || (rows == 0 && !dgamma)) return MX_OK;
+  if (rows > 0) {
+    if (!dy || !s || !gamma || !rstd || !dx) return MX_ERR_NULL;
+    if (dgamma && !workspace) return MX_ERR_NULL;
+    if (dgamma && workspace_bytes < mx_rmsnorm_backward_workspace(rows, cols)) return MX_ERR_ARG;
+  }
+  NormBackwardArgs a{dy,   dsum, s,    gamma, rstd, dx,   dgamma, dgamma ? (float*)workspace : nullptr,
+                     rows, cols, lddy, ldds,  lds,  lddx, dtype == MX_BF16,
+                     gamma_dtype == MX_BF16, stream};
+  return launch_status(mx_launch_rmsnorm_backward(a));
+}
+
+mx_status mx_gemv(const void* x, int32_t dtype, int64_t ldx, const uint8_t* wq, const uint8_t* ws,
+                  int32_t gw, int64_t T, int64_t N, int64_t K, int32_t hadamard,
+                  uint32_t sign_mask, int32_t alpha_exp, int32_t out_dtype, void* y, int64_t ldy,
+                  void* stream) {
+  mx_status s = check_source(x, dtype, T, K, ldx);
+  if (s != MX_OK) return s;
+  if (N < 0 || K % 32 || ldy < N) return MX_ERR_SHAPE;
+  if (!granularity_ok(gw)) return MX_ERR_ARG;
+  if (N % gw) return MX_ERR_SHAPE;
+  if (hadamard != 0 && hadamard != 1) return MX_ERR_ARG;
+  if (out_dtype != MX_F32 && out_dtype != MX_BF16) return MX_ERR_ARG;
+  if (alpha_exp < -126 || alpha_exp > 127) return MX_ERR_ARG;
+  if (!aligned(y, out_dtype == MX_BF16 ? 2 : 4) || !aligned(wq, 16)) return MX_ERR_ARG;
+  if (T == 0 || N == 0) return MX_OK;
+  if (!y || (K > 0 && (!x || !wq || !ws))) return MX_ERR_NULL;
+  GemvArgs a{x, wq, ws, y, T, N, K, ldx, ldy, gw, alpha_exp, sign_mask, dtype == MX_BF16,
+             hadamard == 1, out_dtype == MX_BF16, stream};
+  return launch_status(mx_launch_gemv(a));
 }
 
 const char* mx_status_string(int32_t status) {

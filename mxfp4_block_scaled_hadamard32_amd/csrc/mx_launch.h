@@ -1,5 +1,5 @@
 // mx_launch.h — internal interface between the C ABI layer (mx_api.hip) and the kernel
-// launchers (quant.hip, gemm.hip). Arguments are already validated when these are called.
+// launchers (quant.hip, gemm.hip, norm.hip, gemv.hip). Arguments are already validated when these are called.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -71,3 +71,58 @@ hipError_t mx_launch_gemm_quant(const GemmArgs& g, const GemmQuantOut& q);
 // MXFP8 GEMM: A [M][K], B [N][K] one code byte per element (afmt / bfmt: 0 = E4M3, 1 = E5M2),
 // scales [M][K/32] and [N][K/32] (ga = gb = 1). K must be a positive multiple of 128.
 hipError_t mx_launch_gemm_fp8(const GemmArgs& g, int afmt, int bfmt);
+
+// RMS norm of [rows][cols] (cols a positive multiple of 32, at most kNormMaxCols): s = x
+// (+ residual), outputs each optional: the rounded sum, y, rstd, and codes with scales of fmt
+// 0 none, 1 E2M1, 2 E4M3, 3 E5M2.
+constexpr int64_t kNormMaxCols = 32768;
+struct NormArgs {
+  const void* x;
+  const void* residual;
+  const void* gamma;
+  void* sum;
+  void* y;
+  float* rstd;
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t rows, cols, ldx, ldr, lds, ldy;
+  uint64_t seed;
+  float eps;
+  uint32_t sign_mask;
+  int fmt;
+  bool bf16, gamma_bf16, ceil, sr, hadamard;
+  void* stream;
+};
+hipError_t mx_launch_rmsnorm(const NormArgs& a);
+
+// Its backward pass. partial: mx_norm_backward_blocks(rows, cols) * cols floats, NULL with dgamma.
+struct NormBackwardArgs {
+  const void* dy;
+  const void* dsum;
+  const void* s;
+  const void* gamma;
+  const float* rstd;
+  void* dx;
+  float* dgamma;
+  float* partial;
+  int64_t rows, cols, lddy, ldds, lds, lddx;
+  bool bf16, gamma_bf16;
+  void* stream;
+};
+int64_t mx_norm_backward_blocks(int64_t rows, int64_t cols);
+hipError_t mx_launch_rmsnorm_backward(const NormBackwardArgs& a);
+
+// y[t][n] = 2^alpha * sum_k x[t][k] * W[n][k]; x bf16 or fp32, W packed E2M1 with scales
+// [N/gw][K/32].
+struct GemvArgs {
+  const void* x;
+  const uint8_t* w;
+  const uint8_t* ws;
+  void* y;
+  int64_t T, N, K, ldx, ldy;
+  int gw, alpha;
+  uint32_t sign_mask;
+  bool bf16, hadamard, out_bf16;
+  void* stream;
+};
+hipError_t mx_launch_gemv(const GemvArgs& a);

@@ -1,0 +1,194 @@
+"""Products of a few tokens with MXFP4 weights against float64: fp32 output within 2^-16 sum|x w|
+(the documented bound: a step's 128 products lose at most 132 times 2^-24 of their magnitude in
+the matrix core, and at most 72 fp32 additions join them), bf16 output the rounding of such a
+value. With the rotation, five fp32 stages round each x' five times: 5 more half steps."""
+import numpy as np
+import pytest
+import torch
+
+import workloads as wl
+from tests import norm_reference as ref
+from tests.parity import check_gemm
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+BOUND = 2.0 ** -16
+MASK = 0x2C6FE9B1
+
+
+@pytest.fixture(scope="module")
+def mx():
+    import mxfp4_block_scaled_hadamard32_amd as m
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    m.lib()
+    return m
+
+
+def weights(N, K, g=1, seed=1):
+    """Any codes, scale exponents -10 .. 9."""
+    rng = np.random.default_rng(seed)
+    return (rng.integers(0, 256, (N, K // 2), dtype=np.uint8),
+            rng.integers(117, 137, (N // g, K // 32), dtype=np.uint8))
+
+
+def tokens(T, K, dtype, seed=9):
+    return wl.student_t3((T, K), seed=seed).to(DT[dtype])
+
+
+def expected(orc, x, wq, ws, g, hadamard=0, mask=0, alpha=0, rows=None):
+    W = orc.dequantize_f64(wq, ws, wq.shape[0], 2 * wq.shape[1], g, rows)
+    X = x.double().numpy()
+    if hadamard:
+        X = ref.hadamard_f64(X, mask)
+    f = 2.0 ** alpha
+    return X @ W.T * f, np.abs(X) @ np.abs(W).T * f
+
+
+def up(*arrays):
+    return tuple(torch.from_numpy(a).to(DEV) for a in arrays)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N,K", [(1, 1, 32), (1, 17, 64), (2, 15, 96), (1, 100, 4096),
+                                   (3, 256, 160), (15, 33, 2720), (16, 1003, 4128),
+                                   (17, 64, 1024), (33, 130, 544), (37, 1003, 4128), (64, 96, 128),
+                                   (65, 48, 288), (130, 80, 2048), (1, 4096, 4096),
+                                   (5, 14336, 512), (16, 28672, 256), (1, 512, 28672),
+                                   (40, 9000, 256)])
+def test_against_float64(mx, orc, T, N, K, dtype):
+    x = tokens(T, K, dtype)
+    wq, ws = weights(N, K)
+    C, Cabs = expected(orc, x, wq, ws, 1)
+    dq, ds = up(wq, ws)
+    check_gemm(mx.mx_gemv(x.to(DEV), dq, ds, out_dtype=torch.float32), C, Cabs, rel=BOUND)
+    check_gemm(mx.mx_gemv(x.to(DEV), dq, ds), C, Cabs, rel=BOUND)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N,K", [(1, 40, 4096), (7, 300, 1056), (16, 5000, 256), (35, 64, 512),
+                                   (64, 200, 160)])
+def test_rotated_weights(mx, orc, T, N, K, dtype):
+    """Weights as mx_quantize makes them with the signed transform; fp32's five stages on x."""
+    w = wl.normal((N, K), 0.02, seed=4).to(torch.bfloat16)
+    dq, ds = mx.mx_quantize(w.to(DEV), hadamard=1, sign_mask=MASK, scale_rule=1)
+    x = tokens(T, K, dtype)
+    C, Cabs = expected(orc, x, dq.cpu().numpy(), ds.cpu().numpy(), 1, 1, MASK, -5)
+    # a stage's rounding is relative to its own value, at most the block's sum of |x|: count the
+    # five half steps on sum |x| per block times |w|
+    W = np.abs(orc.dequantize_f64(dq.cpu().numpy(), ds.cpu().numpy(), N, K, 1))
+    A = np.abs(x.double().numpy()).reshape(T, K // 32, 32).sum(2).repeat(32, axis=1) @ W.T / 32
+    y = mx.mx_gemv(x.to(DEV), dq, ds, hadamard=1, sign_mask=MASK, alpha_exp=-5,
+                   out_dtype=torch.float32)
+    check_gemm(y, C, BOUND * Cabs + 5 * 2.0 ** -24 * A, rel=1.0)
+    # the same product as the unrotated layer, up to the quantization of the weights
+    plain = x.double() @ w.double().t()
+    rel = float((y.double().cpu() - plain).norm() / plain.norm())
+    assert rel < 0.25, rel
+
+
+@pytest.mark.parametrize("g", [32, 64])
+@pytest.mark.parametrize("T,N,K", [(1, 192, 256), (20, 4096, 320)])
+def test_tile_scales(mx, orc, g, T, N, K):
+    x = tokens(T, K, "bf16")
+    wq, ws = weights(N, K, g)
+    C, Cabs = expected(orc, x, wq, ws, g)
+    dq, ds = up(wq, ws)
+    check_gemm(mx.mx_gemv(x.to(DEV), dq, ds, g, out_dtype=torch.float32), C, Cabs, rel=BOUND)
+
+
+@pytest.mark.parametrize("T", [1, 18, 50])
+def test_leading_dimensions(mx, orc, T):
+    K, N = 288, 77
+    x = tokens(T, K, "bf16")
+    wq, ws = weights(N, K)
+    dq, ds = up(wq, ws)
+    wide = torch.full((T, K + 24), float("nan"), dtype=torch.bfloat16, device=DEV)
+    wide[:, :K] = x.to(DEV)
+    out = torch.full((T + 2, N + 3), 7.0, dtype=torch.float32, device=DEV)
+    y = mx.mx_gemv(wide[:, :K], dq, ds, alpha_exp=3, out=out[1:T + 1, :N])
+    C, Cabs = expected(orc, x, wq, ws, 1, alpha=3)
+    check_gemm(y, C, Cabs, rel=BOUND)
+    assert (out[0] == 7).all() and (out[T + 1] == 7).all() and (out[:, N:] == 7).all()
+    if T > 1:
+        again = mx.mx_gemv(x.to(DEV), dq, ds, alpha_exp=3, out_dtype=torch.float32)
+        assert torch.equal(again, y)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_special_values(mx, dtype):
+    """An infinity or NaN in x stays in its token; a NaN scale in its output; zeros give zeros."""
+    T, N, K = 6, 40, 160
+    wq, ws = weights(N, K)
+    wq[wq & 7 == 0] |= 1  # no zero weights: infinity times zero is a NaN
+    wq[wq & 0x70 == 0] |= 0x10
+    ws[7, 3] = 255
+    x = tokens(T, K, dtype)
+    x[0] = 0.0
+    x[1, 40] = float("inf")
+    x[2, 99] = float("nan")
+    x[3] = (x[3].float() * 1e30).to(x.dtype)
+    x[4] = (x[4].float() * 1e-36).to(x.dtype)
+    y = mx.mx_gemv(x.to(DEV), *up(wq, ws), out_dtype=torch.float32).cpu()
+    keep = [n for n in range(N) if n != 7]
+    assert torch.isnan(y[:, 7]).all()
+    assert (y[0, keep] == 0).all()
+    assert torch.isinf(y[1, keep]).all()
+    assert torch.isnan(y[2]).all()
+    assert torch.isfinite(y[3:, keep]).all() and (y[3:, keep] != 0).all()
+
+
+def test_empty(mx):
+    q, s = up(*weights(32, 64))
+    x = torch.ones((3, 64), dtype=torch.bfloat16, device=DEV)
+    assert mx.mx_gemv(x[:0], q, s).shape == (0, 32)
+    assert mx.mx_gemv(x, q[:0], s[:0]).shape == (3, 0)
+    out = torch.full((3, 40), 7.0, device=DEV)
+    mx.mx_gemv(x[:, :0], q[:, :0].contiguous(), s[:, :0].contiguous(), out=out[:, :32])
+    assert (out[:, :32] == 0).all() and (out[:, 32:] == 7).all()
+
+
+def test_offsets_past_32_bits(mx, orc):
+    """Codes of 4.3 GB: the rows at the end against float64; outputs 2^31 elements apart."""
+    N, K = (1 << 20) + 7, 8192
+    q = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV)
+    s = torch.randint(117, 137, (N, K // 32), dtype=torch.uint8, device=DEV)
+    x = tokens(2, K, "bf16")
+    buf = torch.empty((1 << 31) + N, dtype=torch.bfloat16, device=DEV)
+    out = buf.as_strided((2, N), (1 << 31, 1))
+    y = mx.mx_gemv(x.to(DEV), q, s, out=out)
+    pick = np.r_[0:64, N // 2:N // 2 + 64, N - 64:N]
+    p = torch.from_numpy(pick).to(DEV)
+    C, Cabs = expected(orc, x, q[p].cpu().numpy(), s[p].cpu().numpy(), 1)
+    check_gemm(y[:, p], C, Cabs, rel=BOUND)
+
+
+def test_streams_and_graph_replays(mx):
+    """Two captured products on streams of their own replayed at once, beside eager calls."""
+    K, N = 4096, 1040
+    q, s = up(*weights(N, K))
+    xs = [torch.zeros((t, K), dtype=torch.bfloat16, device=DEV) for t in (1, 20)]
+    for x in xs:
+        mx.mx_gemv(x, q, s)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(mx.mx_gemv(x, q, s))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in xs]
+    for seed in (1, 2, 3):
+        for x in xs:
+            x.copy_(tokens(x.shape[0], K, "bf16", seed))
+        eager = [mx.mx_gemv(x, q, s) for x in xs]
+        torch.cuda.synchronize()
+        for o in outs:
+            o.fill_(1)
+        torch.cuda.synchronize()
+        for st, g in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(eager, outs):
+            assert torch.equal(a, b)
