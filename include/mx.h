@@ -324,7 +324,8 @@ mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, in
  * every 64 tokens; many more tokens are the GEMMs' work.
  * Accuracy: fp32 accumulation. The products are exact, sums of 128 of them are formed by the
  * matrix core, which drops what lies below 2^-24 of a sum's largest term, and joined in fp32:
- * |y - exact| <= 2^-16 * sum_k |x'_k W_k| before the rounding to bf16 (K <= 65536). A weight
+ * |y - exact| <= 2^-16 * sum_k |x'_k W_k| before the rounding to bf16 (K <= 65536). bf16 tokens
+ * that are rotated for a bf16 y keep 16 bits of each x' (another 2^-17 of the sum). A weight
  * beyond bf16's range, 2^128 or more (scale bytes 253 and 254), counts as infinity; scale byte
  * 255 is NaN.
  * Errors (nothing is launched): MX_ERR_SHAPE, MX_ERR_ARG (types, granularity, hadamard, alpha_exp

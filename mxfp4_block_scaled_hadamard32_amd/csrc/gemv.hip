@@ -5,15 +5,16 @@
 //
 // The weights are read once and are the traffic: 17/32 byte each. A wave takes 16 weight rows and
 // 128 columns of K a step: lane (n, g) = (lane & 15, lane >> 4) reads the 16 code bytes of row n's
-// block 4 step + g (64 contiguous bytes a row) and its scale byte, and the converter turns them
-// into 32 bf16 values, exact because the scale is a power of two. v_mfma_f32_16x16x32_bf16 number
-// j of the step takes values 8j .. 8j+7 of every lane as the reduction index, and the same values
-// of x: the order of k inside a product is free as long as both operands share it.
+// block 4 step + g (64 contiguous bytes a row), and the converter turns them into 32 bf16 values,
+// exact because the block's scale is a power of two. v_mfma_f32_16x16x32_bf16 number j of the step
+// takes values 8j .. 8j+7 of every lane's block as its reduction index, and the same values of x:
+// the order of k inside a product is free as long as both operands share it.
 //
-// fp32 activations (and rotated ones) go in as three bf16 terms that add up to the fp32 value:
-// x = hi + mid + lo by truncation, 8 significant bits each.
+// fp32 activations (and rotated ones) go in as bf16 terms that add up to the fp32 value.
 #include "mx_device.h"
 #include "mx_launch.h"
+
+#include <type_traits>
 
 using namespace mxd;
 
@@ -22,79 +23,83 @@ namespace {
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
-constexpr int kWaves = 8;  // share a workgroup's rows, each a part of K
-
-// 8 codes (a word) times the block's scale as 8 bf16 values
-__device__ __forceinline__ bf16x8_t weights8(uint32_t w, float scale) {
-  u32x4 o;
-  o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
-  o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
-  o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
-  o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
-  return __builtin_bit_cast(bf16x8_t, o);
-}
-
-// 2^(b - 127) with b = 0 the subnormal 2^-127 and b = 255 an infinity, which the converter takes
-// as E8M0's NaN
-__device__ __forceinline__ float e8m0(uint32_t b) {
-  return __uint_as_float(b == 0u ? 0x00400000u : b << 23);
-}
-
-// v = hi + mid + lo exactly (down to bf16's least subnormal); an infinity or NaN stays in hi
-__device__ __forceinline__ void split3(float v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-  const uint32_t b = __float_as_uint(v);
-  hi = b >> 16;
-  if ((b & 0x7F800000u) == 0x7F800000u) {
-    hi |= (b & 0x7FFFFFu) ? 0x40u : 0u;  // a NaN whose payload sits in the dropped bits
-    mid = lo = 0u;
-    return;
+// the 32 weights of a block (16 code bytes), times the block's scale: byte b is 2^(b - 127), byte 0
+// the subnormal 2^-127; byte 255 is an infinity here, which the converter takes as E8M0's NaN
+__device__ __forceinline__ void weights_of(u32x4 q, uint32_t scale, bf16x8_t (&w)[4]) {
+  const uint32_t b = scale << 23;
+  const float f = __uint_as_float(b > 0x00400000u ? b : 0x00400000u);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const u32x4 o = {
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[j], f, 0)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[j], f, 1)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[j], f, 2)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[j], f, 3))};
+    w[j] = __builtin_bit_cast(bf16x8_t, o);
   }
-  const float r = v - __uint_as_float(b & 0xFFFF0000u);
-  const uint32_t rb = __float_as_uint(r);
-  mid = rb >> 16;
-  lo = __float_as_uint(r - __uint_as_float(rb & 0xFFFF0000u)) >> 16;
 }
 
-// A lane's 32 values of x for one step: row m, block b (64 or 128 bytes). SPLIT: three terms.
-template <bool SPLIT>
-struct Activations {
-  u32x4 f[SPLIT ? 3 : 1][4];
+// 16 bytes at any address
+__device__ __forceinline__ u32x4 load16_any(const uint8_t* p) {
+  u32x4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+
+// Two fp32 values as NT pairs of bf16 terms: a truncated first term, then what is left, truncated
+// again, then the rest; with NT = 3 the terms add up to the value exactly (down to bf16's least
+// subnormal), with NT = 2 the second one is rounded to nearest: 16 bits, 2^-17 of the value. The
+// remainder of an infinity is zero, not a NaN; a NaN stays one.
+template <int NT>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&o)[NT]) {
+  const uint32_t ab = __float_as_uint(a), bb = __float_as_uint(b);
+  o[0] = __builtin_amdgcn_perm(bb, ab, 0x07060302u);
+  const float ah = __uint_as_float(ab & 0xFFFF0000u), bh = __uint_as_float(bb & 0xFFFF0000u);
+  float ar = a == ah ? 0.0f : a - ah, br = b == bh ? 0.0f : b - bh;
+  if constexpr (NT == 3) {
+    const uint32_t am = __float_as_uint(ar), bm = __float_as_uint(br);
+    o[1] = __builtin_amdgcn_perm(bm, am, 0x07060302u);
+    ar -= __uint_as_float(am & 0xFFFF0000u);
+    br -= __uint_as_float(bm & 0xFFFF0000u);
+  }
+  const bf16x2_t rest = {(__bf16)ar, (__bf16)br};
+  o[NT - 1] = __builtin_bit_cast(uint32_t, rest);
+}
+
+// a block's 32 values of x as they are in memory
+template <bool BF16>
+struct RawX {
+  u32x4 w[BF16 ? 4 : 8];
 };
 
-template <bool BF16, bool HAD>
-__device__ __forceinline__ void load_x(Activations<!BF16 || HAD>& o, const void* x, int64_t at,
-                                       bool on, uint32_t sign_mask) {
-  constexpr bool kSplit = !BF16 || HAD;
-  if (!on) {
+template <bool BF16>
+__device__ __forceinline__ void load_x(RawX<BF16>& o, const uint8_t* p) {
 #pragma unroll
-    for (int s = 0; s < (kSplit ? 3 : 1); ++s)
+  for (int j = 0; j < (BF16 ? 4 : 8); ++j) o.w[j] = reinterpret_cast<const u32x4*>(p)[j];
+}
+
+// the block's values, rotated (HAD), as NT terms of 4 x 8 bf16 values
+template <bool BF16, bool HAD, int NT>
+__device__ __forceinline__ void terms_of(const RawX<BF16>& x, uint32_t sign_mask,
+                                         u32x4 (&f)[NT][4]) {
+  if constexpr (BF16 && !HAD) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o.f[s][j] = u32x4{0u, 0u, 0u, 0u};
-    return;
-  }
-  if constexpr (!kSplit) {
-    const u32x4* p = reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(x) + at);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o.f[0][j] = p[j];
+    for (int j = 0; j < 4; ++j) f[0][j] = x.w[j];
   } else {
     float v[32];
     if constexpr (BF16) {
-      const u32x4* p = reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(x) + at);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float w[8];
-        widen_bf16x8(p[j], w);
+        widen_bf16x8(x.w[j], w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[8 * j + k] = w[k];
       }
     } else {
-      const f32x4* p = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(x) + at);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const f32x4 w = p[j];
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[4 * j + k] = w[k];
-      }
+        for (int k = 0; k < 4; ++k) v[4 * j + k] = __uint_as_float(x.w[j][k]);
     }
     if constexpr (HAD) {
 #pragma unroll
@@ -104,43 +109,217 @@ __device__ __forceinline__ void load_x(Activations<!BF16 || HAD>& o, const void*
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      uint32_t h[4], m[4], l[4];
+      uint32_t o[4][NT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t h0, m0, l0, h1, m1, l1;
-        split3(v[8 * j + 2 * i], h0, m0, l0);
-        split3(v[8 * j + 2 * i + 1], h1, m1, l1);
-        h[i] = h0 | h1 << 16;
-        m[i] = m0 | m1 << 16;
-        l[i] = l0 | l1 << 16;
-      }
-      o.f[0][j] = u32x4{h[0], h[1], h[2], h[3]};
-      o.f[1][j] = u32x4{m[0], m[1], m[2], m[3]};
-      o.f[2][j] = u32x4{l[0], l[1], l[2], l[3]};
+      for (int i = 0; i < 4; ++i) split_pair<NT>(v[8 * j + 2 * i], v[8 * j + 2 * i + 1], o[i]);
+#pragma unroll
+      for (int s = 0; s < NT; ++s) f[s][j] = u32x4{o[0][s], o[1][s], o[2][s], o[3][s]};
     }
   }
 }
 
-// MT tiles of 16 tokens by RT tiles of 16 weight rows a workgroup; the waves take every kWaves-th
-// step of 128 columns and their sums are joined through LDS in a fixed order.
-template <bool BF16, bool HAD, int MT, int RT>
-__global__ __launch_bounds__(64 * kWaves) void gemv_kernel(const GemvArgs a) {
-  constexpr bool kSplit = !BF16 || HAD;
-  __shared__ float red[kWaves][MT * RT * 4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i16 = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
-  const int64_t nb = a.K / 32;
+__device__ __forceinline__ void store_y(const GemvArgs& a, int64_t at, float v) {
+  v *= __uint_as_float((uint32_t)(a.alpha + 127) << 23);
+  if (a.out_bf16) reinterpret_cast<__bf16*>(a.y)[at] = (__bf16)v;
+  else reinterpret_cast<float*>(a.y)[at] = v;
+}
 
+// bytes between the scale rows of a segment of `seg` blocks in LDS
+__host__ __device__ constexpr int scale_pitch(int seg) { return (seg + 15) / 16 * 16 + 4; }
+
+// Up to 16 tokens whose activations fit in LDS: RT tiles of 16 weight rows a workgroup of WV waves,
+// which take turns at groups of 16 blocks of K (4 steps: 256 contiguous code bytes a row). The
+// workgroup first brings the activations (rotated and split there, once) and its rows' scale bytes
+// into LDS, so the loop's only requests to memory are the codes: a step's registers are loaded
+// with the same step of the wave's next group as soon as they have been used. A segment of K
+// (seg blocks) at a time when LDS does not hold all of it. The waves' sums are joined through LDS
+// in a fixed order.
+template <bool BF16, bool HAD, int NT, int RT, int WV>
+__global__ __launch_bounds__(64 * WV) void gemv_kernel(const GemvArgs a, int seg) {
+  constexpr int kThreads = 64 * WV;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i16 = lane & 15, g = lane >> 4;
+  const int T = (int)a.T;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+  const int nb = (int)(a.K / 32);
+  const int pitch = scale_pitch(seg);
+  u32x4* const xl = reinterpret_cast<u32x4*>(lds);  // [NT][seg][4][T] pieces of 8 values
+  uint8_t* const sl = lds + (size_t)NT * seg * 64 * T;
+  const int64_t s0 = n0 / a.gw;  // first scale row
+  const int64_t nlast = (n0 + 16 * RT < a.N ? n0 + 16 * RT : a.N) - 1;
+  const int srows = (int)(nlast / a.gw - s0) + 1;
+
+  // rows and tokens past the end repeat the last one: their products are not stored
   const uint8_t* wrow[RT];
-  const uint8_t* srow[RT];
+  int soff[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     int64_t n = n0 + 16 * r + i16;
-    n = n < a.N ? n : a.N - 1;  // rows past the end repeat the last one and are not stored
-    wrow[r] = a.w + n * (a.K / 2);
+    n = n < a.N ? n : a.N - 1;
+    wrow[r] = a.w + n * (a.K / 2) + 16 * g;
+    soff[r] = (int)(n / a.gw - s0) * pitch + g;
+  }
+  const int t16 = i16 < T ? i16 : T - 1;
+  f32x4 acc[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  for (int k0 = 0; k0 < nb; k0 += seg) {
+    const int n = nb - k0 < seg ? nb - k0 : seg;  // blocks of this segment
+    const int n4 = (n + 3) / 4 * 4, n16 = (n + 15) / 16;
+    const int ng = n / 16;
+    u32x4 q[4][RT];
+    auto load_codes = [&](int grp, int d) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        q[d][r] = *reinterpret_cast<const u32x4*>(wrow[r] + (int64_t)k0 * 16 + grp * 256 + 64 * d);
+    };
+    if (wave < ng) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d) load_codes(wave, d);
+    }
+    if (k0) __syncthreads();  // the segment before has been read
+    // scale bytes, then activations (zeros up to a multiple of 4 blocks)
+    for (int i = threadIdx.x; i < srows * n16; i += kThreads) {
+      const int row = i / n16, b = i % n16 * 16;
+      const uint8_t* p = a.ws + (s0 + row) * nb + k0 + b;
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (b + 16 <= n) {
+        v = load16_any(p);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (b + k < n) v[k >> 2] |= (uint32_t)p[k] << (8 * (k & 3));
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t*>(sl + row * pitch + b + 4 * k) = v[k];
+    }
+    const uint8_t* const x = reinterpret_cast<const uint8_t*>(a.x);
+    if constexpr (BF16 && !HAD) {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < 4 * n4 * T; i += kThreads) {
+        const int t = i / (4 * n4), p = i % (4 * n4);
+        u32x4 w = {0u, 0u, 0u, 0u};
+        if (p < 4 * n)
+          w = *reinterpret_cast<const u32x4*>(x + (t * a.ldx + 32 * (int64_t)k0) * 2 + 16 * p);
+        xl[p * T + t] = w;
+      }
+    } else {
+      for (int i = threadIdx.x; i < n4 * T; i += kThreads) {
+        const int t = i / n4, b = i % n4;
+        RawX<BF16> raw = {};
+        if (b < n) load_x<BF16>(raw, x + (t * a.ldx + 32 * (int64_t)(k0 + b)) * (BF16 ? 2 : 4));
+        u32x4 f[NT][4];
+        terms_of<BF16, HAD, NT>(raw, a.sign_mask, f);
+#pragma unroll
+        for (int s = 0; s < NT; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) xl[((s * seg + b) * 4 + j) * T + t] = f[s][j];
+      }
+    }
+    __syncthreads();
+
+    // the step of blocks b0 .. b0 + 3
+    auto step = [&](const bf16x8_t (&w)[RT][4], int b0) {
+      // the 128 products of a step are summed apart from the running sum: the matrix core
+      // drops what lies 24 bits below the largest term of a sum, so short sums lose less
+      f32x4 p[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) p[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = NT - 1; s >= 0; --s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bf16x8_t f =
+              __builtin_bit_cast(bf16x8_t, xl[((s * seg + b0 + g) * 4 + j) * T + t16]);
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            p[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, w[r][j], p[r], 0, 0, 0);
+        }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[r] += p[r];
+    };
+    if (wave < ng) {
+      int grp = wave;
+      auto group = [&](auto more) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          bf16x8_t w[RT][4];
+#pragma unroll
+          for (int r = 0; r < RT; ++r) weights_of(q[d][r], sl[soff[r] + 16 * grp + 4 * d], w[r]);
+          if constexpr (more()) load_codes(grp + WV, d);
+          step(w, 16 * grp + 4 * d);
+        }
+        grp += WV;
+      };
+      while (grp + WV < ng) group(std::true_type{});
+      group(std::false_type{});
+    }
+    for (int b0 = 16 * ng; b0 < n; b0 += 4) {
+      if ((b0 / 4 + ng) % WV != wave) continue;
+      bf16x8_t w[RT][4];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        u32x4 c = {0u, 0u, 0u, 0u};  // past the end: zero codes, scale bytes and activations
+        if (b0 + g < n) c = *reinterpret_cast<const u32x4*>(wrow[r] + (int64_t)(k0 + b0) * 16);
+        weights_of(c, sl[soff[r] + b0], w[r]);
+      }
+      step(w, b0);
+    }
+  }
+
+  __syncthreads();
+  float* const red = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[(wave * RT * 4 + r * 4 + i) * 64 + lane] = acc[r][i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < 16 * RT * T; e += kThreads) {
+    const int t = e / (16 * RT), c = e % (16 * RT);  // token, row of the tile
+    if (n0 + c >= a.N) continue;
+    const float* p = red + ((c >> 4) * 4 + (t & 3)) * 64 + (t >> 2) * 16 + (c & 15);
+    float v = p[0];
+#pragma unroll
+    for (int s = 1; s < WV; ++s) v += p[s * RT * 256];
+    store_y(a, t * a.ldy + n0 + c, v);
+  }
+}
+
+// More activations than LDS holds: MT tiles of 16 tokens by RT tiles of 16 weight rows a workgroup
+// of WV waves, which take turns at groups of 16 blocks of K (16 scale bytes a row) and read the
+// activations of their steps themselves. With one token tile, the registers of a step's codes and
+// activations are loaded with the same step of the wave's next group as soon as they have been
+// used, so 4 steps are always on the way; with more, a group's codes are requested together.
+template <bool BF16, bool HAD, int NT, int MT, int RT, int WV>
+__global__ __launch_bounds__(64 * WV) void gemv_direct_kernel(const GemvArgs a) {
+  constexpr bool RING = MT == 1;
+  __shared__ float red[WV][MT * RT * 4][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i16 = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+  const int nb = (int)(a.K / 32);
+  constexpr int kBlock = BF16 ? 64 : 128;  // bytes of a block of x
+
+  // Rows and tokens past the end repeat the last one: their products are not stored, and no load
+  // depends on a branch, which would make the waits for the loads after it count on none of them.
+  const uint8_t* wrow[RT];
+  const uint8_t* srow[RT];
+  const uint8_t* xrow[MT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    int64_t n = n0 + 16 * r + i16;
+    n = n < a.N ? n : a.N - 1;
+    wrow[r] = a.w + n * (a.K / 2) + 16 * g;
     srow[r] = a.ws + n / a.gw * nb;
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    int64_t t = m0 + 16 * m + i16;
+    t = t < a.T ? t : a.T - 1;
+    xrow[m] = reinterpret_cast<const uint8_t*>(a.x) + t * a.ldx * (BF16 ? 2 : 4) + g * kBlock;
   }
   f32x4 acc[MT][RT];
 #pragma unroll
@@ -148,42 +327,107 @@ __global__ __launch_bounds__(64 * kWaves) void gemv_kernel(const GemvArgs a) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[m][r] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  for (int64_t b0 = 4 * wave; b0 < nb; b0 += 4 * kWaves) {
-    const int64_t b = b0 + g;
-    const bool in = b < nb;
+  auto load_codes = [&](u32x4 (&q)[RT], int grp, int d) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      q[r] = *reinterpret_cast<const u32x4*>(wrow[r] + (int64_t)grp * 256 + 64 * d);
+  };
+  auto load_scales = [&](u32x4 (&sc)[RT], int grp) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) sc[r] = load16_any(srow[r] + 16 * grp);
+  };
+  auto multiply = [&](const bf16x8_t (&w)[RT][4], const RawX<BF16>& x, int m) {
+    u32x4 f[NT][4];
+    terms_of<BF16, HAD, NT>(x, a.sign_mask, f);
+    f32x4 p[RT];  // a step's products apart from the running sum, as in gemv_kernel
+#pragma unroll
+    for (int r = 0; r < RT; ++r) p[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = NT - 1; s >= 0; --s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          p[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f[s][j]),
+                                                         w[r][j], p[r], 0, 0, 0);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[m][r] += p[r];
+  };
+
+  const int ng = nb / 16;
+  if (wave < ng) {
+    u32x4 q[4][RT], sc[RT];
+    RawX<BF16> x[RING ? 4 : 1];
+    int grp = wave;
+    if constexpr (RING) {  // in the order of the loop, which the waits in it count on
+      load_scales(sc, grp);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        load_codes(q[d], grp, d);
+        load_x<BF16>(x[d], xrow[0] + (int64_t)(16 * grp + 4 * d) * kBlock);
+      }
+    }
+    auto group = [&](auto more) {
+      u32x4 scn[RT];
+      const int next = grp + WV;  // used if there is one
+      if constexpr (RING && more()) load_scales(scn, next);
+      if constexpr (!RING) {
+        load_scales(sc, grp);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) load_codes(q[d], grp, d);
+      }
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        bf16x8_t w[RT][4];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) weights_of(q[d][r], (sc[r][d] >> (8 * g)) & 0xFFu, w[r]);
+        if constexpr (RING) {
+          if constexpr (more()) load_codes(q[d], next, d);
+          multiply(w, x[d], 0);
+          if constexpr (more()) load_x<BF16>(x[d], xrow[0] + (int64_t)(16 * next + 4 * d) * kBlock);
+        } else {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            load_x<BF16>(x[0], xrow[m] + (int64_t)(16 * grp + 4 * d) * kBlock);
+            multiply(w, x[0], m);
+          }
+        }
+      }
+      if constexpr (RING && more()) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) sc[r] = scn[r];
+      }
+      grp = next;
+    };
+    if constexpr (RING) {
+      while (grp + WV < ng) group(std::true_type{});
+      group(std::false_type{});
+    } else {
+      while (grp < ng) group(std::true_type{});
+    }
+  }
+  for (int b0 = 16 * ng; b0 < nb; b0 += 4) {
+    if ((b0 / 4 + ng) % WV != wave) continue;
+    const bool in = b0 + g < nb;  // past the end: zero weights and zero activations
     bf16x8_t w[RT][4];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       u32x4 q = {0u, 0u, 0u, 0u};
-      uint32_t sb = 127u;
+      uint32_t sb = 0u;
       if (in) {
-        q = *reinterpret_cast<const u32x4*>(wrow[r] + 16 * b);
-        sb = srow[r][b];
+        q = *reinterpret_cast<const u32x4*>(wrow[r] + (int64_t)b0 * 16);
+        sb = srow[r][b0 + g];
       }
-      const float scale = e8m0(sb);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[r][j] = weights8(q[j], scale);
+      weights_of(q, sb, w[r]);
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int64_t t = m0 + 16 * m + i16;
-      Activations<kSplit> x;
-      load_x<BF16, HAD>(x, a.x, t * a.ldx + 32 * b, in && t < a.T, a.sign_mask);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        // the 128 products of a step are summed apart from the running sum: the matrix core
-        // drops what lies 24 bits below the largest term of a sum, so short sums lose less
-        f32x4 p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = (kSplit ? 2 : 0); s >= 0; --s)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x.f[s][j]),
-                                                        w[r][j], p, 0, 0, 0);
-        acc[m][r] += p;
-      }
+      RawX<BF16> x = {};
+      if (in) load_x<BF16>(x, xrow[m] + (int64_t)b0 * kBlock);
+      multiply(w, x, m);
     }
   }
+
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -191,19 +435,14 @@ __global__ __launch_bounds__(64 * kWaves) void gemv_kernel(const GemvArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) red[wave][(m * RT + r) * 4 + i][lane] = acc[m][r][i];
   __syncthreads();
-  const float alpha = __uint_as_float((uint32_t)(a.alpha + 127) << 23);
-  for (int e = threadIdx.x; e < MT * RT * 4 * 64; e += 64 * kWaves) {
+  for (int e = threadIdx.x; e < MT * RT * 4 * 64; e += 64 * WV) {
     const int slot = e >> 6, l = e & 63;
     float v = red[0][slot][l];
 #pragma unroll
-    for (int s = 1; s < kWaves; ++s) v += red[s][slot][l];
-    v *= alpha;
+    for (int s = 1; s < WV; ++s) v += red[s][slot][l];
     const int i = slot & 3, r = (slot >> 2) % RT, m = (slot >> 2) / RT;
     const int64_t t = m0 + 16 * m + 4 * (l >> 4) + i, n = n0 + 16 * r + (l & 15);
-    if (t < a.T && n < a.N) {
-      if (a.out_bf16) reinterpret_cast<__bf16*>(a.y)[t * a.ldy + n] = (__bf16)v;
-      else reinterpret_cast<float*>(a.y)[t * a.ldy + n] = v;
-    }
+    if (t < a.T && n < a.N) store_y(a, t * a.ldy + n, v);
   }
 }
 
@@ -217,18 +456,70 @@ __global__ __launch_bounds__(256) void gemv_zero_kernel(const GemvArgs a) {
   }
 }
 
-template <bool BF16, bool HAD, int MT, int RT>
-hipError_t launch_gemv(const GemvArgs& a) {
+template <bool BF16, bool HAD, int NT, int MT, int RT, int WV>
+hipError_t launch_direct(const GemvArgs& a) {
   const int64_t gx = (a.N + 16 * RT - 1) / (16 * RT), gy = (a.T + 16 * MT - 1) / (16 * MT);
-  if (gx > (1 << 22) || gy > 65535) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemv_kernel<BF16, HAD, MT, RT>), dim3((unsigned)gx, (unsigned)gy),
-                     dim3(64 * kWaves), 0, (hipStream_t)a.stream, a);
+  if (gx > (1 << 22) || gy > 32768) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((gemv_direct_kernel<BF16, HAD, NT, MT, RT, WV>), dim3((unsigned)gx, (unsigned)gy),
+                     dim3(64 * WV), 0, (hipStream_t)a.stream, a);
   return hipGetLastError();
 }
 
-template <bool BF16, bool HAD>
+// blocks of K that a workgroup's LDS holds within `bytes`: NT terms of T tokens and the scale rows
+int segment_blocks(const GemvArgs& a, int nt, int rows, int bytes) {
+  const int srows = a.gw == 1 ? rows : (rows + a.gw - 1) / a.gw;
+  const int64_t nb = a.K / 32, nb4 = (nb + 3) / 4 * 4;
+  int64_t seg = (bytes - 20 * srows) / (64 * nt * a.T + srows) / 16 * 16;
+  return (int)(seg < nb4 ? seg : nb4);
+}
+
+template <bool BF16, bool HAD, int NT, int RT, int WV>
+hipError_t launch_gemv(const GemvArgs& a, int bytes) {
+  const int64_t gx = (a.N + 16 * RT - 1) / (16 * RT);
+  if (gx > (1 << 22)) return hipErrorInvalidValue;
+  const int seg = segment_blocks(a, NT, 16 * RT, bytes);
+  const int srows = a.gw == 1 ? 16 * RT : (16 * RT + a.gw - 1) / a.gw;
+  const size_t use = (size_t)NT * seg * 64 * a.T + (size_t)srows * scale_pitch(seg);
+  const size_t join = (size_t)WV * RT * 1024;
+  hipLaunchKernelGGL((gemv_kernel<BF16, HAD, NT, RT, WV>), dim3((unsigned)gx), dim3(64 * WV),
+                     use > join ? use : join, (hipStream_t)a.stream, a, seg);
+  return hipGetLastError();
+}
+
+// Rows a workgroup takes (RT tiles of 16) so that about one workgroup a compute unit is left: more
+// rows share a fetch (and, in gemv_direct_kernel, a split) of the activations, fewer leave compute
+// units idle. 16 tokens, bf16, K 4096: N 14336 11.5 us with 4 tiles (224 workgroups), 16.4 with 2;
+// N 4096 7.3 us with 1 tile (256 workgroups), 8.5 with 2.
+constexpr int64_t kWorkgroups = 200;
+
+template <bool BF16, bool HAD, int NT>
 hipError_t pick_gemv(const GemvArgs& a) {
-  return launch_gemv<BF16, HAD, 1, 1>(a);
+  // Activations through LDS when a workgroup's share of it holds them: always better when they
+  // have to be rotated or split (one token, N 14336, K 4096: rotated 10.9 us, 14.2 read directly;
+  // fp32 11.9 and 14.8), and for one bf16 token (K 28672: 26.9 and 30.1 us); for several bf16
+  // tokens the direct kernel is the faster one (4 tokens, N 14336, K 4096: 9.7 and 11.1 us).
+  constexpr int kLds = 128 * 1024;
+  const bool one = a.T == 1;
+  if ((BF16 && !HAD) ? one : one || (a.T <= 16 && a.T * a.K * 2 * NT <= kLds)) {
+    if (a.N < 16 * 2 * kWorkgroups) return launch_gemv<BF16, HAD, NT, 1, 8>(a, kLds);
+    // 8 waves of 4 KB of codes each are needed to keep long rows coming; short ones leave half of
+    // 8 waves without a group (one token, N 14336, K 4096: 9.3 us with 4, 10.1 with 8)
+    return a.K > 4096 ? launch_gemv<BF16, HAD, NT, 2, 8>(a, kLds)
+                      : launch_gemv<BF16, HAD, NT, 2, 4>(a, kLds);
+  }
+  if (a.N >= 16 * 4 * kWorkgroups) {
+    if constexpr (NT == 1) {
+      // more token tiles share a conversion of the codes: 64 tokens, N 28672, K 8192: 91 us with
+      // 4 tiles, 134 with 1; 32 tokens, N 14336, K 4096: 16.2 us with 2, 20.9 with 1
+      if (a.T > 32) return launch_direct<BF16, HAD, NT, 4, 4, 4>(a);
+      if (a.T > 16) return launch_direct<BF16, HAD, NT, 2, 4, 8>(a);
+      return launch_direct<BF16, HAD, NT, 1, 4, 8>(a);
+    } else {
+      return launch_direct<BF16, HAD, NT, 1, 4, 4>(a);  // 8 waves would spill
+    }
+  }
+  if (a.N >= 16 * 2 * kWorkgroups) return launch_direct<BF16, HAD, NT, 1, 2, 8>(a);
+  return launch_direct<BF16, HAD, NT, 1, 1, 8>(a);
 }
 
 }  // namespace
@@ -240,6 +531,8 @@ hipError_t mx_launch_gemv(const GemvArgs& a) {
                        0, (hipStream_t)a.stream, a);
     return hipGetLastError();
   }
-  if (a.bf16) return a.hadamard ? pick_gemv<true, true>(a) : pick_gemv<true, false>(a);
-  return a.hadamard ? pick_gemv<false, true>(a) : pick_gemv<false, false>(a);
+  if (a.bf16 && !a.hadamard) return pick_gemv<true, false, 1>(a);
+  if (a.bf16 && a.out_bf16) return pick_gemv<true, true, 2>(a);
+  if (a.bf16) return pick_gemv<true, true, 3>(a);
+  return a.hadamard ? pick_gemv<false, true, 3>(a) : pick_gemv<false, false, 3>(a);
 }

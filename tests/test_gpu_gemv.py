@@ -55,7 +55,9 @@ def up(*arrays):
                                    (17, 64, 1024), (33, 130, 544), (37, 1003, 4128), (64, 96, 128),
                                    (65, 48, 288), (130, 80, 2048), (1, 4096, 4096),
                                    (5, 14336, 512), (16, 28672, 256), (1, 512, 28672),
-                                   (40, 9000, 256)])
+                                   (40, 9000, 256), (1, 13000, 8192), (3, 6500, 1056),
+                                   (9, 12900, 4128), (20, 12900, 544), (50, 12900, 1600),
+                                   (1, 40, 65536), (2, 30, 65536), (16, 6401, 8224)])
 def test_against_float64(mx, orc, T, N, K, dtype):
     x = tokens(T, K, dtype)
     wq, ws = weights(N, K)
@@ -67,7 +69,8 @@ def test_against_float64(mx, orc, T, N, K, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,N,K", [(1, 40, 4096), (7, 300, 1056), (16, 5000, 256), (35, 64, 512),
-                                   (64, 200, 160)])
+                                   (64, 200, 160), (2, 14000, 96),
+                                   (1, 13000, 8192), (1, 100, 65536), (20, 13000, 608)])
 def test_rotated_weights(mx, orc, T, N, K, dtype):
     """Weights as mx_quantize makes them with the signed transform; fp32's five stages on x."""
     w = wl.normal((N, K), 0.02, seed=4).to(torch.bfloat16)
@@ -81,6 +84,9 @@ def test_rotated_weights(mx, orc, T, N, K, dtype):
     y = mx.mx_gemv(x.to(DEV), dq, ds, hadamard=1, sign_mask=MASK, alpha_exp=-5,
                    out_dtype=torch.float32)
     check_gemm(y, C, BOUND * Cabs + 5 * 2.0 ** -24 * A, rel=1.0)
+    # bf16 y of bf16 x: 16 bits of each rotated value, half a step is 2^-17
+    y16 = mx.mx_gemv(x.to(DEV), dq, ds, hadamard=1, sign_mask=MASK, alpha_exp=-5)
+    check_gemm(y16, C, (BOUND + 2.0 ** -17) * Cabs + 5 * 2.0 ** -24 * A, rel=1.0)
     # the same product as the unrotated layer, up to the quantization of the weights
     plain = x.double() @ w.double().t()
     rel = float((y.double().cpu() - plain).norm() / plain.norm())
