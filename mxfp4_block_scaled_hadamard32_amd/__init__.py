@@ -66,7 +66,7 @@ def _buf(t, name: str, shape, dtypes, device, rows_only: bool = False):
     for outputs with a leading dimension). Raises ValueError / TypeError otherwise."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != torch.device(device):
+    if t.device != device and t.device != torch.device(device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
@@ -298,15 +298,21 @@ def mx_scale_mismatch_map(x: torch.Tensor, scale_rule: int = MX_SCALE_FLOOR, out
     return out
 
 
+# the current stream of a device as an address, without a Stream object (3 us on the host)
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _launch(name, device, stream, *args):
     """One library call on `stream` (None: the device's current stream), with the tensors' device
     current during the call."""
-    fn = getattr(lib(), name)
+    raw = _current_raw_stream(device.index) if stream is None else stream.cuda_stream
     if device.index == torch.cuda.current_device():
-        check(fn(*args, _stream(stream)), name)
+        status = getattr(_lib.lib(), name)(*args, raw)
     else:
         with torch.cuda.device(device):
-            check(fn(*args, _stream(stream)), name)
+            status = getattr(_lib.lib(), name)(*args, raw)
+    if status:
+        check(status, name)
 
 
 def _rows(t, name: str):
@@ -314,23 +320,27 @@ def _rows(t, name: str):
     stride of a single row says nothing, so its leading dimension is its length."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.bfloat16, torch.float32):
+    if t.dtype not in _CODE:
         raise TypeError(f"{name} must be bfloat16 or float32")
-    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D CUDA tensor with contiguous rows")
     rows, cols = t.shape
-    return rows, cols, t.stride(0) if rows > 1 else cols
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor with contiguous rows")
+    return rows, cols, ld if rows > 1 else cols
 
 
 def _rows_like(t, name: str, x):
     """Another [rows][cols] operand of x's shape, type and device; returns its ld."""
-    if _rows(t, name)[:2] != tuple(x.shape):
+    rows, cols, ld = _rows(t, name)
+    if (rows, cols) != tuple(x.shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")
     if t.dtype != x.dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {x.dtype}")
     if t.device != x.device:
         raise ValueError(f"{name} is on {t.device}, expected {x.device}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return ld
 
 
 def _data(t):
@@ -353,20 +363,22 @@ def _norm_args(x, gamma, residual, eps, sum, y, with_y, rstd):
     if residual is not None:
         ldr = _rows_like(residual, "residual", x)
         if sum is None:
-            sum = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+            sum, lds = torch.empty(rows, cols, dtype=x.dtype, device=dev), cols
+        else:
+            lds = _rows_like(sum, "sum", x)
         s = sum
-    if sum is not None:
+    elif sum is not None:
         lds = _rows_like(sum, "sum", x)
-    if y is None and with_y:
-        y = torch.empty((rows, cols), dtype=x.dtype, device=dev)
     if y is not None:
         ldy = _rows_like(y, "y", x)
+    elif with_y:
+        y, ldy = torch.empty(rows, cols, dtype=x.dtype, device=dev), cols
     if rstd is None:
-        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     else:
         _buf(rstd, "rstd", (rows,), _F32, dev)
     args = (x.data_ptr(), ldx, _data(residual), ldr, _CODE[x.dtype], rows, cols, gamma.data_ptr(),
-            _CODE[gamma.dtype], float(eps), _data(sum), lds, _data(y), ldy, rstd.data_ptr())
+            _CODE[gamma.dtype], eps, _data(sum), lds, _data(y), ldy, rstd.data_ptr())
     return args, (y, s, rstd)
 
 
@@ -380,6 +392,22 @@ def mx_rmsnorm(x, gamma, residual=None, eps: float = 1e-5, sum=None, y=None, rst
     return out
 
 
+def _norm_quant(name, fmt, width, x, gamma, residual, eps, o, with_y, codes, scales, sum, y, rstd,
+                stream):
+    args, out = _norm_args(x, gamma, residual, eps, sum, y, with_y, rstd)
+    rows, cols, dev = args[5], args[6], x.device
+    if codes is None:
+        codes = torch.empty(rows, cols // width, dtype=torch.uint8, device=dev)
+    else:
+        _buf(codes, "codes", (rows, cols // width), _U8, dev)
+    if scales is None:
+        scales = torch.empty(rows, cols // 32, dtype=torch.uint8, device=dev)
+    else:
+        _buf(scales, "scales", (rows, cols // 32), _U8, dev)
+    _launch(name, dev, stream, *args, *fmt, ctypes.byref(o), codes.data_ptr(), scales.data_ptr())
+    return (codes, scales) + out
+
+
 def mx_rmsnorm_quant(x, gamma, residual=None, eps: float = 1e-5, scale_rule: int = MX_SCALE_FLOOR,
                      round: int = MX_ROUND_RNE, hadamard: int = 0, sign_mask: int = 0,
                      seed: int = 0, with_y: bool = False, codes=None, scales=None, sum=None,
@@ -387,14 +415,9 @@ def mx_rmsnorm_quant(x, gamma, residual=None, eps: float = 1e-5, scale_rule: int
     """mx_rmsnorm with its result in MXFP4, 1x32 blocks along the row -> (codes [rows][cols/2],
     scales [rows][cols/32], y or None, s, rstd). y is written with with_y or when a buffer is
     given."""
-    args, out = _norm_args(x, gamma, residual, eps, sum, y, with_y, rstd)
-    rows, cols = x.shape
-    codes = _codes_out(codes, "codes", (rows, cols // 2), x.device)
-    scales = _codes_out(scales, "scales", (rows, cols // 32), x.device)
-    o = _opts(scale_rule, round, hadamard, sign_mask, seed)
-    _launch("mx_rmsnorm_quant", x.device, stream, *args, ctypes.byref(o), codes.data_ptr(),
-            scales.data_ptr())
-    return (codes, scales) + out
+    return _norm_quant("mx_rmsnorm_quant", (), 2, x, gamma, residual, eps,
+                       _opts(scale_rule, round, hadamard, sign_mask, seed), with_y, codes, scales,
+                       sum, y, rstd, stream)
 
 
 def mx_rmsnorm_quant_mxfp8(x, gamma, residual=None, eps: float = 1e-5, fmt: int = MX_E4M3,
@@ -404,14 +427,9 @@ def mx_rmsnorm_quant_mxfp8(x, gamma, residual=None, eps: float = 1e-5, fmt: int 
                            rstd=None, stream=None):
     """mx_rmsnorm with its result in MXFP8 (fmt MX_E4M3 or MX_E5M2), 1x32 blocks along the row ->
     (codes [rows][cols], scales [rows][cols/32], y or None, s, rstd)."""
-    args, out = _norm_args(x, gamma, residual, eps, sum, y, with_y, rstd)
-    rows, cols = x.shape
-    codes = _codes_out(codes, "codes", (rows, cols), x.device)
-    scales = _codes_out(scales, "scales", (rows, cols // 32), x.device)
-    o = _opts(scale_rule, round, hadamard, sign_mask, seed)
-    _launch("mx_rmsnorm_quant_mxfp8", x.device, stream, *args, int(fmt), ctypes.byref(o),
-            codes.data_ptr(), scales.data_ptr())
-    return (codes, scales) + out
+    return _norm_quant("mx_rmsnorm_quant_mxfp8", (int(fmt),), 1, x, gamma, residual, eps,
+                       _opts(scale_rule, round, hadamard, sign_mask, seed), with_y, codes, scales,
+                       sum, y, rstd, stream)
 
 
 def mx_rmsnorm_backward(dy, s, gamma, rstd, dsum=None, with_dgamma: bool = True, dx=None,
@@ -427,22 +445,25 @@ def mx_rmsnorm_backward(dy, s, gamma, rstd, dsum=None, with_dgamma: bool = True,
     _buf(gamma, "gamma", (cols,), _FLOATS, dev)
     _buf(rstd, "rstd", (rows,), _F32, dev)
     if dx is None:
-        dx = torch.empty((rows, cols), dtype=s.dtype, device=dev)
-    lddx = _rows_like(dx, "dx", s)
+        dx, lddx = torch.empty(rows, cols, dtype=s.dtype, device=dev), cols
+    else:
+        lddx = _rows_like(dx, "dx", s)
     size = 0
     if with_dgamma:
         if dgamma is None:
-            dgamma = torch.empty((cols,), dtype=torch.float32, device=dev)
+            dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
         else:
             _buf(dgamma, "dgamma", (cols,), _F32, dev)
-        if workspace is None:
-            size = lib().mx_rmsnorm_backward_workspace(rows, cols)
-            # from the pool of the stream that uses it: a later allocation there comes after it
-            with torch.cuda.stream(stream):
-                workspace = torch.empty((size,), dtype=torch.uint8, device=dev)
-        else:
+        if workspace is not None:
             size = workspace.numel()
             _buf(workspace, "workspace", (size,), _U8, dev)
+        else:
+            size = lib().mx_rmsnorm_backward_workspace(rows, cols)
+            if stream is None:
+                workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            else:  # from the pool of the stream that uses it: what is allocated there next waits
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
         dgamma = workspace = None
     _launch("mx_rmsnorm_backward", dev, stream, dy.data_ptr(), lddy, _data(dsum), ldds,
@@ -458,11 +479,15 @@ def mx_gemv(x, wq, ws, gw: int = 1, hadamard: int = 0, sign_mask: int = 0, alpha
     quantized rotated, with alpha_exp = -5)."""
     T, K, ldx = _rows(x, "x")
     N, Kw = _operand(wq, ws, gw, "W")
-    if Kw != K or wq.device != x.device:
+    dev = x.device
+    if Kw != K or wq.device != dev:
         raise ValueError("operands disagree on the reduction length or the device")
-    out, code = _out(out, T, N, out_dtype, x.device)
-    ldy = out.stride(0) if T > 1 else N
-    _launch("mx_gemv", x.device, stream, x.data_ptr(), _CODE[x.dtype], ldx, wq.data_ptr(),
-            ws.data_ptr(), int(gw), T, N, K, int(hadamard), int(sign_mask) & 0xFFFFFFFF,
-            int(alpha_exp), code, out.data_ptr(), ldy)
+    if out is None and out_dtype in _CODE:
+        out, code, ldy = torch.empty(T, N, dtype=out_dtype, device=dev), _CODE[out_dtype], N
+    else:
+        out, code = _out(out, T, N, out_dtype, dev)
+        ldy = out.stride(0) if T > 1 else N
+    _launch("mx_gemv", dev, stream, x.data_ptr(), _CODE[x.dtype], ldx, wq.data_ptr(),
+            ws.data_ptr(), gw, T, N, K, hadamard, sign_mask & 0xFFFFFFFF, alpha_exp, code,
+            out.data_ptr(), ldy)
     return out
