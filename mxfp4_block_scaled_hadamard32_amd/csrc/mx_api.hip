@@ -337,7 +337,7 @@ mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, in
   }
   NormBackwardArgs a{dy,   dsum, s,    gamma, rstd, dx,   dgamma, dgamma ? (float*)workspace : nullptr,
                      rows, cols, lddy, ldds,  lds,  lddx, dtype == MX_BF16,
-                     gamma_dtype == MX_BF16, stream};
+                     gamma_dtype == MX_BF16, stream, 0.0f};
   return launch_status(mx_launch_rmsnorm_backward(a));
 }
 

@@ -87,6 +87,7 @@ struct NormArgs {
   uint8_t* scales;
   int64_t rows, cols, ldx, ldr, lds, ldy;
   uint64_t seed;
+  double inv_cols;  // set by the launcher
   float eps;
   uint32_t sign_mask;
   int fmt;
@@ -108,6 +109,7 @@ struct NormBackwardArgs {
   int64_t rows, cols, lddy, ldds, lds, lddx;
   bool bf16, gamma_bf16;
   void* stream;
+  float inv_cols;  // set by the launcher
 };
 int64_t mx_norm_backward_blocks(int64_t rows, int64_t cols);
 hipError_t mx_launch_rmsnorm_backward(const NormBackwardArgs& a);

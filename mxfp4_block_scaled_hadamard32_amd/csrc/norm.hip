@@ -4,18 +4,22 @@
 // Forward, per row:  s = x + r (fp32, rounded to the tensors' type: the residual stream that is
 // stored is the value that is normalised, so the backward pass and a recomputation from the
 // stored sum see the same numbers),  rho = 1 / sqrt(mean(s^2) + eps),  y = s rho g.
-// y is formed in 64 bits and rounded once to every output's type (see odd32), so the outputs do
-// not depend on the order of the sum, that is on the launch shape or on how many rows share the
-// call.
+// The sum of squares and rho are formed in 64 bits and y as an unevaluated sum of two fp32 values
+// (2^-45 of it), and every output is rounded from that once (round_odd). So the outputs do not
+// depend on the order of the sum, that is on the launch shape or on how many rows share the call,
+// and the codes are those of the definition in 64 bits.
 // Backward:  u = dy g, z = s rho, c = mean(u z):  dx = rho (u - z c) (+ dsum),  dg = sum_rows dy z.
 #include "mx_device.h"
 #include "mx_launch.h"
+
+#include <type_traits>
 
 using namespace mxd;
 
 namespace {
 
-constexpr int kMaxBlocks = 1 << 20;  // workgroups walk over the rows beyond this many
+// threads of a grid: what 256 compute units hold at 6 waves a SIMD
+constexpr int64_t kNormThreads = 256 * 6 * 4 * 64;
 
 // 8 values of a row chunk
 template <bool BF16>
@@ -45,35 +49,45 @@ __device__ __forceinline__ u32x4 pack_bf16x8(const float (&v)[8]) {
   return u32x4{w[0], w[1], w[2], w[3]};
 }
 
-template <bool BF16>
-__device__ __forceinline__ void store_chunk(void* p, int64_t off, const float (&v)[8]) {
-  if constexpr (BF16) {
-    *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p) + off) = pack_bf16x8(v);
-  } else {
-    f32x4* q = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + off);
-    q[0] = f32x4{v[0], v[1], v[2], v[3]};
-    q[1] = f32x4{v[4], v[5], v[6], v[7]};
-  }
-}
-
 __device__ __forceinline__ void load_gamma(const void* g, bool bf16, int64_t off, float (&v)[8]) {
   if (bf16) load_chunk<true>(g, off, v);
   else load_chunk<false>(g, off, v);
 }
 
-// fp32 by rounding to odd: toward zero, with the last bit set when bits were dropped. A rounding
-// of the result to at most 22 significant bits (bf16, E4M3, E5M2, E2M1, the thresholds of the
-// stochastic rounding, the block maximum's exponent) is then the rounding of the 64-bit value
-// itself: no tie is made or lost on the way. A value past fp32's range is infinite.
-__device__ __forceinline__ float odd32(double y) {
+// s rho g as hi + lo: products with their rounding errors, which the fused multiply-add gives
+// exactly. |lo| is at most a few half steps of hi; what is dropped is 2^-47 of the product (more
+// where errors fall below fp32's range: |y| under 2^-100, rho under 2^-100).
+__device__ __forceinline__ void product(float s, float rho, float rho_lo, float g, float& hi,
+                                        float& lo) {
+  const float p = s * rho;
+  const float pe = fmaf(s, rho_lo, fmaf(s, rho, -p));
+  hi = p * g;
+  lo = fmaf(pe, g, fmaf(p, g, -hi));
+}
+
+// hi + lo to nearest; a zero keeps the sign of hi (codes carry it), where -0 + 0 would be +0
+__device__ __forceinline__ float sum_of(float hi, float lo) {
+  return __builtin_copysignf(hi + lo, hi);
+}
+
+// hi + lo in fp32 by rounding to odd: of the two fp32 values around an inexact sum the one whose
+// last bit is set. A rounding of the result to at most 22 significant bits (bf16, E4M3, E5M2,
+// E2M1, the thresholds of the stochastic rounding, the block maximum's exponent) is then the
+// rounding of hi + lo itself: no tie is made or lost on the way. Infinities and NaNs stay such.
+__device__ __forceinline__ float round_odd(float hi, float lo) {
+  const float h = sum_of(hi, lo);
+  const float l = lo - (h - hi);  // exact: |lo| <= |hi|
+  const uint32_t hb = __float_as_uint(h), lb = __float_as_uint(l);
+  const uint32_t some = min(lb << 1, 1u);                     // l is not zero
+  const uint32_t below = ((hb ^ lb) >> 31) & some;            // |hi + lo| < |h|
+  const uint32_t b = (hb - below) | some;
+  return fabsf(h) < __builtin_inff() ? __uint_as_float(b) : h;
+}
+
+// the same from 64 bits
+__device__ __forceinline__ float round_odd(double y) {
   const float h = (float)y;
-  const double d = (double)h;
-  uint32_t b = __float_as_uint(h);
-  if ((b & 0x7FFFFFFFu) < 0x7F800000u) {
-    b -= fabs(d) > fabs(y) ? 1u : 0u;
-    b |= d != y ? 1u : 0u;
-  }
-  return __uint_as_float(b);
+  return fabsf(h) < __builtin_inff() ? round_odd(h, (float)(y - (double)h)) : h;
 }
 
 template <int CTRL>
@@ -106,13 +120,50 @@ __device__ __forceinline__ void hadamard_quad64(double (&w)[8], int q, uint32_t 
   for (int k = 0; k < 8; ++k) w[k] = butterfly_xlane64<kQuadXor2>(w[k], q & 2);
 }
 
-// Sum over the T threads of a row (T divides 64, or the row has the whole workgroup); every
-// thread gets it. red: kWaves values, alternating between two areas from one row to the next, so
-// one barrier a row is enough.
+// v of the lane across: 8 lanes (row_ror 8) and less inside a row of 16, then 16 and 32 lanes away.
+// Each returns v + its partner's v.
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + dpp_f32<CTRL>(v);
+}
+template <int CTRL>
+__device__ __forceinline__ double add_dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t p = (uint64_t)dpp_u32<CTRL>((uint32_t)b) |
+                     (uint64_t)dpp_u32<CTRL>((uint32_t)(b >> 32)) << 32;
+  return v + __builtin_bit_cast(double, p);
+}
+__device__ __forceinline__ float add_halves(float v) {
+  uint32_t b = __float_as_uint(v);
+  auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  b = __float_as_uint(v);
+  r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ double add_halves(double v) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t l = (uint32_t)b, h = (uint32_t)(b >> 32);
+    const auto rl = k ? __builtin_amdgcn_permlane32_swap(l, l, false, false)
+                      : __builtin_amdgcn_permlane16_swap(l, l, false, false);
+    const auto rh = k ? __builtin_amdgcn_permlane32_swap(h, h, false, false)
+                      : __builtin_amdgcn_permlane16_swap(h, h, false, false);
+    v = __builtin_bit_cast(double, (uint64_t)rh[0] << 32 | rl[0]) +
+        __builtin_bit_cast(double, (uint64_t)rh[1] << 32 | rl[1]);
+  }
+  return v;
+}
+
+// Sum over the T threads of a row (16 or 64 lanes, or the workgroup); every thread gets the same
+// value. red: one value a wave, in one of two areas in turn from one row to the next, so that one
+// barrier a row is enough.
 template <int T, class F>
 __device__ __forceinline__ F row_sum(F v, F* red) {
-#pragma unroll
-  for (int m = 1; m < (T < 64 ? T : 64); m <<= 1) v += __shfl_xor(v, m);
+  static_assert(T == 16 || T % 64 == 0);
+  v = add_dpp<kRowRor8>(add_dpp<kRowRor4>(add_dpp<kQuadXor2>(add_dpp<kQuadXor1>(v))));
+  if constexpr (T >= 64) v = add_halves(v);
   if constexpr (T > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -123,68 +174,166 @@ __device__ __forceinline__ F row_sum(F v, F* red) {
   return v;
 }
 
-// FMT: 0 no codes, 1 E2M1, 2 E4M3, 3 E5M2. T threads hold a row, V chunks of 8 values each.
-template <bool BF16, int T, int V, int FMT, bool SR>
+// 1 / sqrt(a) to about 2^-52: the hardware's approximation and one step of third order (its error
+// e = 1 - a r^2 enters with e^3). Zero and infinity as the division gives them.
+__device__ __forceinline__ double inv_sqrt(double a) {
+  const double r = __builtin_amdgcn_rsq(a);
+  const double e = fma(-a * r, r, 1.0);
+  const double f = fma(r * e, fma(e, 0.375, 0.5), r);
+  return a > 0.0 && a < __builtin_inf() ? f : r;
+}
+
+// a chunk of 8 values as it is in memory
+template <bool BF16>
+struct RawChunk {
+  u32x4 w[BF16 ? 1 : 2];
+};
+
+template <bool BF16>
+__device__ __forceinline__ RawChunk<BF16> load_raw(const void* p, int64_t off) {
+  RawChunk<BF16> o;
+  const u32x4* q = reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(p) +
+                                                  off * (BF16 ? 2 : 4));
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) o.w[i] = q[i];
+  return o;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_raw(void* p, int64_t off, const RawChunk<BF16>& v) {
+  u32x4* q = reinterpret_cast<u32x4*>(reinterpret_cast<uint8_t*>(p) + off * (BF16 ? 2 : 4));
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) q[i] = v.w[i];
+}
+
+template <bool BF16>
+__device__ __forceinline__ void values(const RawChunk<BF16>& c, float (&v)[8]) {
+  if constexpr (BF16) {
+    widen_bf16x8(c.w[0], v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(c.w[k >> 2][k & 3]);
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ RawChunk<BF16> raw_of(const float (&v)[8]) {
+  RawChunk<BF16> o;
+  if constexpr (BF16) {
+    o.w[0] = pack_bf16x8(v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o.w[i][k] = __float_as_uint(v[4 * i + k]);
+  }
+  return o;
+}
+
+// FMT: 0 no codes, 1 E2M1, 2 E4M3, 3 E5M2. T threads hold a row, V chunks of 8 values each. A
+// workgroup walks over rows with the weights in registers, the next row's values on the way while
+// one is normalised (for up to 2 chunks a thread). Loads past the row or the last row repeat valid places instead of branching:
+// a wait behind a branch would have to count on none of the loads and stores in it.
+template <bool BF16, int T, int V, int FMT, bool SR, bool RES>
 __global__ __launch_bounds__(T > 256 ? T : 256) void rmsnorm_kernel(const NormArgs a) {
   constexpr int kThreads = T > 256 ? T : 256;
   constexpr int kRows = kThreads / T;
+  constexpr bool kAhead = V < 4;  // 4 chunks leave no registers for the next row's
   __shared__ double red[2][T > 64 ? T / 64 : 1];
   const int t = threadIdx.x % T, sub = threadIdx.x / T;
   const int nch = (int)(a.cols / 8);
-  int par = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < a.rows;
-       row0 += (int64_t)gridDim.x * kRows, par ^= 1) {
-    const int64_t row = row0 + sub;
+  float g[V][8];
+  int col[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = t + v * T;
+    col[v] = 8 * (c < nch ? c : nch - 1);
+    load_gamma(a.gamma, a.gamma_bf16, col[v], g[v]);
+  }
+  const int64_t stride = (int64_t)gridDim.x * kRows;
+  int64_t row = (int64_t)blockIdx.x * kRows + sub;
+  RawChunk<BF16> x[V], r[RES ? V : 1];
+  auto load_row = [&](int64_t i) {
+    i = i < a.rows ? i : a.rows - 1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      x[v] = load_raw<BF16>(a.x, i * a.ldx + col[v]);
+      if constexpr (RES) r[v] = load_raw<BF16>(a.residual, i * a.ldr + col[v]);
+    }
+  };
+  if constexpr (kAhead) load_row(row);
+  for (int par = 0; row - sub < a.rows; row += stride, par ^= 1) {
     const bool live = row < a.rows;
-    float s[V][8];
+    if constexpr (!kAhead) load_row(row);
+    RawChunk<BF16> s[V];
     double ss = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = t + v * T;
-      if (live && c < nch) {
-        load_chunk<BF16>(a.x, row * a.ldx + 8 * c, s[v]);
-        if (a.residual) {
-          float r[8];
-          load_chunk<BF16>(a.residual, row * a.ldr + 8 * c, r);
+      float w[8];
+      values<BF16>(x[v], w);
+      s[v] = x[v];
+      if constexpr (RES) {
+        float q[8];
+        values<BF16>(r[v], q);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            s[v][k] += r[k];
-            if (BF16) s[v][k] = (float)(__bf16)s[v][k];  // the stored sum is what is normalised
-          }
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s[v][k] = 0.0f;
+        for (int k = 0; k < 8; ++k) w[k] += q[k];
+        s[v] = raw_of<BF16>(w);
+        values<BF16>(s[v], w);  // the stored sum is what is normalised
       }
+      if (t + v * T < nch) {
+        if (a.sum && live) store_raw<BF16>(a.sum, row * a.lds + col[v], s[v]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fma((double)s[v][k], (double)s[v][k], ss);
+        for (int k = 0; k < 8; ++k) ss = fma((double)w[k], (double)w[k], ss);
+      }
     }
+    if constexpr (kAhead) load_row(row + stride);
     ss = row_sum<T>(ss, red[par]);
-    const double rho = 1.0 / sqrt(ss / (double)a.cols + (double)a.eps);
+    const double rho = inv_sqrt(fma(ss, a.inv_cols, (double)a.eps));
+    const float rho_hi = (float)rho, rho_lo = (float)(rho - (double)rho_hi);
     if (!live) continue;
-    if (a.rstd && t == 0) a.rstd[row] = (float)rho;
+    if (a.rstd && t == 0) a.rstd[row] = rho_hi;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = t + v * T;
-      if (c >= nch) continue;  // whole quads: cols is a multiple of 32
-      if (a.sum) store_chunk<BF16>(a.sum, row * a.lds + 8 * c, s[v]);
-      float g[8];
-      load_gamma(a.gamma, a.gamma_bf16, 8 * c, g);
-      double y[8];
+      if (t + v * T >= nch) continue;  // whole quads: cols is a multiple of 32
+      float w[8], hi[8], lo[8];
+      values<BF16>(s[v], w);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = (double)s[v][k] * rho * (double)g[k];
+      for (int k = 0; k < 8; ++k) {
+        product(w[k], rho_hi, rho_lo, g[v][k], hi[k], lo[k]);
+        w[k] = sum_of(hi[k], lo[k]);
+      }
+      if constexpr (SR) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = round_odd(hi[k], lo[k]);
+      } else if constexpr (BF16 || FMT != 0) {
+        // The nearest fp32 value serves as well, unless it is a tie of the next rounding (or a
+        // power of two that the block maximum may only just miss, or an infinity): with 8
+        // significant bits at most, those have 15 zero bits at the end. One chunk in 4096.
+        uint32_t low = __float_as_uint(w[0]) << 17;
+#pragma unroll
+        for (int k = 1; k < 8; ++k) low = min(low, __float_as_uint(w[k]) << 17);
+        if (low == 0u) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) w[k] = round_odd(hi[k], lo[k]);
+        }
+      }
       if (a.y) {
         float o[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = BF16 ? odd32(y[k]) : (float)y[k];
-        store_chunk<BF16>(a.y, row * a.ldy + 8 * c, o);
+        for (int k = 0; k < 8; ++k) o[k] = BF16 ? w[k] : sum_of(hi[k], lo[k]);
+        store_raw<BF16>(a.y, row * a.ldy + col[v], raw_of<BF16>(o));
       }
       if constexpr (FMT != 0) {
-        if (a.hadamard) hadamard_quad64(y, t & 3, a.sign_mask);
-        float w[8];
+        if (a.hadamard) {
+          double y[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = odd32(y[k]);
-        const int64_t at = row * nch + c;  // chunk index in the codes and for the random fields
+          for (int k = 0; k < 8; ++k)
+            y[k] = __builtin_copysign((double)hi[k] + (double)lo[k], (double)hi[k]);
+          hadamard_quad64(y, t & 3, a.sign_mask);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) w[k] = round_odd(y[k]);
+        }
+        const int64_t at = row * nch + t + v * T;  // chunk of the codes and of the random fields
         uint32_t sb;
         if constexpr (FMT == 1) {
           const uint32_t code = a.ceil
@@ -204,26 +353,43 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void rmsnorm_kernel(const NormAr
 }
 
 template <bool BF16, int T, int V, int FMT, bool SR>
-hipError_t launch_norm(const NormArgs& a) {
+hipError_t launch_norm(NormArgs a) {
   constexpr int kThreads = T > 256 ? T : 256;
   constexpr int kRows = kThreads / T;
   const int64_t want = (a.rows + kRows - 1) / kRows;
-  const unsigned blocks = (unsigned)(want < kMaxBlocks ? want : kMaxBlocks);
-  hipLaunchKernelGGL((rmsnorm_kernel<BF16, T, V, FMT, SR>), dim3(blocks), dim3(kThreads), 0,
-                     (hipStream_t)a.stream, a);
+  const int64_t most = kNormThreads / kThreads;
+  const dim3 grid((unsigned)(want < most ? want : most)), block(kThreads);
+  a.inv_cols = 1.0 / (double)a.cols;
+  if (a.residual)
+    hipLaunchKernelGGL((rmsnorm_kernel<BF16, T, V, FMT, SR, true>), grid, block, 0,
+                       (hipStream_t)a.stream, a);
+  else
+    hipLaunchKernelGGL((rmsnorm_kernel<BF16, T, V, FMT, SR, false>), grid, block, 0,
+                       (hipStream_t)a.stream, a);
   return hipGetLastError();
+}
+
+// The shape of a row's threads by its columns: T threads, V chunks of 8 each.
+template <class F>
+auto with_shape(int64_t cols, F&& f) {
+  using std::integral_constant;
+  auto shape = [&](auto t, auto v) { return f(t, v); };
+#define MX_SHAPE(T, V) return shape(integral_constant<int, T>{}, integral_constant<int, V>{})
+  if (cols <= 128) MX_SHAPE(16, 1);
+  if (cols <= 512) MX_SHAPE(64, 1);
+  if (cols <= 1024) MX_SHAPE(64, 2);
+  if (cols <= 2048) MX_SHAPE(256, 1);
+  if (cols <= 4096) MX_SHAPE(256, 2);
+  if (cols <= 8192) MX_SHAPE(512, 2);
+  if (cols <= 16384) MX_SHAPE(1024, 2);
+  MX_SHAPE(1024, 4);
+#undef MX_SHAPE
 }
 
 template <bool BF16, int FMT, bool SR>
 hipError_t pick_norm_shape(const NormArgs& a) {
-  if (a.cols <= 128) return launch_norm<BF16, 16, 1, FMT, SR>(a);
-  if (a.cols <= 512) return launch_norm<BF16, 64, 1, FMT, SR>(a);
-  if (a.cols <= 1024) return launch_norm<BF16, 64, 2, FMT, SR>(a);
-  if (a.cols <= 2048) return launch_norm<BF16, 64, 4, FMT, SR>(a);
-  if (a.cols <= 4096) return launch_norm<BF16, 256, 2, FMT, SR>(a);
-  if (a.cols <= 8192) return launch_norm<BF16, 256, 4, FMT, SR>(a);
-  if (a.cols <= 16384) return launch_norm<BF16, 1024, 2, FMT, SR>(a);
-  return launch_norm<BF16, 1024, 4, FMT, SR>(a);
+  return with_shape(a.cols,
+                    [&](auto t, auto v) { return launch_norm<BF16, t(), v(), FMT, SR>(a); });
 }
 
 template <bool BF16>
@@ -239,72 +405,90 @@ hipError_t pick_norm_format(const NormArgs& a) {
 // ---------------------------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------------------------
-constexpr int kBwdBlocks = 1024;  // partial sums of the weight gradient
-
-// Every workgroup walks over rows blockIdx, blockIdx + gridDim, ... and keeps its columns' sums
-// of dy z in registers; partial[block][cols] are joined by rmsnorm_dgamma_kernel in a fixed order.
-template <bool BF16, int T, int V>
+// A workgroup walks over rows like the forward kernel and keeps its columns' sums of dy z in
+// registers; rmsnorm_dgamma_kernel joins the workgroups' sums, partial[block][cols], in a fixed
+// order.
+template <bool BF16, int T, int V, bool DSUM>
 __global__ __launch_bounds__(T > 256 ? T : 256) void rmsnorm_backward_kernel(
     const NormBackwardArgs a) {
   constexpr int kThreads = T > 256 ? T : 256;
   constexpr int kRows = kThreads / T;
+  constexpr bool kAhead = V < 4;  // 4 chunks leave no registers for the next row's
   __shared__ float red[2][T > 64 ? T / 64 : 1];
   __shared__ float join[kRows > 1 ? kRows : 1][kRows > 1 ? T * V * 8 : 1];
   const int t = threadIdx.x % T, sub = threadIdx.x / T;
   const int nch = (int)(a.cols / 8);
   float g[V][8], acc[V][8];
+  int col[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = t + v * T;
+    col[v] = 8 * (c < nch ? c : nch - 1);
+    load_gamma(a.gamma, a.gamma_bf16, col[v], g[v]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) g[v][k] = acc[v][k] = 0.0f;
-    if (c < nch) load_gamma(a.gamma, a.gamma_bf16, 8 * c, g[v]);
+    for (int k = 0; k < 8; ++k) acc[v][k] = 0.0f;
   }
-  const float inv_cols = 1.0f / (float)a.cols;
-  int par = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < a.rows;
-       row0 += (int64_t)gridDim.x * kRows, par ^= 1) {
-    const int64_t row = row0 + sub;
+  const int64_t stride = (int64_t)gridDim.x * kRows;
+  int64_t row = (int64_t)blockIdx.x * kRows + sub;
+  RawChunk<BF16> dy[V], s[V], d[DSUM ? V : 1];
+  float rho;
+  auto load_row = [&](int64_t i) {
+    i = i < a.rows ? i : a.rows - 1;
+    rho = a.rstd[i];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      dy[v] = load_raw<BF16>(a.dy, i * a.lddy + col[v]);
+      s[v] = load_raw<BF16>(a.s, i * a.lds + col[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if constexpr (DSUM) d[v] = load_raw<BF16>(a.dsum, i * a.ldds + col[v]);
+  };
+  if constexpr (kAhead) load_row(row);
+  for (int par = 0; row - sub < a.rows; row += stride, par ^= 1) {
     const bool live = row < a.rows;
-    const float rho = live ? a.rstd[row] : 0.0f;
-    float dy[V][8], z[V][8];
+    if constexpr (!kAhead) load_row(row);
+    RawChunk<BF16> y0[V], s0[V], d0[DSUM ? V : 1];
+    const float r = rho;
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = t + v * T;
-      if (live && c < nch) {
-        load_chunk<BF16>(a.dy, row * a.lddy + 8 * c, dy[v]);
-        load_chunk<BF16>(a.s, row * a.lds + 8 * c, z[v]);
-      } else {
+      y0[v] = dy[v];
+      s0[v] = s[v];
+      if constexpr (DSUM) d0[v] = d[v];
+      float y[8], z[8];
+      values<BF16>(y0[v], y);
+      values<BF16>(s0[v], z);
+      if (live && t + v * T < nch) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) dy[v][k] = z[v][k] = 0.0f;
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        z[v][k] *= rho;
-        acc[v][k] = fmaf(dy[v][k], z[v][k], acc[v][k]);
-        sum = fmaf(dy[v][k] * g[v][k], z[v][k], sum);
+        for (int k = 0; k < 8; ++k) {
+          const float p = y[k] * (z[k] * r);  // dy z
+          acc[v][k] += p;
+          sum = fmaf(p, g[v][k], sum);
+        }
       }
     }
-    const float mean = row_sum<T>(sum, red[par]) * inv_cols;
+    if constexpr (kAhead) load_row(row + stride);
+    const float mean = row_sum<T>(sum, red[par]) * a.inv_cols;
     if (!live) continue;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = t + v * T;
-      if (c >= nch) continue;
-      float o[8];
+      if (t + v * T >= nch) continue;
+      float y[8], z[8], o[8];
+      values<BF16>(y0[v], y);
+      values<BF16>(s0[v], z);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = rho * (dy[v][k] * g[v][k] - z[v][k] * mean);
-      if (a.dsum) {
-        float d[8];
-        load_chunk<BF16>(a.dsum, row * a.ldds + 8 * c, d);
+      for (int k = 0; k < 8; ++k) o[k] = r * (y[k] * g[v][k] - z[k] * r * mean);
+      if constexpr (DSUM) {
+        values<BF16>(d0[v], y);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] += d[k];
+        for (int k = 0; k < 8; ++k) o[k] += y[k];
       }
-      store_chunk<BF16>(a.dx, row * a.lddx + 8 * c, o);
+      store_raw<BF16>(a.dx, row * a.lddx + col[v], raw_of<BF16>(o));
     }
   }
   if (!a.partial) return;
+  float* const out = a.partial + (int64_t)blockIdx.x * a.cols;
   if constexpr (kRows > 1) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -314,69 +498,85 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void rmsnorm_backward_kernel(
     for (int c = threadIdx.x; c < (int)a.cols; c += kThreads) {
       float p = join[0][c];
 #pragma unroll
-      for (int r = 1; r < kRows; ++r) p += join[r][c];
-      a.partial[(int64_t)blockIdx.x * a.cols + c] = p;
+      for (int i = 1; i < kRows; ++i) p += join[i][c];
+      out[c] = p;
     }
   } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = t + v * T;
-      if (c < nch) store_chunk<false>(a.partial, (int64_t)blockIdx.x * a.cols + 8 * c, acc[v]);
-    }
+    for (int v = 0; v < V; ++v)
+      if (t + v * T < nch) store_raw<false>(out, col[v], raw_of<false>(acc[v]));
   }
 }
 
-// dgamma[c] = sum over the blocks' partial sums: 32 columns by 8 slices of the blocks a workgroup
+// dgamma[c] = sum of the workgroups' sums, in 64 bits: 16 columns by 64 slices of the workgroups,
+// 4 columns a thread
 __global__ __launch_bounds__(256) void rmsnorm_dgamma_kernel(const float* __restrict__ partial,
                                                              int blocks, int64_t cols,
                                                              float* __restrict__ dgamma) {
-  __shared__ double part[8][32];
-  const int c = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int64_t col = (int64_t)blockIdx.x * 32 + c;  // cols is a multiple of 32
-  double sum = 0.0;
-  for (int b = slice; b < blocks; b += 8) sum += (double)partial[b * cols + col];
-  part[slice][c] = sum;
-  __syncthreads();
-  if (slice == 0) {
+  __shared__ double part[64][17];
+  const int c = threadIdx.x & 3, slice = threadIdx.x >> 2;
+  const float* p = partial + (int64_t)blockIdx.x * 16 + 4 * c;  // cols is a multiple of 32
+  double sum[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 8
+  for (int b = slice; b < blocks; b += 64) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(p + b * cols);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) sum += part[i][c];
-    dgamma[col] = (float)sum;
+    for (int k = 0; k < 4; ++k) sum[k] += (double)v[k];
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) part[slice][4 * c + k] = sum[k];
+  __syncthreads();
+  const int col = threadIdx.x & 15, q = threadIdx.x >> 4;  // 4 slices a thread, then 16 threads
+  double s = part[4 * q][col];
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s += part[4 * q + i][col];
+  __syncthreads();
+  part[q][col] = s;
+  __syncthreads();
+  if (threadIdx.x < 16) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s += part[i][col];
+    dgamma[(int64_t)blockIdx.x * 16 + col] = (float)s;
+  }
+}
+
+// workgroups of the backward kernel: what 256 compute units hold at 6 waves a SIMD with one chunk
+// a thread, 4 with more; fewer for few rows, whose sums would be as much traffic as the rows
+template <int T, int V>
+int64_t backward_blocks(int64_t rows) {
+  constexpr int kThreads = T > 256 ? T : 256;
+  constexpr int kRows = kThreads / T;
+  constexpr int64_t most = 256 * 4 * 64 * (V == 1 ? 6 : 4) / kThreads;
+  const int64_t want = (rows + kRows - 1) / kRows;
+  if (want <= 256) return want;
+  const int64_t few = want / 4 > 256 ? want / 4 : 256;
+  return few < most ? few : most;
 }
 
 template <bool BF16, int T, int V>
-hipError_t launch_backward(const NormBackwardArgs& a) {
+hipError_t launch_backward(NormBackwardArgs a) {
   constexpr int kThreads = T > 256 ? T : 256;
-  const int blocks = (int)mx_norm_backward_blocks(a.rows, a.cols);
+  const int blocks = (int)backward_blocks<T, V>(a.rows);
+  a.inv_cols = 1.0f / (float)a.cols;
   if (blocks > 0) {
-    hipLaunchKernelGGL((rmsnorm_backward_kernel<BF16, T, V>), dim3((unsigned)blocks),
-                       dim3(kThreads), 0, (hipStream_t)a.stream, a);
+    if (a.dsum)
+      hipLaunchKernelGGL((rmsnorm_backward_kernel<BF16, T, V, true>), dim3((unsigned)blocks),
+                         dim3(kThreads), 0, (hipStream_t)a.stream, a);
+    else
+      hipLaunchKernelGGL((rmsnorm_backward_kernel<BF16, T, V, false>), dim3((unsigned)blocks),
+                         dim3(kThreads), 0, (hipStream_t)a.stream, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   if (!a.dgamma) return hipSuccess;
-  hipLaunchKernelGGL(rmsnorm_dgamma_kernel, dim3((unsigned)(a.cols / 32)), dim3(256), 0,
+  hipLaunchKernelGGL(rmsnorm_dgamma_kernel, dim3((unsigned)(a.cols / 16)), dim3(256), 0,
                      (hipStream_t)a.stream, a.partial, blocks, a.cols, a.dgamma);
   return hipGetLastError();
-}
-
-template <bool BF16>
-hipError_t pick_backward_shape(const NormBackwardArgs& a) {
-  if (a.cols <= 128) return launch_backward<BF16, 16, 1>(a);
-  if (a.cols <= 512) return launch_backward<BF16, 64, 1>(a);
-  if (a.cols <= 1024) return launch_backward<BF16, 64, 2>(a);
-  if (a.cols <= 2048) return launch_backward<BF16, 64, 4>(a);
-  if (a.cols <= 4096) return launch_backward<BF16, 256, 2>(a);
-  if (a.cols <= 8192) return launch_backward<BF16, 256, 4>(a);
-  if (a.cols <= 16384) return launch_backward<BF16, 1024, 2>(a);
-  return launch_backward<BF16, 1024, 4>(a);
 }
 
 }  // namespace
 
 int64_t mx_norm_backward_blocks(int64_t rows, int64_t cols) {
-  const int64_t per = cols <= 128 ? 16 : cols <= 2048 ? 4 : 1;  // rows a workgroup holds at once
-  const int64_t want = (rows + per - 1) / per;
-  return want < kBwdBlocks ? want : kBwdBlocks;
+  return with_shape(cols, [&](auto t, auto v) { return backward_blocks<t(), v()>(rows); });
 }
 
 hipError_t mx_launch_rmsnorm(const NormArgs& a) {
@@ -384,5 +584,7 @@ hipError_t mx_launch_rmsnorm(const NormArgs& a) {
 }
 
 hipError_t mx_launch_rmsnorm_backward(const NormBackwardArgs& a) {
-  return a.bf16 ? pick_backward_shape<true>(a) : pick_backward_shape<false>(a);
+  return with_shape(a.cols, [&](auto t, auto v) {
+    return a.bf16 ? launch_backward<true, t(), v()>(a) : launch_backward<false, t(), v()>(a);
+  });
 }

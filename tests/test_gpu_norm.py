@@ -166,6 +166,40 @@ def test_special_rows(mx, orc, dtype):
     assert (host(sc)[0] == 0).all() and (host(sc)[4] == 0xFF).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_values_beside_the_borders_of_the_next_rounding(mx, orc, dtype):
+    """x = +-1 and eps = 0 make rho exactly 1, so y = +-gamma: weights on a tie of E2M1, E4M3,
+    E5M2 and bf16, one fp32 step beside it, and block maxima on and beside a power of two; then
+    the same weights with a rho that is no power of two, where y is a step's fraction beside."""
+    half = torch.tensor([1.25, 1.75, 2.5, 3.5, 5.0, 0.75, 1.0625, 1.1875, 1.125, 1.375, 1.0 + 2**-8,
+                         1.0 + 3 * 2**-8, 0.0625, 6.0, 448.0, 464.0])
+    bits = half.view(torch.int32)
+    g = torch.cat([(bits + d).view(torch.float32) for d in (-1, 0, 1, 2)])  # 64 weights
+    top = torch.full((64,), 1.0).view(torch.int32).repeat(3, 1)
+    top = (top + torch.tensor([[-1], [0], [1]], dtype=torch.int32)).view(torch.float32)
+    g = torch.cat([g, torch.cat([t * torch.linspace(0.1, 1.0, 64) for t in top])])
+    cols = g.numel()
+    x = torch.ones((4, cols))
+    x[1, ::3] = -1.0
+    x[2] *= 3.0
+    x[3] *= 0.7
+    x = x.to(DT[dtype])
+    for fmt in ("fp4", "e4m3", "e5m2"):
+        for rule in (0, 1):
+            for rnd in (0, 1):
+                c, sc, y, s, rstd = quant(mx, fmt, dev(x), dev(g), eps=0.0, with_y=True,
+                                          scale_rule=rule, round=rnd, seed=5)
+                torch.cuda.synchronize()
+                assert float(rstd[0]) == 1.0
+                exact, rho = ref.norm_f64(x, g, 0.0)
+                exact[:2] = x[:2].double().numpy() * g.double().numpy()
+                check_rounded(y, exact)
+                rc, rs = oracle_codes(orc, fmt, exact[:2], 0, 0, scale_rule=rule, round_mode=rnd,
+                                      seed=5)
+                assert_bytes_equal(sc[:2], rs, "scales")
+                assert_bytes_equal(c[:2], rc, "codes")
+
+
 def test_empty(mx):
     g = torch.ones(64, device=DEV)
     y, s, rstd = mx.mx_rmsnorm(torch.empty((0, 64), dtype=torch.bfloat16, device=DEV), g)
@@ -224,9 +258,10 @@ def check_backward(dx, dgamma, dy, s, g, rstd, d):
         lo, hi = bf16_round_f64(lo), bf16_round_f64(hi)
     bad = ~((got >= lo) & (got <= hi))
     assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist())
-    # a workgroup adds at most rows / 1024 + 1 rows one after the other, 16 of them at once; the
-    # blocks' sums are joined in 64 bits. z and the product: one rounding each
-    n = s.shape[0] // 1024 + 1 + 16 + 3
+    # more than 256 rows are shared by at least 256 workgroups, so one adds at most rows / 256 + 1
+    # of them one after the other and joins 16 at the end; the workgroups' sums are joined in 64
+    # bits. z, the product and the last rounding: one each
+    n = s.shape[0] // 256 + 1 + 16 + 3
     err = np.abs(dgamma.cpu().numpy().astype(np.float64) - dg)
     assert (err <= n * ref.EPS32 * dgabs).all(), float((err / (dgabs + 1e-300)).max())
 
