@@ -18,6 +18,10 @@ Two variants from the same page:
     quantized once in square tiles, so the transposed product reads the same codes and scales
     (the tile's transposed copy) instead of a re-blocked quantization; X stays 1x32.
   * fmt = "mxfp8": the query / key projections in MXFP8, X and W in E4M3 and dY in E5M2.
+
+Around the layer: MXRMSNorm (the norm before it, with the residual's addition), MXNormLinear (both
+in one, the norm's kernel writing the Fprop operand's codes) and MXDecodeLinear (the layer's
+product for a few tokens against weights quantized once).
 """
 from __future__ import annotations
 
@@ -26,8 +30,9 @@ from dataclasses import dataclass, field
 import torch
 
 from . import (MX_E4M3, MX_E5M2, MX_ROUND_RNE, MX_SCALE_FLOOR, mx_gemm_dgrad, mx_gemm_fprop,
-               mx_gemm_mxfp8, mx_gemm_wgrad, mx_quantize, mx_quantize_2d_blocks,
-               mx_quantize_mxfp8)
+               mx_gemm_mxfp8, mx_gemm_wgrad, mx_gemv, mx_quantize, mx_quantize_2d_blocks,
+               mx_quantize_mxfp8, mx_rmsnorm, mx_rmsnorm_backward, mx_rmsnorm_quant,
+               mx_rmsnorm_quant_mxfp8)
 
 
 @dataclass
@@ -108,8 +113,11 @@ def _alpha(spec: QuantSpec) -> int:
 
 
 class MXLinearFunction(torch.autograd.Function):
+    """x @ w^T; x_quant: x's Fprop operand (codes, scales), when another kernel has made it with
+    the options of cfg.fprop_q and the seed cfg.seed."""
+
     @staticmethod
-    def forward(ctx, x: torch.Tensor, w: torch.Tensor, cfg: MXLinearConfig):
+    def forward(ctx, x: torch.Tensor, w: torch.Tensor, cfg: MXLinearConfig, x_quant=None):
         cfg.check()
         sx, sw, sdy = cfg.next_seeds()
         ctx.cfg, ctx.seeds = cfg, (sx, sw, sdy)
@@ -121,11 +129,11 @@ class MXLinearFunction(torch.autograd.Function):
             return x @ w.t()
         spec = cfg.fprop_q
         if cfg.fmt == "mxfp8":
-            xq, xs = _q(x, 1, spec, sx, MX_E4M3)
+            xq, xs = x_quant or _q(x, 1, spec, sx, MX_E4M3)
             wq, ws = _q(w, 1, spec, sw, MX_E4M3)
             return mx_gemm_mxfp8(xq, xs, MX_E4M3, wq, ws, MX_E4M3, alpha_exp=_alpha(spec),
                                  out_dtype=x.dtype)
-        xq, xs = _q(x, 1, spec, sx)
+        xq, xs = x_quant or _q(x, 1, spec, sx)
         if cfg.w_block > 1:
             ctx.w_tiles = _tiles(w, cfg.w_block, cfg.w_tile_spec(), sw)
             wq, ws, gw = ctx.w_tiles[0], ctx.w_tiles[1], cfg.w_block
@@ -184,7 +192,7 @@ class MXLinearFunction(torch.autograd.Function):
             else:
                 dw = dy.t() @ x
         ctx.w_tiles = None
-        return dx, dw, None
+        return dx, dw, None, None
 
 
 class MXLinear(torch.nn.Module):
@@ -202,3 +210,127 @@ class MXLinear(torch.nn.Module):
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         return MXLinearFunction.apply(x, self.weight, self.cfg)
+
+
+class MXRMSNormFunction(torch.autograd.Function):
+    """(y, s, codes, scales) of the RMS norm of s = x + residual; s is None without a residual and
+    the codes are None unless quant is given (fmt "mxfp4" or "mxfp8", QuantSpec, seed). The
+    quantizer is the identity in the backward pass."""
+
+    @staticmethod
+    def forward(ctx, x, residual, gamma, eps, quant=None):
+        ctx.set_materialize_grads(False)
+        codes = scales = None
+        if quant is None:
+            y, s, rstd = mx_rmsnorm(x, gamma, residual, eps=eps)
+        else:
+            fmt, spec, seed = quant
+            kw = dict(eps=eps, scale_rule=spec.scale_rule, round=spec.round,
+                      hadamard=spec.hadamard, sign_mask=spec.sign_mask, seed=seed, with_y=True)
+            if fmt == "mxfp8":
+                codes, scales, y, s, rstd = mx_rmsnorm_quant_mxfp8(x, gamma, residual,
+                                                                   fmt=MX_E4M3, **kw)
+            else:
+                codes, scales, y, s, rstd = mx_rmsnorm_quant(x, gamma, residual, **kw)
+            ctx.mark_non_differentiable(codes, scales)
+        ctx.save_for_backward(s, gamma, rstd)
+        return y, (None if residual is None else s), codes, scales
+
+    @staticmethod
+    def backward(ctx, dy, ds, _codes, _scales):
+        s, gamma, rstd = ctx.saved_tensors
+        need_x, need_r, need_g = ctx.needs_input_grad[:3]
+        if ds is not None:
+            ds = _rows_of(ds, s)
+        if dy is None:  # only the sum was used
+            return (ds if need_x else None), (ds if need_r else None), None, None, None
+        dx, dg = mx_rmsnorm_backward(_rows_of(dy, s), s, gamma, rstd, dsum=ds, with_dgamma=need_g)
+        return (dx if need_x else None), (dx if need_r else None), \
+            (dg.to(gamma.dtype) if need_g else None), None, None
+
+
+def _rows_of(grad: torch.Tensor, like: torch.Tensor) -> torch.Tensor:
+    """A gradient in the layout and type that the kernels read (an expanded one has no rows)."""
+    return grad.to(like.dtype).contiguous()
+
+
+def _flat(t: torch.Tensor | None):
+    """[..., n] as [rows][n] with contiguous rows."""
+    if t is None:
+        return None
+    t = t.reshape(-1, t.shape[-1])
+    return t if t.stride(1) == 1 or t.shape[1] <= 1 else t.contiguous()
+
+
+class MXRMSNorm(torch.nn.Module):
+    """RMS norm over the last dimension (a multiple of 32): norm(x) -> y, or norm(x, residual) ->
+    (y, s) with s = x + residual, the new residual stream. x bf16 or fp32; the weight fp32."""
+
+    def __init__(self, features: int, eps: float = 1e-5, device="cuda", dtype=torch.float32):
+        super().__init__()
+        self.eps = eps
+        self.weight = torch.nn.Parameter(torch.ones(features, device=device, dtype=dtype))
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
+        y, s, _, _ = MXRMSNormFunction.apply(_flat(x), _flat(residual), self.weight, self.eps)
+        y = y.view(x.shape)
+        return y if residual is None else (y, s.view(x.shape))
+
+
+class MXNormLinear(torch.nn.Module):
+    """MXLinear of the RMS norm of x (+ residual): the norm's kernel writes the Fprop operand's
+    codes and scales beside y, which the weight gradient quantizes along tokens. The codes come
+    from y before its rounding to x's type. layer(x) -> out, or layer(x, residual) -> (out, s).
+    x: [T][K] as for MXLinear. With Fprop off the norm feeds the bf16 product."""
+
+    def __init__(self, in_features: int, out_features: int, cfg: MXLinearConfig | None = None,
+                 eps: float = 1e-5, device="cuda", dtype=torch.bfloat16):
+        super().__init__()
+        self.norm = MXRMSNorm(in_features, eps, device=device)
+        self.linear = MXLinear(in_features, out_features, cfg, device=device, dtype=dtype)
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
+        cfg = self.linear.cfg
+        quant = (cfg.fmt, cfg.fprop_q, cfg.seed) if cfg.fprop else None
+        y, s, codes, scales = MXRMSNormFunction.apply(x, residual, self.norm.weight, self.norm.eps,
+                                                      quant)
+        out = MXLinearFunction.apply(y, self.linear.weight, cfg,
+                                     None if codes is None else (codes, scales))
+        return out if residual is None else (out, s)
+
+
+class MXDecodeLinear(torch.nn.Module):
+    """y = x W^T for a few tokens against MXFP4 weights quantized once, the activations not
+    quantized: layer(x) with x [..., K] bf16 or fp32 -> [..., N] of x's type. The options are the
+    Fprop ones of an MXLinear (scale rule, rotation, w_block); the weights are rounded to nearest
+    whatever its rounding."""
+
+    def __init__(self, weight: torch.Tensor, spec: QuantSpec | None = None, w_block: int = 1):
+        super().__init__()
+        spec = spec or QuantSpec()
+        if w_block not in (1, 32, 64):
+            raise ValueError("w_block must be 1, 32 or 64")
+        if w_block > 1 and spec.hadamard:
+            raise ValueError("tiles are quantized without the Hadamard rotation")
+        w = weight.detach()
+        if w_block > 1:
+            q, s = mx_quantize_2d_blocks(w, block=w_block, scale_rule=spec.scale_rule,
+                                         transposed=False)[:2]
+        else:
+            q, s = mx_quantize(w, axis=1, scale_rule=spec.scale_rule, hadamard=spec.hadamard,
+                               sign_mask=spec.sign_mask)
+        self.spec, self.w_block = spec, w_block
+        self.register_buffer("codes", q)
+        self.register_buffer("scales", s)
+
+    @classmethod
+    def from_linear(cls, layer: MXLinear) -> "MXDecodeLinear":
+        if layer.cfg.fmt != "mxfp4":
+            raise ValueError("only MXFP4 weights have a few-token product")
+        return cls(layer.weight, layer.cfg.fprop_q, layer.cfg.w_block)
+
+    @torch.no_grad()
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        y = mx_gemv(_flat(x), self.codes, self.scales, self.w_block, hadamard=self.spec.hadamard,
+                    sign_mask=self.spec.sign_mask, alpha_exp=_alpha(self.spec), out_dtype=x.dtype)
+        return y.view(*x.shape[:-1], y.shape[1])
