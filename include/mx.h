@@ -321,20 +321,25 @@ mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, in
  * weights that were quantized rotated; alpha_exp = -5 then undoes the factor 32. T and N are
  * arbitrary (N a multiple of gw), K a multiple of 32. x and its rows (ldx * element size) 16-byte
  * aligned, wq 16-byte aligned, y aligned to its elements, ldy >= N. The weights are read once for
- * every 64 tokens; many more tokens are the GEMMs' work.
+ * every 16 to 64 tokens; many more tokens are the GEMMs' work.
+ * workspace: mx_gemv_workspace(...) bytes, 16-byte aligned, make large products of several tokens
+ * faster (sums over parts of K); 0 bytes are wanted for one token. Its contents are scratch, and
+ * calls that may run at the same time need one each. NULL does without, with other roundings.
  * Accuracy: fp32 accumulation. The products are exact, sums of 128 of them are formed by the
  * matrix core, which drops what lies below 2^-24 of a sum's largest term, and joined in fp32:
- * |y - exact| <= 2^-16 * sum_k |x'_k W_k| before the rounding to bf16 (K <= 65536). bf16 tokens
- * that are rotated for a bf16 y keep 16 bits of each x' (another 2^-17 of the sum). A weight
+ * |y - exact| <= (160 + K / 128) * 2^-24 * sum_k |x'_k W_k| before the rounding to bf16. bf16
+ * tokens that are rotated for a bf16 y keep 16 bits of each x' (another 2^-17 of the sum). A weight
  * beyond bf16's range, 2^128 or more (scale bytes 253 and 254), counts as infinity; scale byte
  * 255 is NaN.
  * Errors (nothing is launched): MX_ERR_SHAPE, MX_ERR_ARG (types, granularity, hadamard, alpha_exp
- * outside [-126, 127], alignment), MX_ERR_NULL, MX_ERR_LAUNCH (N above 2^26 or T above 2^19 rows).
- * T == 0 or N == 0 is a no-op; K == 0 writes zeros. */
+ * outside [-126, 127], alignment, a workspace that is too small), MX_ERR_NULL, MX_ERR_LAUNCH (N
+ * above 2^26 or T above 2^19 rows). T == 0 or N == 0 is a no-op; K == 0 writes zeros. */
+int64_t mx_gemv_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, int32_t hadamard,
+                          int32_t out_dtype);
 mx_status mx_gemv(const void* x, int32_t dtype, int64_t ldx, const uint8_t* wq, const uint8_t* ws,
                   int32_t gw, int64_t T, int64_t N, int64_t K, int32_t hadamard,
                   uint32_t sign_mask, int32_t alpha_exp, int32_t out_dtype, void* y, int64_t ldy,
-                  void* stream);
+                  void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* mx_status_string(int32_t status);

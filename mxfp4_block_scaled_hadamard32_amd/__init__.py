@@ -343,6 +343,15 @@ def _rows_like(t, name: str, x):
     return ld
 
 
+def _scratch(size: int, device, stream):
+    """size bytes from the pool of the stream that uses them: what is allocated there next comes
+    after that use."""
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+
+
 def _data(t):
     return None if t is None else t.data_ptr()
 
@@ -459,11 +468,7 @@ def mx_rmsnorm_backward(dy, s, gamma, rstd, dsum=None, with_dgamma: bool = True,
             _buf(workspace, "workspace", (size,), _U8, dev)
         else:
             size = lib().mx_rmsnorm_backward_workspace(rows, cols)
-            if stream is None:
-                workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-            else:  # from the pool of the stream that uses it: what is allocated there next waits
-                with torch.cuda.stream(stream):
-                    workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            workspace = _scratch(size, dev, stream)
     else:
         dgamma = workspace = None
     _launch("mx_rmsnorm_backward", dev, stream, dy.data_ptr(), lddy, _data(dsum), ldds,
@@ -473,10 +478,11 @@ def mx_rmsnorm_backward(dy, s, gamma, rstd, dsum=None, with_dgamma: bool = True,
 
 
 def mx_gemv(x, wq, ws, gw: int = 1, hadamard: int = 0, sign_mask: int = 0, alpha_exp: int = 0,
-            out_dtype=torch.bfloat16, out=None, stream=None):
+            out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """y[T][N] = 2^alpha x W^T for a few tokens x [T][K] (bf16 or fp32, not quantized) and MXFP4
     weights wq [N][K/2], ws [N/gw][K/32]; hadamard = 1 rotates x as mx_quantize does (for weights
-    quantized rotated, with alpha_exp = -5)."""
+    quantized rotated, with alpha_exp = -5). workspace: a uint8 buffer of at least
+    lib().mx_gemv_workspace(...) bytes, allocated per call when None and wanted."""
     T, K, ldx = _rows(x, "x")
     N, Kw = _operand(wq, ws, gw, "W")
     dev = x.device
@@ -487,7 +493,15 @@ def mx_gemv(x, wq, ws, gw: int = 1, hadamard: int = 0, sign_mask: int = 0, alpha
     else:
         out, code = _out(out, T, N, out_dtype, dev)
         ldy = out.stride(0) if T > 1 else N
-    _launch("mx_gemv", dev, stream, x.data_ptr(), _CODE[x.dtype], ldx, wq.data_ptr(),
-            ws.data_ptr(), gw, T, N, K, hadamard, sign_mask & 0xFFFFFFFF, alpha_exp, code,
-            out.data_ptr(), ldy)
+    dtype, size = _CODE[x.dtype], 0
+    if workspace is not None:
+        size = workspace.numel()
+        _buf(workspace, "workspace", (size,), _U8, dev)
+    elif T > 1:  # one token wants none
+        size = lib().mx_gemv_workspace(dtype, T, N, K, hadamard, code)
+        if size:
+            workspace = _scratch(size, dev, stream)
+    _launch("mx_gemv", dev, stream, x.data_ptr(), dtype, ldx, wq.data_ptr(), ws.data_ptr(), gw, T,
+            N, K, hadamard, sign_mask & 0xFFFFFFFF, alpha_exp, code, out.data_ptr(), ldy,
+            _data(workspace), size)
     return out

@@ -69,7 +69,9 @@ def lib() -> ctypes.CDLL:
     L.mx_rmsnorm_backward_workspace.argtypes = [i64, i64]
     L.mx_rmsnorm_backward_workspace.restype = i64
     L.mx_gemv.argtypes = [vp, i32, i64, vp, vp, i32, i64, i64, i64, i32, u32, i32, i32, vp, i64,
-                          vp]
+                          vp, i64, vp]
+    L.mx_gemv_workspace.argtypes = [i32, i64, i64, i64, i32, i32]
+    L.mx_gemv_workspace.restype = i64
     for name in ("mx_quantize", "mx_quantize_2d", "mx_dequantize", "mx_gemm_fprop",
                  "mx_gemm_dgrad", "mx_gemm_wgrad", "mx_gemm_fprop_quant", "mx_quantize_mxfp8",
                  "mx_gemm_mxfp8", "mx_quantize_2d_blocks", "mx_scale_mismatch_map", "mx_rmsnorm",

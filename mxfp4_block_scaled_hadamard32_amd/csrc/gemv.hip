@@ -118,6 +118,61 @@ __device__ __forceinline__ void terms_of(const RawX<BF16>& x, uint32_t sign_mask
   }
 }
 
+// The same with half a block a lane: values 16h .. 16h+15 in the lanes of parity h, which exchange
+// them for the transform's last stage.
+template <bool BF16>
+struct RawHalf {
+  u32x4 w[BF16 ? 2 : 4];
+};
+
+template <bool BF16, bool HAD, int NT>
+__device__ __forceinline__ void half_terms_of(const RawHalf<BF16>& x, uint32_t sign_mask,
+                                              u32x4 (&f)[NT][2]) {
+  const int h = threadIdx.x & 1;
+  float v[16];
+  if constexpr (BF16) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float w[8];
+      widen_bf16x8(x.w[j], w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[8 * j + k] = w[k];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[4 * j + k] = __uint_as_float(x.w[j][k]);
+  }
+  if constexpr (HAD) {
+    const uint32_t mask = sign_mask >> (16 * h);
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      v[k] = __uint_as_float(__float_as_uint(v[k]) ^ (((mask >> k) & 1u) << 31));
+#pragma unroll
+    for (int s = 1; s < 16; s <<= 1) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (i & s) continue;
+        const float a = v[i], c = v[i + s];
+        v[i] = a + c;
+        v[i + s] = a - c;
+      }
+    }
+    const uint32_t upper = h ? 0x80000000u : 0u;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = butterfly_xlane<kQuadXor1>(v[k], upper);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t o[4][NT];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_pair<NT>(v[8 * j + 2 * i], v[8 * j + 2 * i + 1], o[i]);
+#pragma unroll
+    for (int s = 0; s < NT; ++s) f[s][j] = u32x4{o[0][s], o[1][s], o[2][s], o[3][s]};
+  }
+}
+
 __device__ __forceinline__ void store_y(const GemvArgs& a, int64_t at, float v) {
   v *= __uint_as_float((uint32_t)(a.alpha + 127) << 23);
   if (a.out_bf16) reinterpret_cast<__bf16*>(a.y)[at] = (__bf16)v;
@@ -446,6 +501,215 @@ __global__ __launch_bounds__(64 * WV) void gemv_direct_kernel(const GemvArgs a) 
   }
 }
 
+// Batches of tokens: 8 waves of RT tiles of 16 weight rows each share MT tiles of 16 tokens, which
+// pass through LDS a chunk of 16 blocks of K at a time (rotated and split on the way, once a
+// workgroup) while the chunk before is multiplied. A value of x is fetched once for 128 RT weight
+// rows: the caches give a compute unit about 55 bytes a ns, and the codes alone want 23 of them.
+// A wave's codes are requested 4 steps ahead and stay on the way across the barriers, which wait
+// for LDS alone. K is cut into `splits` parts (blockIdx.z) so that few rows fill the machine too;
+// their sums go to part[split][T][N] and gemv_join_kernel adds them in order.
+template <bool BF16, bool HAD, int NT, int MT, int RT>
+__global__ __launch_bounds__(512) void gemv_shared_kernel(const GemvArgs a, float* part,
+                                                          int splits) {
+  constexpr bool CONV = !BF16 || HAD;
+  constexpr int kBlock = BF16 ? 64 : 128;                      // bytes of a block of x
+  constexpr int kPer = CONV ? MT : 2 * MT;  // half blocks, or 16-byte pieces, of a thread
+  constexpr int kBuf = NT * MT * 16 * 4 * 16;                  // 16-byte pieces of a chunk
+  __shared__ u32x4 xl[2][kBuf];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i16 = lane & 15, g = lane >> 4;
+  const int64_t n0 = ((int64_t)blockIdx.x * 8 + wave) * (16 * RT);
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+  const int nb = (int)(a.K / 32);
+  const int c0 = (int)((int64_t)(nb / 16) * blockIdx.z / splits);
+  const int c1 = (int)((int64_t)(nb / 16) * (blockIdx.z + 1) / splits);
+
+  // rows and tokens past the end repeat the last one: their products are not stored
+  const uint8_t* wrow[RT];
+  const uint8_t* srow[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    int64_t n = n0 + 16 * r + i16;
+    n = n < a.N ? n : a.N - 1;
+    wrow[r] = a.w + n * (a.K / 2) + 16 * g;
+    srow[r] = a.ws + n / a.gw * nb;
+  }
+  auto token = [&](int t) {
+    int64_t i = m0 + t;
+    i = i < a.T ? i : a.T - 1;
+    return reinterpret_cast<const uint8_t*>(a.x) + i * a.ldx * (BF16 ? 2 : 4);
+  };
+  const uint8_t* xp[kPer];
+  RawHalf<BF16> xr[CONV ? kPer : 1];
+  u32x4 xc[CONV ? 1 : kPer];
+#pragma unroll
+  for (int p = 0; p < kPer; ++p) {
+    const int i = threadIdx.x + 512 * p;
+    if constexpr (CONV) xp[p] = token(i / 32) + i % 32 * (kBlock / 2);
+    else xp[p] = token(i / 64) + i % 64 * 16;
+  }
+  auto fetch = [&](int c) {
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
+      const uint8_t* q = xp[p] + (int64_t)c * 16 * kBlock;
+      if constexpr (CONV) {
+#pragma unroll
+        for (int j = 0; j < (BF16 ? 2 : 4); ++j) xr[p].w[j] = reinterpret_cast<const u32x4*>(q)[j];
+      } else {
+        xc[p] = *reinterpret_cast<const u32x4*>(q);
+      }
+    }
+  };
+  // Piece (term, token tile, block, j, token) at slot token ^ (4 block + j) % 16 of its 16: both
+  // the writers (neighbouring pieces of one token) and the readers (16 tokens of one piece) then
+  // spread over all banks.
+  auto slot = [&](int s, int m, int b, int j, int t) {
+    return (((s * MT + m) * 16 + b) * 4 + j) * 16 + (t ^ ((4 * b + j) & 15));
+  };
+  auto put = [&](int buf) {
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
+      const int i = threadIdx.x + 512 * p;
+      if constexpr (CONV) {
+        const int t = i / 32, b = i % 32 / 2, h = i & 1;
+        u32x4 f[NT][2];
+        half_terms_of<BF16, HAD, NT>(xr[p], a.sign_mask, f);
+#pragma unroll
+        for (int s = 0; s < NT; ++s)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) xl[buf][slot(s, t / 16, b, 2 * h + j, t & 15)] = f[s][j];
+      } else {
+        const int t = i / 64, q = i % 64;
+        xl[buf][slot(0, t / 16, q / 4, q % 4, t & 15)] = xc[p];
+      }
+    }
+  };
+  auto sync = [] { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+
+  f32x4 acc[MT][RT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[m][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 q[4][RT], sc[RT], scn[RT];
+  auto load_codes = [&](int c, int d) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      q[d][r] = *reinterpret_cast<const u32x4*>(wrow[r] + (int64_t)c * 256 + 64 * d);
+  };
+  auto load_scales = [&](u32x4 (&o)[RT], int c) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) o[r] = load16_any(srow[r] + 16 * c);
+  };
+  auto chunk = [&](int c, int buf, auto more) {
+    if constexpr (more()) {
+      fetch(c + 1);
+      load_scales(scn, c + 1);
+    }
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      bf16x8_t w[RT][4];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) weights_of(q[d][r], (sc[r][d] >> (8 * g)) & 0xFFu, w[r]);
+      if constexpr (more()) load_codes(c + 1, d);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f32x4 p[RT];  // a step's products apart from the running sum, as in gemv_kernel
+#pragma unroll
+        for (int r = 0; r < RT; ++r) p[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = NT - 1; s >= 0; --s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bf16x8_t f =
+                __builtin_bit_cast(bf16x8_t, xl[buf][slot(s, m, 4 * d + g, j, i16)]);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+              p[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, w[r][j], p[r], 0, 0, 0);
+          }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[m][r] += p[r];
+      }
+    }
+    if constexpr (more()) {
+      put(buf ^ 1);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) sc[r] = scn[r];
+      sync();
+    }
+  };
+  if (c0 < c1) {
+    fetch(c0);
+    load_scales(sc, c0);
+#pragma unroll
+    for (int d = 0; d < 4; ++d) load_codes(c0, d);
+    put(0);
+    sync();
+    int c = c0;
+    for (; c + 1 < c1; ++c) chunk(c, (c - c0) & 1, std::true_type{});
+    chunk(c, (c - c0) & 1, std::false_type{});
+  }
+  // the blocks after the last whole chunk: every wave reads its steps' activations itself
+  if (blockIdx.z + 1 == (unsigned)splits) {
+    for (int b0 = nb / 16 * 16; b0 < nb; b0 += 4) {
+      const bool in = b0 + g < nb;  // past the end: zero weights and zero activations
+      bf16x8_t w[RT][4];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        uint32_t s = 0u;
+        if (in) {
+          v = *reinterpret_cast<const u32x4*>(wrow[r] + (int64_t)b0 * 16);
+          s = srow[r][b0 + g];
+        }
+        weights_of(v, s, w[r]);
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        RawX<BF16> x = {};
+        if (in) load_x<BF16>(x, token(16 * m + i16) + (int64_t)(b0 + g) * kBlock);
+        u32x4 f[NT][4];
+        terms_of<BF16, HAD, NT>(x, a.sign_mask, f);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = NT - 1; s >= 0; --s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f[s][j]),
+                                                          w[r][j], p, 0, 0, 0);
+          acc[m][r] += p;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t t = m0 + 16 * m + 4 * g + i, n = n0 + 16 * r + i16;
+        if (t >= a.T || n >= a.N) continue;
+        if (splits > 1) part[(blockIdx.z * a.T + t) * a.N + n] = acc[m][r][i];
+        else store_y(a, t * a.ldy + n, acc[m][r][i]);
+      }
+}
+
+// y = 2^alpha times the sum of the parts, in their order
+__global__ __launch_bounds__(256) void gemv_join_kernel(const GemvArgs a,
+                                                        const float* __restrict__ part,
+                                                        int splits) {
+  const int64_t count = a.T * a.N;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < count;
+       e += (int64_t)gridDim.x * 256) {
+    float v = part[e];
+    for (int s = 1; s < splits; ++s) v += part[s * count + e];
+    store_y(a, e / a.N * a.ldy + e % a.N, v);
+  }
+}
+
 __global__ __launch_bounds__(256) void gemv_zero_kernel(const GemvArgs a) {
   const int64_t count = a.T * a.N;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < count;
@@ -486,26 +750,75 @@ hipError_t launch_gemv(const GemvArgs& a, int bytes) {
   return hipGetLastError();
 }
 
+template <bool BF16, bool HAD, int NT, int MT, int RT>
+hipError_t launch_shared(const GemvArgs& a, float* part, int splits) {
+  constexpr int kRows = 128 * RT;
+  const int64_t gx = (a.N + kRows - 1) / kRows, gy = (a.T + 16 * MT - 1) / (16 * MT);
+  if (gx > (1 << 22) || gy > 32768) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((gemv_shared_kernel<BF16, HAD, NT, MT, RT>),
+                     dim3((unsigned)gx, (unsigned)gy, (unsigned)splits), dim3(512), 0,
+                     (hipStream_t)a.stream, a, part, splits);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess || splits == 1) return e;
+  const int64_t blocks = (a.T * a.N + 255) / 256;
+  hipLaunchKernelGGL(gemv_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256),
+                     0, (hipStream_t)a.stream, a, part, splits);
+  return hipGetLastError();
+}
+
 // Rows a workgroup takes (RT tiles of 16) so that about one workgroup a compute unit is left: more
 // rows share a fetch (and, in gemv_direct_kernel, a split) of the activations, fewer leave compute
 // units idle. 16 tokens, bf16, K 4096: N 14336 11.5 us with 4 tiles (224 workgroups), 16.4 with 2;
-// N 4096 7.3 us with 1 tile (256 workgroups), 8.5 with 2.
+// N 4096 7.2 us with 1 tile (256 workgroups), 8.5 with 2.
 constexpr int64_t kWorkgroups = 200;
+
+// Token tiles of gemv_shared_kernel: two chunks of NT terms take 32 KB of LDS a tile.
+constexpr int shared_tiles(int64_t T, int nt) {
+  return T > 32 && nt == 1 ? 4 : T > 16 && nt <= 2 ? 2 : 1;
+}
+
+// Parts of K for gemv_shared_kernel (several want a workspace), 0 where it is not taken. It pays once the codes take longer
+// than its second kernel, and with few tokens once K is long: 16 bf16 tokens, N 8192, K 28672: 31.8
+// us, 48.4 directly; N 14336, K 4096: 13.7 and 11.5; 64 tokens, N 28672, K 8192: 51.6 and 90.6; 16
+// rotated tokens, N 28672, K 8192: 37.6 and 50.9. One workgroup a compute unit (its 8 waves keep
+// 64 KB on the way; two were slower: 42.7 us for the last), at least two chunks a part.
+int shared_parts(int64_t T, int64_t N, int64_t K, int nt) {
+  const int64_t chunks = K / 512;
+  if (T == 1 || N * K < (1 << 25) || chunks < 2) return 0;
+  if (nt == 1 && T <= 16 && K < 8192) return 0;
+  const int64_t tiles = 16 * shared_tiles(T, nt);
+  const int64_t groups = (N + 255) / 256 * ((T + tiles - 1) / tiles);
+  const int64_t parts = 256 / groups < chunks / 2 ? 256 / groups : chunks / 2;
+  return parts > 1 ? (int)parts : 1;
+}
+
+constexpr int kLds = 128 * 1024;
+
+// Activations of all tokens through LDS in one piece: always better when they have to be rotated or
+// split (one token, N 14336, K 4096: rotated 10.9 us, 14.2 read directly; fp32 11.9 and 14.8), and
+// for one bf16 token (K 28672: 26.9 and 30.1 us); for several bf16 tokens the direct kernel is the
+// faster one (4 tokens, N 14336, K 4096: 9.7 and 11.1 us).
+bool takes_lds(int64_t T, int64_t K, int nt) {
+  return T == 1 || (nt > 1 && T <= 16 && T * K * 2 * nt <= kLds);
+}
 
 template <bool BF16, bool HAD, int NT>
 hipError_t pick_gemv(const GemvArgs& a) {
-  // Activations through LDS when a workgroup's share of it holds them: always better when they
-  // have to be rotated or split (one token, N 14336, K 4096: rotated 10.9 us, 14.2 read directly;
-  // fp32 11.9 and 14.8), and for one bf16 token (K 28672: 26.9 and 30.1 us); for several bf16
-  // tokens the direct kernel is the faster one (4 tokens, N 14336, K 4096: 9.7 and 11.1 us).
-  constexpr int kLds = 128 * 1024;
-  const bool one = a.T == 1;
-  if ((BF16 && !HAD) ? one : one || (a.T <= 16 && a.T * a.K * 2 * NT <= kLds)) {
+  if (takes_lds(a.T, a.K, NT)) {
     if (a.N < 16 * 2 * kWorkgroups) return launch_gemv<BF16, HAD, NT, 1, 8>(a, kLds);
     // 8 waves of 4 KB of codes each are needed to keep long rows coming; short ones leave half of
     // 8 waves without a group (one token, N 14336, K 4096: 9.3 us with 4, 10.1 with 8)
     return a.K > 4096 ? launch_gemv<BF16, HAD, NT, 2, 8>(a, kLds)
                       : launch_gemv<BF16, HAD, NT, 2, 4>(a, kLds);
+  }
+  const int parts = shared_parts(a.T, a.N, a.K, NT);
+  if (parts == 1 || (parts > 1 && a.part)) {
+    constexpr int kMost = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+    const int tiles = shared_tiles(a.T, NT);
+    if constexpr (kMost >= 4)
+      if (tiles == 4) return launch_shared<BF16, HAD, NT, 4, 2>(a, a.part, parts);
+    if constexpr (kMost >= 2)
+      if (tiles == 2) return launch_shared<BF16, HAD, NT, 2, 2>(a, a.part, parts);
+    return launch_shared<BF16, HAD, NT, 1, 2>(a, a.part, parts);
   }
   if (a.N >= 16 * 4 * kWorkgroups) {
     if constexpr (NT == 1) {
@@ -522,7 +835,20 @@ hipError_t pick_gemv(const GemvArgs& a) {
   return launch_direct<BF16, HAD, NT, 1, 1, 8>(a);
 }
 
+// bf16 terms of an activation: fp32 values take 3; rotated bf16 ones 2 when y is bf16
+int terms(bool bf16, bool hadamard, bool out_bf16) {
+  return bf16 && !hadamard ? 1 : bf16 && out_bf16 ? 2 : 3;
+}
+
 }  // namespace
+
+int64_t mx_gemv_workspace_bytes(int64_t T, int64_t N, int64_t K, bool bf16, bool hadamard,
+                                bool out_bf16) {
+  const int nt = terms(bf16, hadamard, out_bf16);
+  if (takes_lds(T, K, nt)) return 0;
+  const int64_t parts = shared_parts(T, N, K, nt);
+  return parts > 1 ? parts * T * N * (int64_t)sizeof(float) : 0;
+}
 
 hipError_t mx_launch_gemv(const GemvArgs& a) {
   if (a.K == 0) {

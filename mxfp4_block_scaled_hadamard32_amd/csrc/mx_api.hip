@@ -344,7 +344,7 @@ mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, in
 mx_status mx_gemv(const void* x, int32_t dtype, int64_t ldx, const uint8_t* wq, const uint8_t* ws,
                   int32_t gw, int64_t T, int64_t N, int64_t K, int32_t hadamard,
                   uint32_t sign_mask, int32_t alpha_exp, int32_t out_dtype, void* y, int64_t ldy,
-                  void* stream) {
+                  void* workspace, int64_t workspace_bytes, void* stream) {
   mx_status s = check_source(x, dtype, T, K, ldx);
   if (s != MX_OK) return s;
   if (N < 0 || K % 32 || ldy < N) return MX_ERR_SHAPE;
@@ -356,9 +356,19 @@ mx_status mx_gemv(const void* x, int32_t dtype, int64_t ldx, const uint8_t* wq, 
   if (!aligned(y, out_dtype == MX_BF16 ? 2 : 4) || !aligned(wq, 16)) return MX_ERR_ARG;
   if (T == 0 || N == 0) return MX_OK;
   if (!y || (K > 0 && (!x || !wq || !ws))) return MX_ERR_NULL;
+  const int64_t need = mx_gemv_workspace(dtype, T, N, K, hadamard, out_dtype);
+  if (workspace && need > 0 && (workspace_bytes < need || !aligned(workspace, 16)))
+    return MX_ERR_ARG;
   GemvArgs a{x, wq, ws, y, T, N, K, ldx, ldy, gw, alpha_exp, sign_mask, dtype == MX_BF16,
-             hadamard == 1, out_dtype == MX_BF16, stream};
+             hadamard == 1, out_dtype == MX_BF16, stream,
+             need > 0 ? static_cast<float*>(workspace) : nullptr};
   return launch_status(mx_launch_gemv(a));
+}
+
+int64_t mx_gemv_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, int32_t hadamard,
+                          int32_t out_dtype) {
+  if (T <= 0 || N <= 0 || K <= 0) return 0;
+  return mx_gemv_workspace_bytes(T, N, K, dtype == MX_BF16, hadamard == 1, out_dtype == MX_BF16);
 }
 
 const char* mx_status_string(int32_t status) {

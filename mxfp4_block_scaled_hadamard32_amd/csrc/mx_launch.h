@@ -126,5 +126,8 @@ struct GemvArgs {
   uint32_t sign_mask;
   bool bf16, hadamard, out_bf16;
   void* stream;
+  float* part;  // mx_gemv_workspace_bytes of workspace where that is not 0, or NULL
 };
+int64_t mx_gemv_workspace_bytes(int64_t T, int64_t N, int64_t K, bool bf16, bool hadamard,
+                                bool out_bf16);
 hipError_t mx_launch_gemv(const GemvArgs& a);

@@ -1,7 +1,9 @@
-"""Products of a few tokens with MXFP4 weights against float64: fp32 output within 2^-16 sum|x w|
-(the documented bound: a step's 128 products lose at most 132 times 2^-24 of their magnitude in
-the matrix core, and at most 72 fp32 additions join them), bf16 output the rounding of such a
-value. With the rotation, five fp32 stages round each x' five times: 5 more half steps."""
+"""Products of a few tokens with MXFP4 weights against float64: fp32 output within
+(160 + K / 128) 2^-24 sum|x w|, the documented bound: a step's 128 products, 4 instructions of 33
+addends each, lose at most 133 times 2^-24 of their magnitude in the matrix core (further bf16
+terms of x add 2^-8 of that), the K / 128 steps are joined by as many fp32 additions at most, and
+8 waves or 14 parts by their number. bf16 output is the rounding of such a value. With the
+rotation, five fp32 stages round each x' five times: 5 more half steps."""
 import numpy as np
 import pytest
 import torch
@@ -13,7 +15,12 @@ from tests.parity import check_gemm
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
-BOUND = 2.0 ** -16
+
+
+def bound(K):
+    return (160 + K / 128) * 2.0 ** -24
+
+
 MASK = 0x2C6FE9B1
 
 
@@ -57,20 +64,25 @@ def up(*arrays):
                                    (5, 14336, 512), (16, 28672, 256), (1, 512, 28672),
                                    (40, 9000, 256), (1, 13000, 8192), (3, 6500, 1056),
                                    (9, 12900, 4128), (20, 12900, 544), (50, 12900, 1600),
-                                   (1, 40, 65536), (2, 30, 65536), (16, 6401, 8224)])
+                                   (1, 40, 65536), (2, 30, 65536), (16, 6401, 8224),
+                                   # products that take a workspace: one and several parts of K,
+                                   # a part of a chunk left over, rows and tokens past the end
+                                   (2, 4099, 8224), (16, 4096, 8192), (23, 8200, 4128),
+                                   (64, 4100, 8256), (33, 33000, 1056), (70, 5000, 8192)])
 def test_against_float64(mx, orc, T, N, K, dtype):
     x = tokens(T, K, dtype)
     wq, ws = weights(N, K)
     C, Cabs = expected(orc, x, wq, ws, 1)
     dq, ds = up(wq, ws)
-    check_gemm(mx.mx_gemv(x.to(DEV), dq, ds, out_dtype=torch.float32), C, Cabs, rel=BOUND)
-    check_gemm(mx.mx_gemv(x.to(DEV), dq, ds), C, Cabs, rel=BOUND)
+    check_gemm(mx.mx_gemv(x.to(DEV), dq, ds, out_dtype=torch.float32), C, Cabs, rel=bound(K))
+    check_gemm(mx.mx_gemv(x.to(DEV), dq, ds), C, Cabs, rel=bound(K))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,N,K", [(1, 40, 4096), (7, 300, 1056), (16, 5000, 256), (35, 64, 512),
                                    (64, 200, 160), (2, 14000, 96),
-                                   (1, 13000, 8192), (1, 100, 65536), (20, 13000, 608)])
+                                   (1, 13000, 8192), (1, 100, 65536), (20, 13000, 608),
+                                   (16, 4100, 8224), (40, 8200, 4128)])
 def test_rotated_weights(mx, orc, T, N, K, dtype):
     """Weights as mx_quantize makes them with the signed transform; fp32's five stages on x."""
     w = wl.normal((N, K), 0.02, seed=4).to(torch.bfloat16)
@@ -83,10 +95,10 @@ def test_rotated_weights(mx, orc, T, N, K, dtype):
     A = np.abs(x.double().numpy()).reshape(T, K // 32, 32).sum(2).repeat(32, axis=1) @ W.T / 32
     y = mx.mx_gemv(x.to(DEV), dq, ds, hadamard=1, sign_mask=MASK, alpha_exp=-5,
                    out_dtype=torch.float32)
-    check_gemm(y, C, BOUND * Cabs + 5 * 2.0 ** -24 * A, rel=1.0)
+    check_gemm(y, C, bound(K) * Cabs + 5 * 2.0 ** -24 * A, rel=1.0)
     # bf16 y of bf16 x: 16 bits of each rotated value, half a step is 2^-17
     y16 = mx.mx_gemv(x.to(DEV), dq, ds, hadamard=1, sign_mask=MASK, alpha_exp=-5)
-    check_gemm(y16, C, (BOUND + 2.0 ** -17) * Cabs + 5 * 2.0 ** -24 * A, rel=1.0)
+    check_gemm(y16, C, (bound(K) + 2.0 ** -17) * Cabs + 5 * 2.0 ** -24 * A, rel=1.0)
     # the same product as the unrotated layer, up to the quantization of the weights
     plain = x.double() @ w.double().t()
     rel = float((y.double().cpu() - plain).norm() / plain.norm())
@@ -94,13 +106,43 @@ def test_rotated_weights(mx, orc, T, N, K, dtype):
 
 
 @pytest.mark.parametrize("g", [32, 64])
-@pytest.mark.parametrize("T,N,K", [(1, 192, 256), (20, 4096, 320)])
+@pytest.mark.parametrize("T,N,K", [(1, 192, 256), (20, 4096, 320), (20, 8192, 4096)])
 def test_tile_scales(mx, orc, g, T, N, K):
     x = tokens(T, K, "bf16")
     wq, ws = weights(N, K, g)
     C, Cabs = expected(orc, x, wq, ws, g)
     dq, ds = up(wq, ws)
-    check_gemm(mx.mx_gemv(x.to(DEV), dq, ds, g, out_dtype=torch.float32), C, Cabs, rel=BOUND)
+    check_gemm(mx.mx_gemv(x.to(DEV), dq, ds, g, out_dtype=torch.float32), C, Cabs, rel=bound(K))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_workspace(mx, orc, dtype):
+    """A given workspace (its end untouched), one of another call's leavings, and none at all."""
+    T, N, K = 20, 4100, 8256
+    x = tokens(T, K, dtype).to(DEV)
+    wq, ws = weights(N, K)
+    q, s = up(wq, ws)
+    size = mx.lib().mx_gemv_workspace(1 if dtype == "bf16" else 0, T, N, K, 0, 0)
+    assert size > 0 and size % (4 * T * N) == 0
+    y = mx.mx_gemv(x, q, s, out_dtype=torch.float32)
+    work = torch.full((size + 64,), 0xFF, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        assert torch.equal(mx.mx_gemv(x, q, s, out_dtype=torch.float32, workspace=work[:size]), y)
+    assert (work[size:] == 0xFF).all()
+    with pytest.raises(mx.MxError):
+        mx.mx_gemv(x, q, s, out_dtype=torch.float32, workspace=work[:size - 16])
+    # the C entry without one
+    out = torch.empty((T, N), device=DEV)
+    mx._launch("mx_gemv", x.device, None, x.data_ptr(), 1 if dtype == "bf16" else 0, K,
+               q.data_ptr(), s.data_ptr(), 1, T, N, K, 0, 0, 0, 0, out.data_ptr(), N, None, 0)
+    C, Cabs = expected(orc, x.cpu(), wq, ws, 1)
+    check_gemm(out, C, Cabs, rel=bound(K))
+    check_gemm(y, C, Cabs, rel=bound(K))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    z = mx.mx_gemv(x, q, s, out_dtype=torch.float32, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(z, y)
 
 
 @pytest.mark.parametrize("T", [1, 18, 50])
@@ -114,7 +156,7 @@ def test_leading_dimensions(mx, orc, T):
     out = torch.full((T + 2, N + 3), 7.0, dtype=torch.float32, device=DEV)
     y = mx.mx_gemv(wide[:, :K], dq, ds, alpha_exp=3, out=out[1:T + 1, :N])
     C, Cabs = expected(orc, x, wq, ws, 1, alpha=3)
-    check_gemm(y, C, Cabs, rel=BOUND)
+    check_gemm(y, C, Cabs, rel=bound(K))
     assert (out[0] == 7).all() and (out[T + 1] == 7).all() and (out[:, N:] == 7).all()
     if T > 1:
         again = mx.mx_gemv(x.to(DEV), dq, ds, alpha_exp=3, out_dtype=torch.float32)
@@ -166,14 +208,14 @@ def test_offsets_past_32_bits(mx, orc):
     pick = np.r_[0:64, N // 2:N // 2 + 64, N - 64:N]
     p = torch.from_numpy(pick).to(DEV)
     C, Cabs = expected(orc, x, q[p].cpu().numpy(), s[p].cpu().numpy(), 1)
-    check_gemm(y[:, p], C, Cabs, rel=BOUND)
+    check_gemm(y[:, p], C, Cabs, rel=bound(K))
 
 
 def test_streams_and_graph_replays(mx):
-    """Two captured products on streams of their own replayed at once, beside eager calls."""
-    K, N = 4096, 1040
+    """Three captured products (two of them with workspaces) on streams of their own replayed at once, beside eager calls."""
+    K, N = 8192, 4112
     q, s = up(*weights(N, K))
-    xs = [torch.zeros((t, K), dtype=torch.bfloat16, device=DEV) for t in (1, 20)]
+    xs = [torch.zeros((t, K), dtype=torch.bfloat16, device=DEV) for t in (1, 20, 17)]
     for x in xs:
         mx.mx_gemv(x, q, s)
     torch.cuda.synchronize()

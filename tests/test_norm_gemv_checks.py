@@ -106,7 +106,7 @@ def test_backward_workspace_size(m):
 
 def gemv_call(m, **kw):
     v = dict(x=A, dtype=1, ldx=64, wq=A, ws=A, gw=1, T=3, N=10, K=64, had=0, mask=0, alpha=0,
-             odt=1, y=A, ldy=10)
+             odt=1, y=A, ldy=10, work=None, size=0)
     v.update(kw)
     return m.lib().mx_gemv(*v.values(), None)
 
@@ -124,6 +124,20 @@ def gemv_call(m, **kw):
 ])
 def test_gemv_refusals(m, bad, status):
     assert gemv_call(m, **bad) == getattr(m, "MX_ERR_" + status)
+
+
+def test_gemv_workspace(m):
+    f = m.lib().mx_gemv_workspace
+    big = dict(T=16, N=8192, K=28672, ldx=28672, ldy=8192)
+    need = f(1, 16, 8192, 28672, 0, 1)
+    assert need > 0 and need % (4 * 16 * 8192) == 0
+    assert gemv_call(m, work=A, size=need - 1, **big) == m.MX_ERR_ARG
+    assert gemv_call(m, work=ctypes.c_void_p(0x10008), size=need, **big) == m.MX_ERR_ARG
+    for dtype in (0, 1):
+        for had in (0, 1):
+            assert f(dtype, 1, 8192, 28672, had, 1) == 0   # one token
+            assert f(dtype, 16, 100, 512, had, 1) == 0     # a small product
+            assert f(dtype, 0, 8192, 28672, had, 1) == 0
 
 
 def test_gemv_nothing_to_do(m):
