@@ -189,13 +189,13 @@ __host__ __device__ constexpr int scale_pitch(int seg) { return (seg + 15) / 16 
 // with the same step of the wave's next group as soon as they have been used. A segment of K
 // (seg blocks) at a time when LDS does not hold all of it. The waves' sums are joined through LDS
 // in a fixed order.
-template <bool BF16, bool HAD, int NT, int RT, int WV>
+template <bool BF16, bool HAD, int NT, int RT, int WV, bool ONE>
 __global__ __launch_bounds__(64 * WV) void gemv_kernel(const GemvArgs a, int seg) {
   constexpr int kThreads = 64 * WV;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
-  const int T = (int)a.T;
+  const int T = ONE ? 1 : (int)a.T;  // a single token's addresses in LDS are constants
   const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
   const int nb = (int)(a.K / 32);
   const int pitch = scale_pitch(seg);
@@ -745,8 +745,15 @@ hipError_t launch_gemv(const GemvArgs& a, int bytes) {
   const int srows = a.gw == 1 ? 16 * RT : (16 * RT + a.gw - 1) / a.gw;
   const size_t use = (size_t)NT * seg * 64 * a.T + (size_t)srows * scale_pitch(seg);
   const size_t join = (size_t)WV * RT * 1024;
-  hipLaunchKernelGGL((gemv_kernel<BF16, HAD, NT, RT, WV>), dim3((unsigned)gx), dim3(64 * WV),
-                     use > join ? use : join, (hipStream_t)a.stream, a, seg);
+  const dim3 grid((unsigned)gx), block(64 * WV);
+  if (a.T == 1) {
+    hipLaunchKernelGGL((gemv_kernel<BF16, HAD, NT, RT, WV, true>), grid, block,
+                       use > join ? use : join, (hipStream_t)a.stream, a, seg);
+    return hipGetLastError();
+  }
+  if constexpr (NT > 1)  // takes_lds
+    hipLaunchKernelGGL((gemv_kernel<BF16, HAD, NT, RT, WV, false>), grid, block,
+                       use > join ? use : join, (hipStream_t)a.stream, a, seg);
   return hipGetLastError();
 }
 
@@ -804,11 +811,14 @@ bool takes_lds(int64_t T, int64_t K, int nt) {
 template <bool BF16, bool HAD, int NT>
 hipError_t pick_gemv(const GemvArgs& a) {
   if (takes_lds(a.T, a.K, NT)) {
+    // Few workgroups need 8 waves each to keep enough codes coming (one bf16 token, N 8192, K 28672:
+    // 26.8 us, 30.6 with 4 waves); with many, 4 waves and in the end one row tile do better (N
+    // 14336, K 4096: 9.2 us with 2 tiles of 4 waves, 10.1 with 8; N 28672, K 8192: 30.2 us with 1
+    // tile of 4, 32.1 with 2, over 34 with 2 of 8)
     if (a.N < 16 * 2 * kWorkgroups) return launch_gemv<BF16, HAD, NT, 1, 8>(a, kLds);
-    // 8 waves of 4 KB of codes each are needed to keep long rows coming; short ones leave half of
-    // 8 waves without a group (one token, N 14336, K 4096: 9.3 us with 4, 10.1 with 8)
-    return a.K > 4096 ? launch_gemv<BF16, HAD, NT, 2, 8>(a, kLds)
-                      : launch_gemv<BF16, HAD, NT, 2, 4>(a, kLds);
+    if (a.N < 16 * 3 * kWorkgroups) return launch_gemv<BF16, HAD, NT, 2, 8>(a, kLds);
+    if (a.N < 16 * 5 * kWorkgroups) return launch_gemv<BF16, HAD, NT, 2, 4>(a, kLds);
+    return launch_gemv<BF16, HAD, NT, 1, 4>(a, kLds);
   }
   const int parts = shared_parts(a.T, a.N, a.K, NT);
   if (parts == 1 || (parts > 1 && a.part)) {
