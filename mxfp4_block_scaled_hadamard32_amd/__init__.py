@@ -64,9 +64,12 @@ def _buf(t, name: str, shape, dtypes, device, rows_only: bool = False):
     """Checks a caller-supplied buffer before its address goes to a kernel: a tensor on `device`
     with one of `dtypes` and exactly `shape`, contiguous (rows_only: only its rows contiguous,
     for outputs with a leading dimension). Raises ValueError / TypeError otherwise."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        return t  # what nearly every call has; the rest finds out what is wrong
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device and t.device != torch.device(device):
+    if t.device != torch.device(device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
@@ -333,6 +336,9 @@ def _rows(t, name: str):
 
 def _rows_like(t, name: str, x):
     """Another [rows][cols] operand of x's shape, type and device; returns its ld."""
+    if (isinstance(t, torch.Tensor) and t.dtype is x.dtype and t.shape == x.shape
+            and t.device == x.device and t.is_contiguous()):
+        return t.shape[1]
     rows, cols, ld = _rows(t, name)
     if (rows, cols) != tuple(x.shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(x.shape)}")

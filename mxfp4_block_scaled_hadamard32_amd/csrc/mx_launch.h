@@ -96,7 +96,8 @@ struct NormArgs {
 };
 hipError_t mx_launch_rmsnorm(const NormArgs& a);
 
-// Its backward pass. partial: mx_norm_backward_blocks(rows, cols) * cols floats, NULL with dgamma.
+// Its backward pass. partial: at least mx_norm_backward_blocks(rows, cols) * cols floats (the most
+// that either type uses), NULL without dgamma.
 struct NormBackwardArgs {
   const void* dy;
   const void* dsum;

@@ -156,9 +156,9 @@ __device__ __forceinline__ double add_halves(double v) {
   return v;
 }
 
-// Sum over the T threads of a row (16 or 64 lanes, or the workgroup); every thread gets the same
-// value. red: one value a wave, in one of two areas in turn from one row to the next, so that one
-// barrier a row is enough.
+// Sum over the T threads of a row (16 or 64 lanes, or several waves of the workgroup, all of which
+// take part); every thread gets the same value. red: one value a wave, in one of two areas in turn
+// from one row to the next, so that one barrier a row is enough.
 template <int T, class F>
 __device__ __forceinline__ F row_sum(F v, F* red) {
   static_assert(T == 16 || T % 64 == 0);
@@ -167,6 +167,7 @@ __device__ __forceinline__ F row_sum(F v, F* red) {
   if constexpr (T > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
+    red += threadIdx.x / T * (T / 64);
     v = red[0];
 #pragma unroll
     for (int w = 1; w < T / 64; ++w) v += red[w];
@@ -407,84 +408,120 @@ hipError_t pick_norm_format(const NormArgs& a) {
 // ---------------------------------------------------------------------------------------------
 // A workgroup walks over rows like the forward kernel and keeps its columns' sums of dy z in
 // registers; rmsnorm_dgamma_kernel joins the workgroups' sums, partial[block][cols], in a fixed
-// order.
+// order. Two rows and more a workgroup halve what it has to read.
+template <bool BF16, int T>
+constexpr int kBackwardThreads = T <= 64 ? 256 : T <= 256 || (BF16 && T <= 512) ? 2 * T : T;
+
 template <bool BF16, int T, int V, bool DSUM>
-__global__ __launch_bounds__(T > 256 ? T : 256) void rmsnorm_backward_kernel(
+__global__ __launch_bounds__((kBackwardThreads<BF16, T>)) void rmsnorm_backward_kernel(
     const NormBackwardArgs a) {
-  constexpr int kThreads = T > 256 ? T : 256;
+  constexpr int kThreads = kBackwardThreads<BF16, T>;
   constexpr int kRows = kThreads / T;
-  constexpr bool kAhead = V < 4;  // 4 chunks leave no registers for the next row's
-  __shared__ float red[2][T > 64 ? T / 64 : 1];
+  // The widest rows leave no registers for the next row's values (16 waves have 128 each), nor for
+  // their own between the sum and the result: they are read again, from the caches.
+  constexpr bool kAhead = V < 4 && (BF16 || T < 1024);
+  __shared__ float red[2][kThreads / 64];
   __shared__ float join[kRows > 1 ? kRows : 1][kRows > 1 ? T * V * 8 : 1];
   const int t = threadIdx.x % T, sub = threadIdx.x / T;
   const int nch = (int)(a.cols / 8);
-  float g[V][8], acc[V][8];
+  float g[V][8], acc[V][8];  // g only where the next row is loaded ahead
   int col[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = t + v * T;
     col[v] = 8 * (c < nch ? c : nch - 1);
-    load_gamma(a.gamma, a.gamma_bf16, col[v], g[v]);
+    if constexpr (kAhead) load_gamma(a.gamma, a.gamma_bf16, col[v], g[v]);
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[v][k] = 0.0f;
   }
   const int64_t stride = (int64_t)gridDim.x * kRows;
   int64_t row = (int64_t)blockIdx.x * kRows + sub;
-  RawChunk<BF16> dy[V], s[V], d[DSUM ? V : 1];
+  constexpr int kHeld = kAhead ? V : 1;
+  RawChunk<BF16> dy[kHeld], s[kHeld], d[DSUM ? kHeld : 1];
   float rho;
   auto load_row = [&](int64_t i) {
     i = i < a.rows ? i : a.rows - 1;
     rho = a.rstd[i];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < kHeld; ++v) {
       dy[v] = load_raw<BF16>(a.dy, i * a.lddy + col[v]);
       s[v] = load_raw<BF16>(a.s, i * a.lds + col[v]);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < kHeld; ++v)
       if constexpr (DSUM) d[v] = load_raw<BF16>(a.dsum, i * a.ldds + col[v]);
+  };
+  // a chunk's share of the sum of u z, and its dy z
+  auto first = [&](int v, const RawChunk<BF16>& cy, const RawChunk<BF16>& cs, const float (&w)[8],
+                   float r, bool on, float& sum) {
+    float y[8], z[8];
+    values<BF16>(cy, y);
+    values<BF16>(cs, z);
+    if (on) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float p = y[k] * (z[k] * r);  // dy z
+        acc[v][k] += p;
+        sum = fmaf(p, w[k], sum);
+      }
+    }
+  };
+  auto second = [&](int v, const RawChunk<BF16>& cy, const RawChunk<BF16>& cs,
+                    const RawChunk<BF16>& cd, const float (&w)[8], float r, float mean) {
+    float y[8], z[8], o[8];
+    values<BF16>(cy, y);
+    values<BF16>(cs, z);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = r * (y[k] * w[k] - z[k] * r * mean);
+    if constexpr (DSUM) {
+      values<BF16>(cd, y);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] += y[k];
+    }
+    store_raw<BF16>(a.dx, row * a.lddx + col[v], raw_of<BF16>(o));
   };
   if constexpr (kAhead) load_row(row);
   for (int par = 0; row - sub < a.rows; row += stride, par ^= 1) {
     const bool live = row < a.rows;
-    if constexpr (!kAhead) load_row(row);
-    RawChunk<BF16> y0[V], s0[V], d0[DSUM ? V : 1];
-    const float r = rho;
     float sum = 0.0f;
+    if constexpr (kAhead) {
+      RawChunk<BF16> y0[V], s0[V], d0[DSUM ? V : 1];
+      const float r = rho;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      y0[v] = dy[v];
-      s0[v] = s[v];
-      if constexpr (DSUM) d0[v] = d[v];
-      float y[8], z[8];
-      values<BF16>(y0[v], y);
-      values<BF16>(s0[v], z);
-      if (live && t + v * T < nch) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float p = y[k] * (z[k] * r);  // dy z
-          acc[v][k] += p;
-          sum = fmaf(p, g[v][k], sum);
-        }
+      for (int v = 0; v < V; ++v) {
+        y0[v] = dy[v];
+        s0[v] = s[v];
+        if constexpr (DSUM) d0[v] = d[v];
+        first(v, y0[v], s0[v], g[v], r, live && t + v * T < nch, sum);
       }
-    }
-    if constexpr (kAhead) load_row(row + stride);
-    const float mean = row_sum<T>(sum, red[par]) * a.inv_cols;
-    if (!live) continue;
+      load_row(row + stride);
+      const float mean = row_sum<T>(sum, red[par]) * a.inv_cols;
+      if (!live) continue;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (t + v * T >= nch) continue;
-      float y[8], z[8], o[8];
-      values<BF16>(y0[v], y);
-      values<BF16>(s0[v], z);
+      for (int v = 0; v < V; ++v)
+        if (t + v * T < nch) second(v, y0[v], s0[v], d0[DSUM ? v : 0], g[v], r, mean);
+    } else {
+      const int64_t i = live ? row : a.rows - 1;
+      const float r = a.rstd[i];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = r * (y[k] * g[v][k] - z[k] * r * mean);
-      if constexpr (DSUM) {
-        values<BF16>(d0[v], y);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] += y[k];
+      for (int v = 0; v < V; ++v) {
+        float w[8];
+        load_gamma(a.gamma, a.gamma_bf16, col[v], w);
+        first(v, load_raw<BF16>(a.dy, i * a.lddy + col[v]), load_raw<BF16>(a.s, i * a.lds + col[v]),
+              w, r, live && t + v * T < nch, sum);
       }
-      store_raw<BF16>(a.dx, row * a.lddx + col[v], raw_of<BF16>(o));
+      const float mean = row_sum<T>(sum, red[par]) * a.inv_cols;
+      if (!live) continue;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (t + v * T >= nch) continue;
+        float w[8];
+        load_gamma(a.gamma, a.gamma_bf16, col[v], w);
+        RawChunk<BF16> cd = {};
+        if constexpr (DSUM) cd = load_raw<BF16>(a.dsum, i * a.ldds + col[v]);
+        second(v, load_raw<BF16>(a.dy, i * a.lddy + col[v]),
+               load_raw<BF16>(a.s, i * a.lds + col[v]), cd, w, r, mean);
+      }
     }
   }
   if (!a.partial) return;
@@ -542,9 +579,9 @@ __global__ __launch_bounds__(256) void rmsnorm_dgamma_kernel(const float* __rest
 
 // workgroups of the backward kernel: what 256 compute units hold at 6 waves a SIMD with one chunk
 // a thread, 4 with more; fewer for few rows, whose sums would be as much traffic as the rows
-template <int T, int V>
+template <bool BF16, int T, int V>
 int64_t backward_blocks(int64_t rows) {
-  constexpr int kThreads = T > 256 ? T : 256;
+  constexpr int kThreads = kBackwardThreads<BF16, T>;
   constexpr int kRows = kThreads / T;
   constexpr int64_t most = 256 * 4 * 64 * (V == 1 ? 6 : 4) / kThreads;
   const int64_t want = (rows + kRows - 1) / kRows;
@@ -555,8 +592,8 @@ int64_t backward_blocks(int64_t rows) {
 
 template <bool BF16, int T, int V>
 hipError_t launch_backward(NormBackwardArgs a) {
-  constexpr int kThreads = T > 256 ? T : 256;
-  const int blocks = (int)backward_blocks<T, V>(a.rows);
+  constexpr int kThreads = kBackwardThreads<BF16, T>;
+  const int blocks = (int)backward_blocks<BF16, T, V>(a.rows);
   a.inv_cols = 1.0f / (float)a.cols;
   if (blocks > 0) {
     if (a.dsum)
@@ -576,7 +613,10 @@ hipError_t launch_backward(NormBackwardArgs a) {
 }  // namespace
 
 int64_t mx_norm_backward_blocks(int64_t rows, int64_t cols) {
-  return with_shape(cols, [&](auto t, auto v) { return backward_blocks<t(), v()>(rows); });
+  return with_shape(cols, [&](auto t, auto v) {
+    const int64_t b = backward_blocks<true, t(), v()>(rows), f = backward_blocks<false, t(), v()>(rows);
+    return b > f ? b : f;
+  });
 }
 
 hipError_t mx_launch_rmsnorm(const NormArgs& a) {
