@@ -267,7 +267,8 @@ mx_status mx_scale_mismatch_map(const void* x, int32_t dtype, int64_t rows, int6
  * the stored sum. The sum of squares, rho and y are formed in 64 bits and every output is rounded
  * once, to the nearest value, so a row's outputs depend on that row alone (not on how many rows
  * share the call). A row that holds an infinity or a NaN gives NaNs (or zeros beside an infinity),
- * as the formula does. sum and y may each be x or residual itself (same leading dimension).
+ * as the formula does. sum and y may each be x or residual itself (same leading dimension), not
+ * both the same one.
  * cols is a multiple of 32 and at most 32768 (MX_ERR_UNSUPPORTED beyond); pointers to rows and
  * gamma 16-byte aligned, rstd 4-byte, every leading dimension * element size a multiple of 16
  * bytes. Errors (nothing is launched): MX_ERR_NULL for a NULL x, gamma or y; MX_ERR_SHAPE for
@@ -302,10 +303,11 @@ mx_status mx_rmsnorm_quant_mxfp8(const void* x, int64_t ldx, const void* residua
  *   dx = rstd * (u - z * c) + dsum     (the gradient of x and of residual alike),
  *   dgamma[j] = sum over the rows of dy * z   (fp32; may be NULL).
  * fp32 throughout, dx rounded to dtype at the end; the order of every sum is fixed by the sizes.
- * dx may be dy or dsum itself (same leading dimension). With dgamma, workspace holds at least
- * mx_rmsnorm_backward_workspace(rows, cols) bytes, 16-byte aligned; its contents are scratch, and
- * calls that may run at the same time need one each. Sizes, alignment and errors as for
- * mx_rmsnorm; MX_ERR_ARG also for a workspace that is too small. rows == 0 writes a zero dgamma. */
+ * dx may be dsum itself (same leading dimension), or without dgamma dy. With dgamma, workspace
+ * holds at least mx_rmsnorm_backward_workspace(rows, cols) bytes (0 for small tensors), 16-byte
+ * aligned; its contents are scratch, and calls that may run at the same time need one each. Sizes, alignment and errors as for
+ * mx_rmsnorm; MX_ERR_ARG also for a workspace that is too small and for dx on dy or s with
+ * dgamma. rows == 0 writes a zero dgamma. */
 int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
 mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, int64_t ldds,
                               const void* s, int64_t lds, int32_t dtype, int64_t rows,

@@ -474,7 +474,8 @@ def mx_rmsnorm_backward(dy, s, gamma, rstd, dsum=None, with_dgamma: bool = True,
             _buf(workspace, "workspace", (size,), _U8, dev)
         else:
             size = lib().mx_rmsnorm_backward_workspace(rows, cols)
-            workspace = _scratch(size, dev, stream)
+            if size:  # small tensors want none
+                workspace = _scratch(size, dev, stream)
     else:
         dgamma = workspace = None
     _launch("mx_rmsnorm_backward", dev, stream, dy.data_ptr(), lddy, _data(dsum), ldds,

@@ -332,12 +332,15 @@ mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, in
   if (cols == 0 || (rows == 0 && !dgamma)) return MX_OK;
   if (rows > 0) {
     if (!dy || !s || !gamma || !rstd || !dx) return MX_ERR_NULL;
-    if (dgamma && !workspace) return MX_ERR_NULL;
-    if (dgamma && workspace_bytes < mx_rmsnorm_backward_workspace(rows, cols)) return MX_ERR_ARG;
+    // dgamma reads dy beside the rows that are written
+    if (dgamma && (dx == dy || dx == s)) return MX_ERR_ARG;
+    const int64_t need = dgamma ? mx_rmsnorm_backward_workspace(rows, cols) : 0;
+    if (need > 0 && !workspace) return MX_ERR_NULL;
+    if (workspace_bytes < need) return MX_ERR_ARG;
   }
   NormBackwardArgs a{dy,   dsum, s,    gamma, rstd, dx,   dgamma, dgamma ? (float*)workspace : nullptr,
                      rows, cols, lddy, ldds,  lds,  lddx, dtype == MX_BF16,
-                     gamma_dtype == MX_BF16, stream, 0.0f};
+                     gamma_dtype == MX_BF16, stream, 0.0f, 0};
   return launch_status(mx_launch_rmsnorm_backward(a));
 }
 

@@ -97,7 +97,7 @@ struct NormArgs {
 hipError_t mx_launch_rmsnorm(const NormArgs& a);
 
 // Its backward pass. partial: at least mx_norm_backward_blocks(rows, cols) * cols floats (the most
-// that either type uses), NULL without dgamma.
+// that either type uses; 0 for small tensors), NULL without dgamma.
 struct NormBackwardArgs {
   const void* dy;
   const void* dsum;
@@ -110,7 +110,8 @@ struct NormBackwardArgs {
   int64_t rows, cols, lddy, ldds, lds, lddx;
   bool bf16, gamma_bf16;
   void* stream;
-  float inv_cols;  // set by the launcher
+  float inv_cols;  // set by the launcher, as row_blocks
+  int row_blocks;
 };
 int64_t mx_norm_backward_blocks(int64_t rows, int64_t cols);
 hipError_t mx_launch_rmsnorm_backward(const NormBackwardArgs& a);

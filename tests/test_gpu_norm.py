@@ -222,7 +222,8 @@ def test_offsets_past_32_bits(mx):
     y0, s0, r0 = mx.mx_rmsnorm(dev(src), g)
     assert torch.equal(x, y0)
     dx0, dg0 = mx.mx_rmsnorm_backward(y0, s0, g, r0)
-    dx, dg = mx.mx_rmsnorm_backward(x, s0, g, r0, dx=x)
+    _, dg = mx.mx_rmsnorm_backward(x, s0, g, r0)
+    dx, _ = mx.mx_rmsnorm_backward(x, s0, g, r0, dx=x, with_dgamma=False)
     assert torch.equal(x, dx0) and torch.equal(dg, dg0)
     del buf, x, y, dx
     rows = (1 << 26) + 5
@@ -258,17 +259,21 @@ def check_backward(dx, dgamma, dy, s, g, rstd, d):
         lo, hi = bf16_round_f64(lo), bf16_round_f64(hi)
     bad = ~((got >= lo) & (got <= hi))
     assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist())
-    # more than 256 rows are shared by at least 256 workgroups, so one adds at most rows / 256 + 1
-    # of them one after the other and joins 16 at the end; the workgroups' sums are joined in 64
-    # bits. z, the product and the last rounding: one each
-    n = s.shape[0] // 256 + 1 + 16 + 3
+    # a thread adds at most rows / 64 + 1 rows one after the other (64 slices of the rows, or at
+    # least 256 workgroups that share more than 256 rows); then at most 4 lane steps and 16 waves,
+    # or 16 rows of a workgroup and a join in 64 bits. z, the product and the last rounding: one each
+    n = s.shape[0] // 64 + 1 + 20 + 3
     err = np.abs(dgamma.cpu().numpy().astype(np.float64) - dg)
     assert (err <= n * ref.EPS32 * dgabs).all(), float((err / (dgabs + 1e-300)).max())
 
 
 @pytest.mark.parametrize("dsum", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,cols", SHAPES + [(2500, 256), (1100, 2720), (20000, 128)])
+@pytest.mark.parametrize("rows,cols", SHAPES + [(2500, 256), (1100, 2720), (20000, 128),
+                                                # past 2^22 elements: dgamma by workgroups' sums
+                                                (40000, 128), (8300, 512), (4500, 1024),
+                                                (2100, 2048), (1600, 2720), (550, 8192),
+                                                (530, 8224), (140, 32768), (257, 16416)])
 def test_backward_against_the_formula(mx, rows, cols, dtype, dsum):
     dy, s, g, rstd, d = make_backward(rows, cols, dtype, dsum, "bf16" if cols % 64 else "f32")
     dx, dg = mx.mx_rmsnorm_backward(dev(dy), dev(s), dev(g), dev(rstd), dsum=dev(d))
@@ -312,8 +317,9 @@ def test_backward_against_differences(mx):
     assert abs(got - fd) <= noise / (2 * h) + slack + fp32
 
 
-def test_backward_leading_dimensions_and_aliasing(mx):
-    rows, cols, pad = 9, 1056, 40
+@pytest.mark.parametrize("rows,cols", [(9, 1056), (4100, 1056)])
+def test_backward_leading_dimensions_and_aliasing(mx, rows, cols):
+    pad = 40
     dy, s, g, rstd, d = (dev(t) for t in make_backward(rows, cols, "bf16", True))
     dx0, dg0 = mx.mx_rmsnorm_backward(dy, s, g, rstd, dsum=d)
     wide = [torch.full((rows, cols + pad), 7.0, dtype=s.dtype, device=DEV) for _ in range(4)]
@@ -322,22 +328,25 @@ def test_backward_leading_dimensions_and_aliasing(mx):
     wdy, ws, wd, wdx = (w[:, :cols] for w in wide)
     dx, dg = mx.mx_rmsnorm_backward(wdy, ws, g, rstd, dsum=wd, dx=wdx)
     assert torch.equal(wdx, dx0) and torch.equal(dg, dg0)
-    mx.mx_rmsnorm_backward(wdy, ws, g, rstd, dsum=wd, dx=wdy)  # over dy
-    assert torch.equal(wdy, dx0)
-    wdy.copy_(dy)
     size = mx.lib().mx_rmsnorm_backward_workspace(rows, cols)
+    assert (size > 0) == (rows * cols > 1 << 22)
     work = torch.full((size + 16,), 0xA5, dtype=torch.uint8, device=DEV)
     _, dg = mx.mx_rmsnorm_backward(wdy, ws, g, rstd, dsum=wd, dx=wd, workspace=work[:size])
     assert torch.equal(wd, dx0) and torch.equal(dg, dg0)  # over dsum
     assert (work[size:] == 0xA5).all()
+    wd.copy_(d)
+    mx.mx_rmsnorm_backward(wdy, ws, g, rstd, dsum=wd, dx=wdy, with_dgamma=False)  # over dy
+    assert torch.equal(wdy, dx0)
+    with pytest.raises(mx.MxError):
+        mx.mx_rmsnorm_backward(wdy, ws, g, rstd, dx=wdy)
     for w in wide:
         assert (w[:, cols:] == 7.0).all()
 
 
-def test_streams_and_graph_replays(mx):
-    """The norm and its backward pass captured together on a side stream, replayed on new inputs
-    beside eager calls."""
-    rows, cols = 65, 4096
+@pytest.mark.parametrize("rows,cols", [(65, 4096), (1030, 4096)])
+def test_streams_and_graph_replays(mx, rows, cols):
+    """The norm and its backward pass (without and with a workspace) captured together on a side
+    stream, replayed on new inputs beside eager calls."""
     x, r, g = (dev(t) for t in make(rows, cols, "bf16", True))
     dy = dev(wl.normal((rows, cols), 1e-2, seed=3).to(torch.bfloat16))
 

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 A = ctypes.c_void_p(0x10000)   # aligned, never dereferenced
+B = ctypes.c_void_p(0x20000)
 ODD = ctypes.c_void_p(0x10004)
 
 
@@ -70,8 +71,8 @@ def test_norm_output_refusals(m):
 
 
 def backward_call(m, **kw):
-    v = dict(dy=A, lddy=64, dsum=A, ldds=64, s=A, lds=64, dtype=1, rows=4, cols=64, gamma=A, gdt=0,
-             rstd=A, dx=A, lddx=64, dgamma=A, work=A, size=1 << 20)
+    v = dict(dy=A, lddy=64, dsum=B, ldds=64, s=A, lds=64, dtype=1, rows=1 << 20, cols=64, gamma=A,
+             gdt=0, rstd=A, dx=B, lddx=64, dgamma=A, work=A, size=1 << 20)
     v.update(kw)
     return m.lib().mx_rmsnorm_backward(*v.values(), None)
 
@@ -85,7 +86,7 @@ def backward_call(m, **kw):
     (dict(dtype=5), "ARG"), (dict(gdt=5), "ARG"), (dict(dy=ODD), "ARG"), (dict(dsum=ODD), "ARG"),
     (dict(s=ODD), "ARG"), (dict(dx=ODD), "ARG"), (dict(gamma=ODD), "ARG"), (dict(work=ODD), "ARG"),
     (dict(rstd=ctypes.c_void_p(0x10001)), "ARG"), (dict(dgamma=ctypes.c_void_p(0x10002)), "ARG"),
-    (dict(size=16), "ARG"),
+    (dict(size=16), "ARG"), (dict(dx=A), "ARG"),
 ])
 def test_backward_refusals(m, bad, status):
     assert backward_call(m, **bad) == getattr(m, "MX_ERR_" + status)
@@ -100,7 +101,8 @@ def test_backward_workspace_size(m):
     f = m.lib().mx_rmsnorm_backward_workspace
     assert f(0, 64) == 0 and f(4, 0) == 0 and f(-1, 64) == 0 and f(4, 40) == 0
     assert f(4, 65536) == 0
-    for rows, cols in ((1, 32), (16384, 8192), (1 << 20, 128), (3, 32768)):
+    assert f(1, 32) == 0 and f(4096, 1024) == 0  # small tensors
+    for rows, cols in ((4097, 1024), (16384, 8192), (1 << 20, 128), (129, 32768)):
         assert f(rows, cols) % (4 * cols) == 0 and 0 < f(rows, cols) <= min(rows, 1536) * 4 * cols
 
 
