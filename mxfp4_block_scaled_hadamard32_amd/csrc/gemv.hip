@@ -560,11 +560,12 @@ __global__ __launch_bounds__(512) void gemv_shared_kernel(const GemvArgs a, floa
       }
     }
   };
-  // Piece (term, token tile, block, j, token) at slot token ^ (4 block + j) % 16 of its 16: both
-  // the writers (neighbouring pieces of one token) and the readers (16 tokens of one piece) then
-  // spread over all banks.
+  // Piece (term, token tile, block, j, token) at slot token ^ (4 (block / 2) + j) % 16 of its 16:
+  // the writers (neighbouring pieces of one token) spread over the banks, and the readers (16
+  // tokens of blocks g, of which a 16-byte read serves tokens 0-3 and 12-15 of one block together
+  // with 4-11 of its neighbour) meet no conflict: neighbours share the exchange.
   auto slot = [&](int s, int m, int b, int j, int t) {
-    return (((s * MT + m) * 16 + b) * 4 + j) * 16 + (t ^ ((4 * b + j) & 15));
+    return (((s * MT + m) * 16 + b) * 4 + j) * 16 + (t ^ ((4 * (b >> 1) + j) & 15));
   };
   auto put = [&](int buf) {
 #pragma unroll
