@@ -18,8 +18,10 @@ using namespace mxd;
 
 namespace {
 
-// threads of a grid: what 256 compute units hold at 6 waves a SIMD
-constexpr int64_t kNormThreads = 256 * 6 * 4 * 64;
+// threads of a grid: 12 waves a SIMD of 256 compute units, two to three times what they hold, which
+// evens out the workgroups' ends (262144 rows of 128: 25.4 us, 27.9 with 6 waves, 31.0 with 4;
+// 8192 x 4096: 58.0, 60.4 and 58.5)
+constexpr int64_t kNormThreads = 256 * 12 * 4 * 64;
 
 // 8 values of a row chunk
 template <bool BF16>
@@ -56,7 +58,7 @@ __device__ __forceinline__ void load_gamma(const void* g, bool bf16, int64_t off
 
 // s rho g as hi + lo: products with their rounding errors, which the fused multiply-add gives
 // exactly. |lo| is at most a few half steps of hi; what is dropped is 2^-47 of the product (more
-// where errors fall below fp32's range: |y| under 2^-100, rho under 2^-100).
+// where errors fall below fp32's range: |y| under 2^-100; rho is kept within 2^-90 .. 2^90).
 __device__ __forceinline__ void product(float s, float rho, float rho_lo, float g, float& hi,
                                         float& lo) {
   const float p = s * rho;
@@ -65,9 +67,13 @@ __device__ __forceinline__ void product(float s, float rho, float rho_lo, float 
   lo = fmaf(pe, g, fmaf(p, g, -hi));
 }
 
-// hi + lo to nearest; a zero keeps the sign of hi (codes carry it), where -0 + 0 would be +0
+// hi + lo to nearest; a zero keeps the sign of hi (codes carry it), where -0 + 0 would be +0. Where
+// hi is infinite, lo is the opposite infinity and the sum a NaN: see nearest.
 __device__ __forceinline__ float sum_of(float hi, float lo) {
   return __builtin_copysignf(hi + lo, hi);
+}
+__device__ __forceinline__ float nearest(float hi, float lo) {
+  return fabsf(hi) < __builtin_inff() ? sum_of(hi, lo) : hi;
 }
 
 // hi + lo in fp32 by rounding to odd: of the two fp32 values around an inexact sum the one whose
@@ -75,7 +81,7 @@ __device__ __forceinline__ float sum_of(float hi, float lo) {
 // E2M1, the thresholds of the stochastic rounding, the block maximum's exponent) is then the
 // rounding of hi + lo itself: no tie is made or lost on the way. Infinities and NaNs stay such.
 __device__ __forceinline__ float round_odd(float hi, float lo) {
-  const float h = sum_of(hi, lo);
+  const float h = nearest(hi, lo);
   const float l = lo - (h - hi);  // exact: |lo| <= |hi|
   const uint32_t hb = __float_as_uint(h), lb = __float_as_uint(l);
   const uint32_t some = min(lb << 1, 1u);                     // l is not zero
@@ -233,8 +239,11 @@ __device__ __forceinline__ RawChunk<BF16> raw_of(const float (&v)[8]) {
 
 // FMT: 0 no codes, 1 E2M1, 2 E4M3, 3 E5M2. T threads hold a row, V chunks of 8 values each. A
 // workgroup walks over rows with the weights in registers, the next row's values on the way while
-// one is normalised (for up to 2 chunks a thread). Loads past the row or the last row repeat valid places instead of branching:
-// a wait behind a branch would have to count on none of the loads and stores in it.
+// one is normalised (for up to 2 chunks a thread). Loads past the row or the last row repeat valid
+// places instead of branching: a wait behind a branch would have to count on none of the loads and
+// stores in it.
+// Bound by HBM: 16384 x 8192 bf16 with residual, y and E4M3 codes 210 us (5.8 TB/s of 9 bytes an
+// element), 8192 x 4096 58 us; rows of 128 by the vector ALU (26 us for 262144, 3.9 TB/s).
 template <bool BF16, int T, int V, int FMT, bool SR, bool RES>
 __global__ __launch_bounds__(T > 256 ? T : 256) void rmsnorm_kernel(const NormArgs a) {
   constexpr int kThreads = T > 256 ? T : 256;
@@ -290,14 +299,20 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void rmsnorm_kernel(const NormAr
     if constexpr (kAhead) load_row(row + stride);
     ss = row_sum<T>(ss, red[par]);
     const double rho = inv_sqrt(fma(ss, a.inv_cols, (double)a.eps));
-    const float rho_hi = (float)rho, rho_lo = (float)(rho - (double)rho_hi);
     if (!live) continue;
-    if (a.rstd && t == 0) a.rstd[row] = rho_hi;
+    if (a.rstd && t == 0) a.rstd[row] = (float)rho;
+    // rows of extreme size: 2^64 moves from one factor of s rho to the other
+    const double scale = rho < 0x1p-90 ? 0x1p64 : rho > 0x1p90 ? 0x1p-64 : 1.0;
+    const float rho_hi = (float)(rho * scale), rho_lo = (float)(rho * scale - (double)rho_hi);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (t + v * T >= nch) continue;  // whole quads: cols is a multiple of 32
       float w[8], hi[8], lo[8];
       values<BF16>(s[v], w);
+      if (scale != 1.0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] *= (float)(1.0 / scale);
+      }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         product(w[k], rho_hi, rho_lo, g[v][k], hi[k], lo[k]);
@@ -308,7 +323,7 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void rmsnorm_kernel(const NormAr
         for (int k = 0; k < 8; ++k) w[k] = round_odd(hi[k], lo[k]);
       } else if constexpr (BF16 || FMT != 0) {
         // The nearest fp32 value serves as well, unless it is a tie of the next rounding (or a
-        // power of two that the block maximum may only just miss, or an infinity): with 8
+        // power of two that the block maximum may only just miss, or an infinity's NaN): with 8
         // significant bits at most, those have 15 zero bits at the end. One chunk in 4096.
         uint32_t low = __float_as_uint(w[0]) << 17;
 #pragma unroll
@@ -321,7 +336,7 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void rmsnorm_kernel(const NormAr
       if (a.y) {
         float o[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = BF16 ? w[k] : sum_of(hi[k], lo[k]);
+        for (int k = 0; k < 8; ++k) o[k] = BF16 ? w[k] : nearest(hi[k], lo[k]);
         store_raw<BF16>(a.y, row * a.ldy + col[v], raw_of<BF16>(o));
       }
       if constexpr (FMT != 0) {
@@ -409,6 +424,8 @@ hipError_t pick_norm_format(const NormArgs& a) {
 // A workgroup walks over rows like the forward kernel and keeps its columns' sums of dy z in
 // registers; rmsnorm_dgamma_kernel joins the workgroups' sums, partial[block][cols], in a fixed
 // order. Two rows and more a workgroup halve what it has to read.
+// Bound by HBM: 16384 x 8192 bf16 with dsum 194 us (5.5 TB/s of 8 bytes an element), 8192 x 4096 53
+// us, the join 4-6 us of either.
 template <bool BF16, int T>
 constexpr int kBackwardThreads = T <= 64 ? 256 : T <= 256 || (BF16 && T <= 512) ? 2 * T : T;
 

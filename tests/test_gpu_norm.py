@@ -50,7 +50,8 @@ def check_rounded(got: torch.Tensor, exact: np.ndarray, slack=2.0 ** -40):
     if got.dtype == torch.bfloat16:
         lo, hi = bf16_round_f64(lo), bf16_round_f64(hi)
     else:
-        lo, hi = lo.astype(np.float32), hi.astype(np.float32)
+        with np.errstate(over="ignore"):
+            lo, hi = lo.astype(np.float32), hi.astype(np.float32)
     v = got.detach().float().cpu().numpy()
     same_nan = np.isnan(v) == np.isnan(exact)
     assert same_nan.all(), np.argwhere(~same_nan)[:4].tolist()
@@ -164,6 +165,36 @@ def test_special_rows(mx, orc, dtype):
         assert_bytes_equal(sc, rs, "scales")
         assert_bytes_equal(c, rc, "codes")
     assert (host(sc)[0] == 0).all() and (host(sc)[4] == 0xFF).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_extreme_rows_and_weights(mx, orc, dtype):
+    """y past the types' ranges is infinite (fp32 and bf16 apart from one another), rows near the
+    largest and, with eps = 0, the smallest numbers are normalised like others."""
+    x, _, g = make(8, 256, dtype, False)
+    x = x.clamp(-20.0, 20.0)
+    g[3], g[40], g[100] = 3.0e38, -3.0e38, 3.0e-38
+    x[1] = (x[1].float() * 1e37).to(x.dtype)
+    x[2] = (x[2].float() * 1e-37).to(x.dtype)  # subnormals among them
+    x[3] = (x[3].float() * 1e-30).to(x.dtype)
+    for eps in (0.0, EPS):
+        for fmt in ("fp4", "e4m3", "e5m2"):
+            c, sc, y, s, rstd = quant(mx, fmt, dev(x), dev(g), eps=eps, with_y=True)
+            torch.cuda.synchronize()
+            exact, rho = ref.norm_f64(x, g, eps)
+            rho32 = rho.astype(np.float32)
+            assert np.allclose(rstd.cpu().numpy(), rho32, rtol=2.0 ** -23, atol=2.0 ** -149)
+            # weights below fp32's normal range leave errors that fp32 cannot hold
+            big = np.abs(exact) > 2.0 ** -100
+            check_rounded(torch.where(torch.from_numpy(big), y.cpu(), torch.zeros_like(y.cpu())),
+                          np.where(big, exact, 0.0))
+            assert torch.isinf(y[:, 3][y[:, 3].abs() > 3.4e38]).all()
+            rc, rs = oracle_codes(orc, fmt, exact, 0, 0)
+            assert_bytes_equal(sc, rs, "scales")
+            blocks = [b for b in range(8) if b != 3]  # block 3 holds the tiny weight
+            width = c.shape[1] // 8
+            got, want = host(c).reshape(8, 8, width), rc.reshape(8, 8, width)
+            assert np.array_equal(got[:, blocks], want[:, blocks])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
