@@ -98,8 +98,12 @@ def _operand(q, s, g: int, name: str, k_bytes_per_elem: float = 0.5):
     on a CUDA device; returns (rows, K)."""
     if not isinstance(q, torch.Tensor) or q.dim() != 2 or not q.is_cuda:
         raise ValueError(f"{name} codes must be a 2-D CUDA tensor")
-    rows = q.shape[0]
-    K = int(round(q.shape[1] / k_bytes_per_elem))
+    rows, width = q.shape
+    if (k_bytes_per_elem == 0.5 and g == 1 and q.dtype is torch.uint8 and q.is_contiguous()
+            and isinstance(s, torch.Tensor) and s.dtype is torch.uint8
+            and s.shape == (rows, width // 16) and s.device == q.device and s.is_contiguous()):
+        return rows, 2 * width  # what nearly every call has; the rest finds out what is wrong
+    K = int(round(width / k_bytes_per_elem))
     _buf(q, f"{name} codes", tuple(q.shape), _U8, q.device)
     if int(g) not in (1, 32, 64) or rows % int(g):
         raise ValueError(f"{name} scale granularity {g} does not divide its {rows} rows")

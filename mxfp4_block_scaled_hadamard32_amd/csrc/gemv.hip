@@ -784,17 +784,29 @@ constexpr int shared_tiles(int64_t T, int nt) {
   return T > 32 && nt == 1 ? 4 : T > 16 && nt <= 2 ? 2 : 1;
 }
 
-// Parts of K for gemv_shared_kernel (several want a workspace), 0 where it is not taken. It pays once the codes take longer
-// than its second kernel, and with few tokens once K is long: 16 bf16 tokens, N 8192, K 28672: 31.8
-// us, 48.4 directly; N 14336, K 4096: 13.7 and 11.5; 64 tokens, N 28672, K 8192: 51.6 and 90.6; 16
-// rotated tokens, N 28672, K 8192: 37.6 and 50.9. One workgroup a compute unit (its 8 waves keep
-// 64 KB on the way; two were slower: 42.7 us for the last), at least two chunks a part.
+// Its rows a workgroup: 128 where that leaves few workgroups before K is cut (16 fp32 tokens, N 4096,
+// K 16384: 18.5 us in 8 parts, 19.2 with 256 rows in 16), else 256.
+int64_t shared_groups(int64_t T, int64_t N, int nt, int rows) {
+  const int64_t tiles = 16 * shared_tiles(T, nt);
+  return (N + rows - 1) / rows * ((T + tiles - 1) / tiles);
+}
+bool shared_half(int64_t T, int64_t N, int nt) { return shared_groups(T, N, nt, 128) <= 40; }
+
+// Parts of K for gemv_shared_kernel (several want a workspace), 0 where it is not taken. It pays
+// where K is long, since it is cut: 16 tokens, N 1003, K 16384: 12.2 us, 24.2 directly (fp32 13.9
+// and 37.6; K 4128: 5.95 directly), and where there are many codes for several tokens: 16 rotated
+// tokens, N 28672, K 8192: 37.4 and 50.9; 64 tokens: 51.6 and 90.6; 16 tokens, N 14336, K 4096: 13.4
+// and 11.5. One workgroup a compute unit (its 8 waves keep 64 KB on the way; two were slower: 42.7
+// us for the rotated case), at least two chunks a part.
 int shared_parts(int64_t T, int64_t N, int64_t K, int nt) {
   const int64_t chunks = K / 512;
-  if (T == 1 || N * K < (1 << 25) || chunks < 2) return 0;
-  if (nt == 1 && T <= 16 && K < 8192) return 0;
-  const int64_t tiles = 16 * shared_tiles(T, nt);
-  const int64_t groups = (N + 255) / 256 * ((T + tiles - 1) / tiles);
+  if (T == 1 || chunks < 2) return 0;
+  const bool big = N * K >= (1 << 25);
+  const bool take = nt > 1     ? big || K >= 8192
+                    : T <= 16 ? (big && K >= 8192) || K >= 12288
+                              : big || K >= 12288;
+  if (!take) return 0;
+  const int64_t groups = shared_groups(T, N, nt, shared_half(T, N, nt) ? 128 : 256);
   const int64_t parts = 256 / groups < chunks / 2 ? 256 / groups : chunks / 2;
   return parts > 1 ? (int)parts : 1;
 }
@@ -825,11 +837,17 @@ hipError_t pick_gemv(const GemvArgs& a) {
   if (parts == 1 || (parts > 1 && a.part)) {
     constexpr int kMost = NT == 1 ? 4 : NT == 2 ? 2 : 1;
     const int tiles = shared_tiles(a.T, NT);
+    const bool half = shared_half(a.T, a.N, NT);
     if constexpr (kMost >= 4)
-      if (tiles == 4) return launch_shared<BF16, HAD, NT, 4, 2>(a, a.part, parts);
+      if (tiles == 4)
+        return half ? launch_shared<BF16, HAD, NT, 4, 1>(a, a.part, parts)
+                    : launch_shared<BF16, HAD, NT, 4, 2>(a, a.part, parts);
     if constexpr (kMost >= 2)
-      if (tiles == 2) return launch_shared<BF16, HAD, NT, 2, 2>(a, a.part, parts);
-    return launch_shared<BF16, HAD, NT, 1, 2>(a, a.part, parts);
+      if (tiles == 2)
+        return half ? launch_shared<BF16, HAD, NT, 2, 1>(a, a.part, parts)
+                    : launch_shared<BF16, HAD, NT, 2, 2>(a, a.part, parts);
+    return half ? launch_shared<BF16, HAD, NT, 1, 1>(a, a.part, parts)
+                : launch_shared<BF16, HAD, NT, 1, 2>(a, a.part, parts);
   }
   if (a.N >= 16 * 4 * kWorkgroups) {
     if constexpr (NT == 1) {

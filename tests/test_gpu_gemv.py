@@ -68,7 +68,9 @@ def up(*arrays):
                                    # products that take a workspace: one and several parts of K,
                                    # a part of a chunk left over, rows and tokens past the end
                                    (2, 4099, 8224), (16, 4096, 8192), (23, 8200, 4128),
-                                   (64, 4100, 8256), (33, 33000, 1056), (70, 5000, 8192)])
+                                   (64, 4100, 8256), (33, 33000, 1056), (70, 5000, 8192),
+                                   (5, 300, 16416), (20, 1003, 12320), (40, 17, 16384),
+                                   (130, 5000, 12832), (2, 1, 65536)])
 def test_against_float64(mx, orc, T, N, K, dtype):
     x = tokens(T, K, dtype)
     wq, ws = weights(N, K)
@@ -82,7 +84,8 @@ def test_against_float64(mx, orc, T, N, K, dtype):
 @pytest.mark.parametrize("T,N,K", [(1, 40, 4096), (7, 300, 1056), (16, 5000, 256), (35, 64, 512),
                                    (64, 200, 160), (2, 14000, 96),
                                    (1, 13000, 8192), (1, 100, 65536), (20, 13000, 608),
-                                   (16, 4100, 8224), (40, 8200, 4128)])
+                                   (16, 4100, 8224), (40, 8200, 4128), (3, 33, 8224),
+                                   (37, 500, 16416)])
 def test_rotated_weights(mx, orc, T, N, K, dtype):
     """Weights as mx_quantize makes them with the signed transform; fp32's five stages on x."""
     w = wl.normal((N, K), 0.02, seed=4).to(torch.bfloat16)
@@ -106,7 +109,9 @@ def test_rotated_weights(mx, orc, T, N, K, dtype):
 
 
 @pytest.mark.parametrize("g", [32, 64])
-@pytest.mark.parametrize("T,N,K", [(1, 192, 256), (20, 4096, 320), (20, 8192, 4096)])
+@pytest.mark.parametrize("T,N,K", [(1, 192, 256), (20, 4096, 320), (20, 8192, 4096),
+                                   (1, 6464, 4640), (1, 9664, 320), (1, 16448, 544),
+                                   (9, 12864, 320), (3, 6464, 96), (4, 320, 12832)])
 def test_tile_scales(mx, orc, g, T, N, K):
     x = tokens(T, K, "bf16")
     wq, ws = weights(N, K, g)
