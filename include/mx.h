@@ -330,9 +330,10 @@ mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, in
  * Accuracy: fp32 accumulation. The products are exact, sums of 128 of them are formed by the
  * matrix core, which drops what lies below 2^-24 of a sum's largest term, and joined in fp32:
  * |y - exact| <= (160 + K / 128) * 2^-24 * sum_k |x'_k W_k| before the rounding to bf16. bf16
- * tokens that are rotated for a bf16 y keep 16 bits of each x' (another 2^-17 of the sum). A weight
- * beyond bf16's range, 2^128 or more (scale bytes 253 and 254), counts as infinity; scale byte
- * 255 is NaN.
+ * tokens that are rotated for a bf16 y keep 16 bits of each x' (another 2^-17 of the sum), and of
+ * fp32 or rotated values what lies below bf16's least subnormal, 2^-133, is rounded away. A weight
+ * beyond bf16's range, 2^128 or more (scale bytes 253 and 254), counts as infinity: with fp32 or
+ * rotated tokens, or zeros in x, its output may be NaN. Scale byte 255 is NaN.
  * Errors (nothing is launched): MX_ERR_SHAPE, MX_ERR_ARG (types, granularity, hadamard, alpha_exp
  * outside [-126, 127], alignment, a workspace that is too small), MX_ERR_NULL, MX_ERR_LAUNCH (N
  * above 2^26 or T above 2^19 rows). T == 0 or N == 0 is a no-op; K == 0 writes zeros. */

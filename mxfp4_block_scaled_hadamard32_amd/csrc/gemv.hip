@@ -779,25 +779,33 @@ hipError_t launch_shared(const GemvArgs& a, float* part, int splits) {
 // N 4096 7.2 us with 1 tile (256 workgroups), 8.5 with 2.
 constexpr int64_t kWorkgroups = 200;
 
-// Token tiles of gemv_shared_kernel: two chunks of NT terms take 32 KB of LDS a tile.
+// Token tiles of gemv_shared_kernel: two chunks of NT terms take 32 KB of LDS a tile. Four tiles
+// convert the codes once for 64 tokens (N 28672, K 8192: 43.6 us, 50.4 with two).
 constexpr int shared_tiles(int64_t T, int nt) {
   return T > 32 && nt == 1 ? 4 : T > 16 && nt <= 2 ? 2 : 1;
 }
 
 // Its rows a workgroup: 128 where that leaves few workgroups before K is cut (16 fp32 tokens, N 4096,
-// K 16384: 18.5 us in 8 parts, 19.2 with 256 rows in 16), else 256.
+// K 16384: 18.5 us in 8 parts, 19.2 with 256 rows in 16), else 256 (16 bf16 tokens, N 28672, K 8192:
+// 32.7 us in 2 parts, 35.0 with 128 rows in one). With four token tiles a part's sums are four times
+// as long and 128 rows are better as long as one round of workgroups takes them all (64 tokens, N
+// 28672, K 8192: 43.6 us, 51.1 with 256 rows in 2 parts; N 8192, K 28672: 43.9 in 4 parts and 48.0;
+// N 40960, K 4096, 320 workgroups: 45.2 and 42.6).
 int64_t shared_groups(int64_t T, int64_t N, int nt, int rows) {
   const int64_t tiles = 16 * shared_tiles(T, nt);
   return (N + rows - 1) / rows * ((T + tiles - 1) / tiles);
 }
-bool shared_half(int64_t T, int64_t N, int nt) { return shared_groups(T, N, nt, 128) <= 40; }
+bool shared_half(int64_t T, int64_t N, int nt) {
+  return shared_groups(T, N, nt, 128) <= (shared_tiles(T, nt) == 4 ? 256 : 40);
+}
 
 // Parts of K for gemv_shared_kernel (several want a workspace), 0 where it is not taken. It pays
 // where K is long, since it is cut: 16 tokens, N 1003, K 16384: 12.2 us, 24.2 directly (fp32 13.9
 // and 37.6; K 4128: 5.95 directly), and where there are many codes for several tokens: 16 rotated
-// tokens, N 28672, K 8192: 37.4 and 50.9; 64 tokens: 51.6 and 90.6; 16 tokens, N 14336, K 4096: 13.4
+// tokens, N 28672, K 8192: 37.4 and 50.9; 64 tokens: 43.6 and 90.2; 16 tokens, N 14336, K 4096: 13.4
 // and 11.5. One workgroup a compute unit (its 8 waves keep 64 KB on the way; two were slower: 42.7
-// us for the rotated case), at least two chunks a part.
+// us for the rotated case), at least two chunks a part. Workgroups of 7 waves (28672 rows in 256 of them: 43.6 us for the rotated case) or
+// 16 (40.4) were no better.
 int shared_parts(int64_t T, int64_t N, int64_t K, int nt) {
   const int64_t chunks = K / 512;
   if (T == 1 || chunks < 2) return 0;

@@ -70,7 +70,7 @@ def up(*arrays):
                                    (2, 4099, 8224), (16, 4096, 8192), (23, 8200, 4128),
                                    (64, 4100, 8256), (33, 33000, 1056), (70, 5000, 8192),
                                    (5, 300, 16416), (20, 1003, 12320), (40, 17, 16384),
-                                   (130, 5000, 12832), (2, 1, 65536)])
+                                   (130, 5000, 12832), (2, 1, 65536), (50, 20003, 1696)])
 def test_against_float64(mx, orc, T, N, K, dtype):
     x = tokens(T, K, dtype)
     wq, ws = weights(N, K)
