@@ -28,6 +28,7 @@ from __future__ import annotations
 from dataclasses import dataclass, field
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (MX_E4M3, MX_E5M2, MX_ROUND_RNE, MX_SCALE_FLOOR, mx_gemm_dgrad, mx_gemm_fprop,
                mx_gemm_mxfp8, mx_gemm_wgrad, mx_gemv, mx_quantize, mx_quantize_2d_blocks,
@@ -237,6 +238,7 @@ class MXRMSNormFunction(torch.autograd.Function):
         return y, (None if residual is None else s), codes, scales
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, ds, _codes, _scales):
         s, gamma, rstd = ctx.saved_tensors
         need_x, need_r, need_g = ctx.needs_input_grad[:3]
@@ -250,8 +252,10 @@ class MXRMSNormFunction(torch.autograd.Function):
 
 
 def _rows_of(grad: torch.Tensor, like: torch.Tensor) -> torch.Tensor:
-    """A gradient in the layout and type that the kernels read (an expanded one has no rows)."""
-    return grad.to(like.dtype).contiguous()
+    """A gradient in the layout and type that the kernels read (an expanded one has no rows, a view
+    into a flat buffer may start anywhere)."""
+    grad = grad.to(like.dtype).contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
 
 
 def _flat(t: torch.Tensor | None):

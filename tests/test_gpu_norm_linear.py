@@ -140,6 +140,26 @@ def test_norm_module_shapes_and_gradients(lin):
     assert x.grad is not None and norm.weight.grad is None
 
 
+def test_norm_gradient_views_and_second_order(lin):
+    """Gradients that are views into a flat buffer at any element; a second derivative is refused."""
+    K = 96
+    norm = lin.MXRMSNorm(K)
+    x = wl.student_t3((10, K), seed=5).to(DEV).requires_grad_(True)
+    r = wl.student_t3((10, K), seed=6).to(DEV).requires_grad_(True)
+    y, s = norm(x, r)
+    flat = wl.normal((10 * K + 1, 2), 1.0, seed=7).to(DEV).t().contiguous()
+    dy, ds = (f[1:].view(10, K) for f in flat)
+    assert dy.data_ptr() % 16 and ds.data_ptr() % 16
+    got = torch.autograd.grad((y, s), (x, r, norm.weight), (dy, ds), retain_graph=True)
+    want = torch.autograd.grad((y, s), (x, r, norm.weight), (dy.clone(), ds.clone()),
+                               retain_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    dy = dy.clone().requires_grad_(True)
+    dx, = torch.autograd.grad(y, x, dy, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.sum().backward()
+
+
 def test_training_step_in_a_graph(lin):
     """Forward and backward of the half-layer captured once and replayed on new inputs; no eager
     graph of the same leaves is alive meanwhile."""
