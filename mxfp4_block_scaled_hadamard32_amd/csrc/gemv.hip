@@ -182,7 +182,7 @@ __device__ __forceinline__ void store_y(const GemvArgs& a, int64_t at, float v) 
 // bytes between the scale rows of a segment of `seg` blocks in LDS
 __host__ __device__ constexpr int scale_pitch(int seg) { return (seg + 15) / 16 * 16 + 4; }
 
-// Up to 16 tokens whose activations fit in LDS: RT tiles of 16 weight rows a workgroup of WV waves,
+// One token, or a few whose activations fit in LDS: RT tiles of 16 weight rows a workgroup of WV waves,
 // which take turns at groups of 16 blocks of K (4 steps: 256 contiguous code bytes a row). The
 // workgroup first brings the activations (rotated and split there, once) and its rows' scale bytes
 // into LDS, so the loop's only requests to memory are the codes: a step's registers are loaded
@@ -342,19 +342,18 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(const GemvArgs a, int seg
   }
 }
 
-// More activations than LDS holds: MT tiles of 16 tokens by RT tiles of 16 weight rows a workgroup
-// of WV waves, which take turns at groups of 16 blocks of K (16 scale bytes a row) and read the
-// activations of their steps themselves. With one token tile, the registers of a step's codes and
-// activations are loaded with the same step of the wave's next group as soon as they have been
-// used, so 4 steps are always on the way; with more, a group's codes are requested together.
-template <bool BF16, bool HAD, int NT, int MT, int RT, int WV>
-__global__ __launch_bounds__(64 * WV) void gemv_direct_kernel(const GemvArgs a) {
-  constexpr bool RING = MT == 1;
-  __shared__ float red[WV][MT * RT * 4][64];
+// Few rows or a short K: 16 tokens by RT tiles of 16 weight rows a workgroup of 8 waves, which take
+// turns at groups of 16 blocks of K (16 scale bytes a row) and read the activations of their steps
+// themselves. The registers of a step's codes and activations are loaded with the same step of the
+// wave's next group as soon as they have been used, so 4 steps are always on the way.
+template <bool BF16, bool HAD, int NT, int RT>
+__global__ __launch_bounds__(512) void gemv_direct_kernel(const GemvArgs a) {
+  constexpr int WV = 8;
+  __shared__ float red[WV][RT * 4][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+  const int64_t m0 = (int64_t)blockIdx.y * 16;
   const int nb = (int)(a.K / 32);
   constexpr int kBlock = BF16 ? 64 : 128;  // bytes of a block of x
 
@@ -362,7 +361,6 @@ __global__ __launch_bounds__(64 * WV) void gemv_direct_kernel(const GemvArgs a) 
   // depends on a branch, which would make the waits for the loads after it count on none of them.
   const uint8_t* wrow[RT];
   const uint8_t* srow[RT];
-  const uint8_t* xrow[MT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     int64_t n = n0 + 16 * r + i16;
@@ -370,17 +368,12 @@ __global__ __launch_bounds__(64 * WV) void gemv_direct_kernel(const GemvArgs a) 
     wrow[r] = a.w + n * (a.K / 2) + 16 * g;
     srow[r] = a.ws + n / a.gw * nb;
   }
+  const int64_t t16 = m0 + i16 < a.T ? m0 + i16 : a.T - 1;
+  const uint8_t* const xrow =
+      reinterpret_cast<const uint8_t*>(a.x) + t16 * a.ldx * (BF16 ? 2 : 4) + g * kBlock;
+  f32x4 acc[RT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    int64_t t = m0 + 16 * m + i16;
-    t = t < a.T ? t : a.T - 1;
-    xrow[m] = reinterpret_cast<const uint8_t*>(a.x) + t * a.ldx * (BF16 ? 2 : 4) + g * kBlock;
-  }
-  f32x4 acc[MT][RT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) acc[m][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   auto load_codes = [&](u32x4 (&q)[RT], int grp, int d) {
 #pragma unroll
@@ -391,7 +384,7 @@ __global__ __launch_bounds__(64 * WV) void gemv_direct_kernel(const GemvArgs a) 
 #pragma unroll
     for (int r = 0; r < RT; ++r) sc[r] = load16_any(srow[r] + 16 * grp);
   };
-  auto multiply = [&](const bf16x8_t (&w)[RT][4], const RawX<BF16>& x, int m) {
+  auto multiply = [&](const bf16x8_t (&w)[RT][4], const RawX<BF16>& x) {
     u32x4 f[NT][4];
     terms_of<BF16, HAD, NT>(x, a.sign_mask, f);
     f32x4 p[RT];  // a step's products apart from the running sum, as in gemv_kernel
@@ -406,60 +399,42 @@ __global__ __launch_bounds__(64 * WV) void gemv_direct_kernel(const GemvArgs a) 
           p[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f[s][j]),
                                                          w[r][j], p[r], 0, 0, 0);
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[m][r] += p[r];
+    for (int r = 0; r < RT; ++r) acc[r] += p[r];
   };
 
   const int ng = nb / 16;
   if (wave < ng) {
     u32x4 q[4][RT], sc[RT];
-    RawX<BF16> x[RING ? 4 : 1];
+    RawX<BF16> x[4];
     int grp = wave;
-    if constexpr (RING) {  // in the order of the loop, which the waits in it count on
-      load_scales(sc, grp);
+    // in the order of the loop, which the waits in it count on
+    load_scales(sc, grp);
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        load_codes(q[d], grp, d);
-        load_x<BF16>(x[d], xrow[0] + (int64_t)(16 * grp + 4 * d) * kBlock);
-      }
+    for (int d = 0; d < 4; ++d) {
+      load_codes(q[d], grp, d);
+      load_x<BF16>(x[d], xrow + (int64_t)(16 * grp + 4 * d) * kBlock);
     }
     auto group = [&](auto more) {
       u32x4 scn[RT];
       const int next = grp + WV;  // used if there is one
-      if constexpr (RING && more()) load_scales(scn, next);
-      if constexpr (!RING) {
-        load_scales(sc, grp);
-#pragma unroll
-        for (int d = 0; d < 4; ++d) load_codes(q[d], grp, d);
-      }
+      if constexpr (more()) load_scales(scn, next);
 #pragma unroll
       for (int d = 0; d < 4; ++d) {
         bf16x8_t w[RT][4];
 #pragma unroll
         for (int r = 0; r < RT; ++r) weights_of(q[d][r], (sc[r][d] >> (8 * g)) & 0xFFu, w[r]);
-        if constexpr (RING) {
-          if constexpr (more()) load_codes(q[d], next, d);
-          multiply(w, x[d], 0);
-          if constexpr (more()) load_x<BF16>(x[d], xrow[0] + (int64_t)(16 * next + 4 * d) * kBlock);
-        } else {
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            load_x<BF16>(x[0], xrow[m] + (int64_t)(16 * grp + 4 * d) * kBlock);
-            multiply(w, x[0], m);
-          }
-        }
+        if constexpr (more()) load_codes(q[d], next, d);
+        multiply(w, x[d]);
+        if constexpr (more()) load_x<BF16>(x[d], xrow + (int64_t)(16 * next + 4 * d) * kBlock);
       }
-      if constexpr (RING && more()) {
+      if constexpr (more()) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) sc[r] = scn[r];
       }
       grp = next;
     };
-    if constexpr (RING) {
-      while (grp + WV < ng) group(std::true_type{});
-      group(std::false_type{});
-    } else {
-      while (grp < ng) group(std::true_type{});
-    }
+    while (grp + WV < ng) group(std::true_type{});
+    group(std::false_type{});
   }
   for (int b0 = 16 * ng; b0 < nb; b0 += 4) {
     if ((b0 / 4 + ng) % WV != wave) continue;
@@ -475,28 +450,23 @@ __global__ __launch_bounds__(64 * WV) void gemv_direct_kernel(const GemvArgs a) 
       }
       weights_of(q, sb, w[r]);
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      RawX<BF16> x = {};
-      if (in) load_x<BF16>(x, xrow[m] + (int64_t)b0 * kBlock);
-      multiply(w, x, m);
-    }
+    RawX<BF16> x = {};
+    if (in) load_x<BF16>(x, xrow + (int64_t)b0 * kBlock);
+    multiply(w, x);
   }
 
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) red[wave][(m * RT + r) * 4 + i][lane] = acc[m][r][i];
+    for (int i = 0; i < 4; ++i) red[wave][r * 4 + i][lane] = acc[r][i];
   __syncthreads();
-  for (int e = threadIdx.x; e < MT * RT * 4 * 64; e += 64 * WV) {
+  for (int e = threadIdx.x; e < RT * 4 * 64; e += 64 * WV) {
     const int slot = e >> 6, l = e & 63;
     float v = red[0][slot][l];
 #pragma unroll
     for (int s = 1; s < WV; ++s) v += red[s][slot][l];
-    const int i = slot & 3, r = (slot >> 2) % RT, m = (slot >> 2) / RT;
-    const int64_t t = m0 + 16 * m + 4 * (l >> 4) + i, n = n0 + 16 * r + (l & 15);
+    const int i = slot & 3, r = slot >> 2;
+    const int64_t t = m0 + 4 * (l >> 4) + i, n = n0 + 16 * r + (l & 15);
     if (t < a.T && n < a.N) store_y(a, t * a.ldy + n, v);
   }
 }
@@ -721,12 +691,12 @@ __global__ __launch_bounds__(256) void gemv_zero_kernel(const GemvArgs a) {
   }
 }
 
-template <bool BF16, bool HAD, int NT, int MT, int RT, int WV>
+template <bool BF16, bool HAD, int NT, int RT>
 hipError_t launch_direct(const GemvArgs& a) {
-  const int64_t gx = (a.N + 16 * RT - 1) / (16 * RT), gy = (a.T + 16 * MT - 1) / (16 * MT);
+  const int64_t gx = (a.N + 16 * RT - 1) / (16 * RT), gy = (a.T + 15) / 16;
   if (gx > (1 << 22) || gy > 32768) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemv_direct_kernel<BF16, HAD, NT, MT, RT, WV>), dim3((unsigned)gx, (unsigned)gy),
-                     dim3(64 * WV), 0, (hipStream_t)a.stream, a);
+  hipLaunchKernelGGL((gemv_direct_kernel<BF16, HAD, NT, RT>), dim3((unsigned)gx, (unsigned)gy),
+                     dim3(512), 0, (hipStream_t)a.stream, a);
   return hipGetLastError();
 }
 
@@ -752,7 +722,7 @@ hipError_t launch_gemv(const GemvArgs& a, int bytes) {
                        use > join ? use : join, (hipStream_t)a.stream, a, seg);
     return hipGetLastError();
   }
-  if constexpr (NT > 1)  // takes_lds
+  if constexpr (NT > 1 && RT == 1 && WV == 8)  // takes_lds
     hipLaunchKernelGGL((gemv_kernel<BF16, HAD, NT, RT, WV, false>), grid, block,
                        use > join ? use : join, (hipStream_t)a.stream, a, seg);
   return hipGetLastError();
@@ -773,65 +743,94 @@ hipError_t launch_shared(const GemvArgs& a, float* part, int splits) {
   return hipGetLastError();
 }
 
-// Rows a workgroup takes (RT tiles of 16) so that about one workgroup a compute unit is left: more
-// rows share a fetch (and, in gemv_direct_kernel, a split) of the activations, fewer leave compute
-// units idle. 16 tokens, bf16, K 4096: N 14336 11.5 us with 4 tiles (224 workgroups), 16.4 with 2;
-// N 4096 7.2 us with 1 tile (256 workgroups), 8.5 with 2.
-constexpr int64_t kWorkgroups = 200;
-
-// Token tiles of gemv_shared_kernel: two chunks of NT terms take 32 KB of LDS a tile. Four tiles
-// convert the codes once for 64 tokens (N 28672, K 8192: 43.6 us, 50.4 with two).
-constexpr int shared_tiles(int64_t T, int nt) {
-  return T > 32 && nt == 1 ? 4 : T > 16 && nt <= 2 ? 2 : 1;
-}
-
-// Its rows a workgroup: 128 where that leaves few workgroups before K is cut (16 fp32 tokens, N 4096,
-// K 16384: 18.5 us in 8 parts, 19.2 with 256 rows in 16), else 256 (16 bf16 tokens, N 28672, K 8192:
-// 32.7 us in 2 parts, 35.0 with 128 rows in one). With four token tiles a part's sums are four times
-// as long and 128 rows are better as long as one round of workgroups takes them all (64 tokens, N
-// 28672, K 8192: 43.6 us, 51.1 with 256 rows in 2 parts; N 8192, K 28672: 43.9 in 4 parts and 48.0;
-// N 40960, K 4096, 320 workgroups: 45.2 and 42.6).
-int64_t shared_groups(int64_t T, int64_t N, int nt, int rows) {
-  const int64_t tiles = 16 * shared_tiles(T, nt);
-  return (N + rows - 1) / rows * ((T + tiles - 1) / tiles);
-}
-bool shared_half(int64_t T, int64_t N, int nt) {
-  return shared_groups(T, N, nt, 128) <= (shared_tiles(T, nt) == 4 ? 256 : 40);
-}
-
-// Parts of K for gemv_shared_kernel (several want a workspace), 0 where it is not taken. It pays
-// where K is long, since it is cut: 16 tokens, N 1003, K 16384: 12.2 us, 24.2 directly (fp32 13.9
-// and 37.6; K 4128: 5.95 directly), and where there are many codes for several tokens: 16 rotated
-// tokens, N 28672, K 8192: 37.4 and 50.9; 64 tokens: 43.6 and 90.2; 16 tokens, N 14336, K 4096: 13.4
-// and 11.5. One workgroup a compute unit (its 8 waves keep 64 KB on the way; two were slower: 42.7
-// us for the rotated case), at least two chunks a part. Workgroups of 7 waves (28672 rows in 256 of them: 43.6 us for the rotated case) or
-// 16 (40.4) were no better.
-int shared_parts(int64_t T, int64_t N, int64_t K, int nt) {
-  const int64_t chunks = K / 512;
-  if (T == 1 || chunks < 2) return 0;
-  const bool big = N * K >= (1 << 25);
-  const bool take = nt > 1     ? big || K >= 8192
-                    : T <= 16 ? (big && K >= 8192) || K >= 12288
-                              : big || K >= 12288;
-  if (!take) return 0;
-  const int64_t groups = shared_groups(T, N, nt, shared_half(T, N, nt) ? 128 : 256);
-  const int64_t parts = 256 / groups < chunks / 2 ? 256 / groups : chunks / 2;
-  return parts > 1 ? (int)parts : 1;
-}
-
 constexpr int kLds = 128 * 1024;
+constexpr int64_t kWorkgroups = 200;  // about one a compute unit
 
-// Activations of all tokens through LDS in one piece: always better when they have to be rotated or
-// split (one token, N 14336, K 4096: rotated 10.9 us, 14.2 read directly; fp32 11.9 and 14.8), and
-// for one bf16 token (K 28672: 26.9 and 30.1 us); for several bf16 tokens the direct kernel is the
-// faster one (4 tokens, N 14336, K 4096: 9.7 and 11.1 us).
-bool takes_lds(int64_t T, int64_t K, int nt) {
-  return T == 1 || (nt > 1 && T <= 16 && T * K * 2 * nt <= kLds);
+// All activations through LDS in one piece: for one token always (N 14336, K 4096: rotated 10.9 us,
+// 14.2 read directly; fp32 11.9 and 14.8; bf16, N 8192, K 28672: 26.9 and 30.1), and for very few
+// tokens that have to be rotated or split, few rows and a K that is not short, as long as two
+// workgroups a compute unit hold them (4 rotated tokens, N 4096, K 4128: 8.8 us, 10.7 with
+// gemv_shared_kernel; N 5120, K 512: 7.7 and 4.6; N 28672, K 1024: 15.5 and 7.5).
+bool takes_lds(int64_t T, int64_t N, int64_t K, int nt) {
+  return T == 1 || (nt > 1 && T * nt <= 8 && K >= 2048 && T * K * 2 * nt <= kLds / 2 &&
+                    N <= 16 * 256);
+}
+
+// How a product of several tokens is taken: by gemv_shared_kernel with `tiles` tiles of 16 tokens,
+// 128 `rt` rows a workgroup and K in `parts` parts (several want a workspace), or, with parts = 0, by
+// gemv_direct_kernel with `rt` tiles of 16 rows.
+struct Plan {
+  int tiles, rt, parts;
+};
+
+// The shapes differ in how many workgroups there are, how often activations are fetched and split and
+// codes converted, and in the join; which one is best changes with every size (16 bf16 tokens, K
+// 4096: N 4096 7.2 us directly, 9.0 shared; K 1024, N 28672: 9.5 and 6.7; K 8192: 48.4 and 32.7; N
+// 1003, K 16384: 24.2 and 12.2; 64 fp32 tokens, N 8192, K 2048: 23.1 and 12.6). So the time is
+// estimated, in us, from what a workgroup does one after the other (chunks of 512 of K, in rounds of
+// 256 workgroups), what the machine does in all (codes), the blocks after the last chunk, and the
+// join. The constants are fitted to 2550 sizes (2 to 100 tokens, N 64 to 40960, K 256 to 28672, all
+// types; every shape of either kernel timed): the choice is 1 to 4% from the best one on average and
+// 1.5 times at worst, where thresholds on N and K were at 11 to 13% and up to 6 times.
+// Workgroups of 7 or 16 waves for gemv_shared_kernel were no better (16 rotated tokens, N 28672, K
+// 8192: 43.6 and 40.4 us, 37.4 with 8), nor more parts than one workgroup a compute unit (42.7).
+double shared_time(int64_t T, int64_t N, int64_t K, int nt, int tiles, int rt, int64_t parts) {
+  const int64_t groups = (N + 128 * rt - 1) / (128 * rt) * ((T + 16 * tiles - 1) / (16 * tiles));
+  const int64_t wgs = groups * parts, len = (K / 512 + parts - 1) / parts, rounds = (wgs + 255) / 256;
+  const int64_t rest = (K % 512 + 127) / 128;  // steps
+  const double chunk = rt * (0.68 + 0.22 * tiles * nt) + tiles * (nt > 1 ? 0.28 + 0.17 * nt : 0.28);
+  const double after = rest ? 1.2 + rest * rt * (0.07 + 0.3 * tiles * nt) : 0.0;
+  const double join = parts > 1 ? 3.2 + 0.2e-6 * (double)(parts * T * N) : 0.0;
+  return 3.2 + rounds * (len * chunk + after) + 0.33 / 256 * rt * (double)(wgs * len) + join;
+}
+
+double direct_time(int64_t T, int64_t N, int64_t K, int nt, int rt) {
+  struct Cost {
+    double start, turn, turn_rt, x, all, all_rt, rest, rest_rt;
+  };
+  constexpr Cost kCost[3] = {{2.0, 0.12, 0.51, 3.15, 0.43, 1.22, 0.45, 0.26},
+                             {1.7, 2.72, 0.67, 2.87, 1.49, 0.61, 1.20, 0.44},
+                             {1.6, 1.63, 1.07, 5.26, 1.27, 0.80, 1.21, 0.39}};
+  const Cost& c = kCost[nt - 1];
+  const int64_t wgs = (N + 16 * rt - 1) / (16 * rt) * ((T + 15) / 16), rounds = (wgs + 255) / 256;
+  const int64_t chunks = K / 512, turns = (chunks + 7) / 8;  // of 8 waves
+  const double x = (double)chunks / 8 * c.x * (T < 16 ? (double)T / 16 : 1.0);
+  const double rest = K % 512 ? c.rest + c.rest_rt * rt : 0.0;
+  return c.start + rounds * (turns * (c.turn + c.turn_rt * rt) + x + rest) +
+         (double)(wgs * chunks) / 2048 * (c.all + c.all_rt * rt);
+}
+
+Plan plan_gemv(int64_t T, int64_t N, int64_t K, int nt, bool workspace) {
+  Plan best{1, 1, 0};
+  double least = direct_time(T, N, K, nt, 1);
+  auto offer = [&](double time, const Plan& p) {
+    if (time < least) {
+      least = time;
+      best = p;
+    }
+  };
+  for (int rt = 2; rt <= (nt == 1 ? 4 : 2); rt *= 2)
+    offer(direct_time(T, N, K, nt, rt), Plan{1, rt, 0});
+  const int64_t chunks = K / 512;
+  if (chunks < 1) return best;
+  // More than 8 parts have two chunks at least: 16 fp32 tokens, N 1003, K 16384: 13.9 us in 16, 16.0
+  // in 32; 37, K 4128: 10.8 in 8, 11.7 in 4.
+  const int64_t cut = chunks <= 8 ? chunks : chunks / 2 < 8 ? 8 : chunks / 2;
+  const int most_tiles = nt == 1 ? 4 : nt == 2 ? 2 : 1;  // two chunks of a tile: 32 KB of LDS a term
+  for (int tiles = 1; tiles <= most_tiles && (tiles == 1 || T > 8 * tiles); tiles *= 2)
+    for (int rt = 1; rt <= 2; ++rt) {
+      const int64_t groups = (N + 128 * rt - 1) / (128 * rt) * ((T + 16 * tiles - 1) / (16 * tiles));
+      const int64_t most = !workspace || groups > 128 ? 1 : 256 / groups < cut ? 256 / groups : cut;
+      for (int64_t s = 1; s < most; s *= 2)
+        offer(shared_time(T, N, K, nt, tiles, rt, s), Plan{tiles, rt, (int)s});
+      offer(shared_time(T, N, K, nt, tiles, rt, most), Plan{tiles, rt, (int)most});
+    }
+  return best;
 }
 
 template <bool BF16, bool HAD, int NT>
 hipError_t pick_gemv(const GemvArgs& a) {
-  if (takes_lds(a.T, a.K, NT)) {
+  if (takes_lds(a.T, a.N, a.K, NT)) {
     // Few workgroups need 8 waves each to keep enough codes coming (one bf16 token, N 8192, K 28672:
     // 26.8 us, 30.6 with 4 waves); with many, 4 waves and in the end one row tile do better (N
     // 14336, K 4096: 9.2 us with 2 tiles of 4 waves, 10.1 with 8; N 28672, K 8192: 30.2 us with 1
@@ -841,35 +840,22 @@ hipError_t pick_gemv(const GemvArgs& a) {
     if (a.N < 16 * 5 * kWorkgroups) return launch_gemv<BF16, HAD, NT, 2, 4>(a, kLds);
     return launch_gemv<BF16, HAD, NT, 1, 4>(a, kLds);
   }
-  const int parts = shared_parts(a.T, a.N, a.K, NT);
-  if (parts == 1 || (parts > 1 && a.part)) {
-    constexpr int kMost = NT == 1 ? 4 : NT == 2 ? 2 : 1;
-    const int tiles = shared_tiles(a.T, NT);
-    const bool half = shared_half(a.T, a.N, NT);
-    if constexpr (kMost >= 4)
-      if (tiles == 4)
-        return half ? launch_shared<BF16, HAD, NT, 4, 1>(a, a.part, parts)
-                    : launch_shared<BF16, HAD, NT, 4, 2>(a, a.part, parts);
-    if constexpr (kMost >= 2)
-      if (tiles == 2)
-        return half ? launch_shared<BF16, HAD, NT, 2, 1>(a, a.part, parts)
-                    : launch_shared<BF16, HAD, NT, 2, 2>(a, a.part, parts);
-    return half ? launch_shared<BF16, HAD, NT, 1, 1>(a, a.part, parts)
-                : launch_shared<BF16, HAD, NT, 1, 2>(a, a.part, parts);
+  const Plan p = plan_gemv(a.T, a.N, a.K, NT, a.part != nullptr);
+  if (p.parts == 0) {
+    if constexpr (NT == 1)
+      if (p.rt == 4) return launch_direct<BF16, HAD, NT, 4>(a);
+    return p.rt == 2 ? launch_direct<BF16, HAD, NT, 2>(a) : launch_direct<BF16, HAD, NT, 1>(a);
   }
-  if (a.N >= 16 * 4 * kWorkgroups) {
-    if constexpr (NT == 1) {
-      // more token tiles share a conversion of the codes: 64 tokens, N 28672, K 8192: 91 us with
-      // 4 tiles, 134 with 1; 32 tokens, N 14336, K 4096: 16.2 us with 2, 20.9 with 1
-      if (a.T > 32) return launch_direct<BF16, HAD, NT, 4, 4, 4>(a);
-      if (a.T > 16) return launch_direct<BF16, HAD, NT, 2, 4, 8>(a);
-      return launch_direct<BF16, HAD, NT, 1, 4, 8>(a);
-    } else {
-      return launch_direct<BF16, HAD, NT, 1, 4, 4>(a);  // 8 waves would spill
-    }
-  }
-  if (a.N >= 16 * 2 * kWorkgroups) return launch_direct<BF16, HAD, NT, 1, 2, 8>(a);
-  return launch_direct<BF16, HAD, NT, 1, 1, 8>(a);
+  if constexpr (NT == 1)
+    if (p.tiles == 4)
+      return p.rt == 2 ? launch_shared<BF16, HAD, NT, 4, 2>(a, a.part, p.parts)
+                       : launch_shared<BF16, HAD, NT, 4, 1>(a, a.part, p.parts);
+  if constexpr (NT <= 2)
+    if (p.tiles == 2)
+      return p.rt == 2 ? launch_shared<BF16, HAD, NT, 2, 2>(a, a.part, p.parts)
+                       : launch_shared<BF16, HAD, NT, 2, 1>(a, a.part, p.parts);
+  return p.rt == 2 ? launch_shared<BF16, HAD, NT, 1, 2>(a, a.part, p.parts)
+                   : launch_shared<BF16, HAD, NT, 1, 1>(a, a.part, p.parts);
 }
 
 // bf16 terms of an activation: fp32 values take 3; rotated bf16 ones 2 when y is bf16
@@ -882,8 +868,8 @@ int terms(bool bf16, bool hadamard, bool out_bf16) {
 int64_t mx_gemv_workspace_bytes(int64_t T, int64_t N, int64_t K, bool bf16, bool hadamard,
                                 bool out_bf16) {
   const int nt = terms(bf16, hadamard, out_bf16);
-  if (takes_lds(T, K, nt)) return 0;
-  const int64_t parts = shared_parts(T, N, K, nt);
+  if (takes_lds(T, N, K, nt)) return 0;
+  const int64_t parts = plan_gemv(T, N, K, nt, true).parts;
   return parts > 1 ? parts * T * N * (int64_t)sizeof(float) : 0;
 }
 

@@ -70,7 +70,9 @@ def up(*arrays):
                                    (2, 4099, 8224), (16, 4096, 8192), (23, 8200, 4128),
                                    (64, 4100, 8256), (33, 33000, 1056), (70, 5000, 8192),
                                    (5, 300, 16416), (20, 1003, 12320), (40, 17, 16384),
-                                   (130, 5000, 12832), (2, 1, 65536), (50, 20003, 1696)])
+                                   (130, 5000, 12832), (2, 1, 65536), (50, 20003, 1696),
+                                   (2, 40010, 1056), (20, 40010, 576), (3, 500, 2080),
+                                   (2, 300, 4128), (64, 2049, 16416)])
 def test_against_float64(mx, orc, T, N, K, dtype):
     x = tokens(T, K, dtype)
     wq, ws = weights(N, K)
@@ -82,7 +84,8 @@ def test_against_float64(mx, orc, T, N, K, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,N,K", [(1, 40, 4096), (7, 300, 1056), (16, 5000, 256), (35, 64, 512),
-                                   (64, 200, 160), (2, 14000, 96),
+                                   (64, 200, 160), (2, 14000, 96), (3, 500, 2080),
+                                   (20, 20003, 1056), (40, 40010, 544),
                                    (1, 13000, 8192), (1, 100, 65536), (20, 13000, 608),
                                    (16, 4100, 8224), (40, 8200, 4128), (3, 33, 8224),
                                    (37, 500, 16416)])
