@@ -324,7 +324,7 @@ mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, in
  * arbitrary (N a multiple of gw), K a multiple of 32. x and its rows (ldx * element size) 16-byte
  * aligned, wq 16-byte aligned, y aligned to its elements, ldy >= N. The weights are read once for
  * every 16 to 64 tokens; many more tokens are the GEMMs' work.
- * workspace: mx_gemv_workspace(...) bytes, 16-byte aligned, make large products of several tokens
+ * workspace: mx_gemv_workspace(...) bytes, 16-byte aligned, make many products of several tokens
  * faster (sums over parts of K); 0 bytes are wanted for one token. Its contents are scratch, and
  * calls that may run at the same time need one each. NULL does without, with other roundings.
  * Accuracy: fp32 accumulation. The products are exact, sums of 128 of them are formed by the

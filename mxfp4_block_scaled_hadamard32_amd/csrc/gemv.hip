@@ -676,8 +676,16 @@ __global__ __launch_bounds__(256) void gemv_join_kernel(const GemvArgs a,
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < count;
        e += (int64_t)gridDim.x * 256) {
     float v = part[e];
-    for (int s = 1; s < splits; ++s) v += part[s * count + e];
-    store_y(a, e / a.N * a.ldy + e % a.N, v);
+    int s = 1;
+    for (; s + 4 <= splits; s += 4) {  // four loads on the way
+      float p[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p[k] = part[(s + k) * count + e];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v += p[k];
+    }
+    for (; s < splits; ++s) v += part[s * count + e];
+    store_y(a, a.ldy == a.N ? e : e / a.N * a.ldy + e % a.N, v);
   }
 }
 
