@@ -242,8 +242,9 @@ __device__ __forceinline__ RawChunk<BF16> raw_of(const float (&v)[8]) {
 // one is normalised (for up to 2 chunks a thread). Loads past the row or the last row repeat valid
 // places instead of branching: a wait behind a branch would have to count on none of the loads and
 // stores in it.
-// Bound by HBM: 16384 x 8192 bf16 with residual, y and E4M3 codes 210 us (5.8 TB/s of 9 bytes an
-// element), 8192 x 4096 58 us; rows of 128 by the vector ALU (26 us for 262144, 3.9 TB/s).
+// Bound by HBM: 16384 x 8192 bf16 with residual, y and E4M3 codes 205 to 228 us from card to card
+// (5.3 to 5.9 TB/s of 9 bytes an element; 225 to 231 on one with 4 to 12 waves a SIMD), 8192 x 4096
+// 58 us; rows of 128 by the vector ALU (26 us for 262144, 3.9 TB/s).
 template <bool BF16, int T, int V, int FMT, bool SR, bool RES>
 __global__ __launch_bounds__(T > 256 ? T : 256) void rmsnorm_kernel(const NormArgs a) {
   constexpr int kThreads = T > 256 ? T : 256;
@@ -424,7 +425,7 @@ hipError_t pick_norm_format(const NormArgs& a) {
 // A workgroup walks over rows like the forward kernel and keeps its columns' sums of dy z in
 // registers; rmsnorm_dgamma_kernel joins the workgroups' sums, partial[block][cols], in a fixed
 // order. Two rows and more a workgroup halve what it has to read.
-// Bound by HBM: 16384 x 8192 bf16 with dsum 194 us (5.5 TB/s of 8 bytes an element), 8192 x 4096 53
+// Bound by HBM: 16384 x 8192 bf16 with dsum 194 us (5.5 TB/s of 8 bytes an element), 8192 x 4096 54
 // us, the join 4-6 us of either.
 template <bool BF16, int T>
 constexpr int kBackwardThreads = T <= 64 ? 256 : T <= 256 || (BF16 && T <= 512) ? 2 * T : T;
