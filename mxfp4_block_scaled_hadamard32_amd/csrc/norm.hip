@@ -427,8 +427,11 @@ hipError_t pick_norm_format(const NormArgs& a) {
 // order. Two rows and more a workgroup halve what it has to read.
 // Bound by HBM: 16384 x 8192 bf16 with dsum 194 us (5.5 TB/s of 8 bytes an element), 8192 x 4096 54
 // us, the join 4-6 us of either.
-template <bool BF16, int T>
-constexpr int kBackwardThreads = T <= 64 ? 256 : T <= 256 || (BF16 && T <= 512) ? 2 * T : T;
+// SMALL (below): 512 threads also for narrow rows, for the columns' sake (4096 x 32 bf16: 6.1 us, 8.8
+// with 256 threads).
+template <bool BF16, int T, bool SMALL>
+constexpr int kBackwardThreads =
+    T <= 64 ? (SMALL ? 512 : 256) : T <= 256 || (BF16 && T <= 512) ? 2 * T : T;
 
 // dgamma of columns 32 i .. 32 i + 31 over all rows, for tensors that the caches hold: 4 threads a
 // row, every 4th lane another one.
@@ -461,18 +464,21 @@ __device__ __forceinline__ void dgamma_columns(const NormBackwardArgs& a, int i)
   }
 }
 
-// SMALL: the workgroups after the first a.row_blocks form dgamma from the columns, beside the rows:
-// one launch and no workspace.
+// SMALL: the first workgroups form dgamma from the columns, beside the rows: one launch and no
+// workspace. They come first because they take longest (1024 x 4096 fp32: 16.8 us, 20.4 last).
 template <bool BF16, int T, int V, bool DSUM, bool SMALL>
-__global__ __launch_bounds__((kBackwardThreads<BF16, T>)) void rmsnorm_backward_kernel(
+__global__ __launch_bounds__((kBackwardThreads<BF16, T, SMALL>)) void rmsnorm_backward_kernel(
     const NormBackwardArgs a) {
-  constexpr int kThreads = kBackwardThreads<BF16, T>;
+  constexpr int kThreads = kBackwardThreads<BF16, T, SMALL>;
   constexpr int kRows = kThreads / T;
+  int block = (int)blockIdx.x;
   if constexpr (SMALL) {
-    if ((int)blockIdx.x >= a.row_blocks) {
-      dgamma_columns<BF16, kThreads>(a, (int)blockIdx.x - a.row_blocks);
+    const int columns = a.dgamma ? (int)(a.cols / 32) : 0;
+    if (block < columns) {
+      dgamma_columns<BF16, kThreads>(a, block);
       return;
     }
+    block -= columns;
   }
   // The widest rows leave no registers for the next row's values (16 waves have 128 each), nor for
   // their own between the sum and the result: they are read again, from the caches.
@@ -492,7 +498,7 @@ __global__ __launch_bounds__((kBackwardThreads<BF16, T>)) void rmsnorm_backward_
     for (int k = 0; k < 8; ++k) acc[v][k] = 0.0f;
   }
   const int64_t stride = (int64_t)a.row_blocks * kRows;
-  int64_t row = (int64_t)blockIdx.x * kRows + sub;
+  int64_t row = (int64_t)block * kRows + sub;
   constexpr int kHeld = kAhead ? V : 1;
   RawChunk<BF16> dy[kHeld], s[kHeld], d[DSUM ? kHeld : 1];
   float rho;
@@ -640,7 +646,7 @@ __global__ __launch_bounds__(256) void rmsnorm_dgamma_kernel(const float* __rest
 // a thread, 4 with more; fewer for few rows, whose sums would be as much traffic as the rows
 template <bool BF16, int T, int V>
 int64_t backward_blocks(int64_t rows) {
-  constexpr int kThreads = kBackwardThreads<BF16, T>;
+  constexpr int kThreads = kBackwardThreads<BF16, T, false>;
   constexpr int kRows = kThreads / T;
   constexpr int64_t most = 256 * 4 * 64 * (V == 1 ? 6 : 4) / kThreads;
   const int64_t want = (rows + kRows - 1) / kRows;
@@ -650,14 +656,21 @@ int64_t backward_blocks(int64_t rows) {
 }
 
 // Tensors whose dgamma is formed from the columns: dy and s are read twice, the second time from
-// the caches. 777 x 2720 fp32: 9.4 us, 12.4 with the workgroups' sums and their join.
-bool small_backward(int64_t rows, int64_t cols) { return rows * cols <= (1 << 22); }
+// the caches, and each of the cols / 32 workgroups walks over all rows, so their number is bounded
+// as well as the tensor's size. Kernel times in us, columns | the workgroups' sums and their join
+// (which costs a caller without a graph 3 us on the host besides: a second launch, a workspace):
+//   777 x 2720 fp32 9.2 | 11.4     1024 x 1024 bf16 3.8 | 7.3    2048 x 128 bf16 4.4 | 5.2
+//   4096 x 32 bf16 6.1 | 5.4       4096 x 128 bf16 6.3 | 6.0     4096 x 1024 bf16 21.7 | 10.4
+//   8192 x 32 bf16 10.3 | 5.9      8192 x 512 bf16 36 | 11       131072 x 32 bf16 326 | 18
+bool small_backward(int64_t rows, int64_t cols) {
+  return rows <= 4096 && rows * cols <= (1 << 22);
+}
 
 template <bool BF16, int T, int V, bool DSUM>
 hipError_t launch_backward(NormBackwardArgs a) {
-  constexpr int kThreads = kBackwardThreads<BF16, T>;
   a.inv_cols = 1.0f / (float)a.cols;
   if (small_backward(a.rows, a.cols)) {
+    constexpr int kThreads = kBackwardThreads<BF16, T, true>;
     a.row_blocks = (int)((a.rows + kThreads / T - 1) / (kThreads / T));
     const unsigned blocks = a.row_blocks + (a.dgamma ? (unsigned)(a.cols / 32) : 0u);
     hipLaunchKernelGGL((rmsnorm_backward_kernel<BF16, T, V, DSUM, true>), dim3(blocks),
@@ -666,7 +679,8 @@ hipError_t launch_backward(NormBackwardArgs a) {
   }
   a.row_blocks = (int)backward_blocks<BF16, T, V>(a.rows);
   hipLaunchKernelGGL((rmsnorm_backward_kernel<BF16, T, V, DSUM, false>),
-                     dim3((unsigned)a.row_blocks), dim3(kThreads), 0, (hipStream_t)a.stream, a);
+                     dim3((unsigned)a.row_blocks), dim3((kBackwardThreads<BF16, T, false>)), 0,
+                     (hipStream_t)a.stream, a);
   if (hipError_t e = hipGetLastError(); e != hipSuccess || !a.dgamma) return e;
   hipLaunchKernelGGL(rmsnorm_dgamma_kernel, dim3((unsigned)(a.cols / 16)), dim3(256), 0,
                      (hipStream_t)a.stream, a.partial, a.row_blocks, a.cols, a.dgamma);

@@ -317,6 +317,20 @@ def test_backward_against_the_formula(mx, rows, cols, dtype, dsum):
     assert none is None and torch.equal(only, dx)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(4096, 32), (4097, 32), (4096, 992), (8192, 96),
+                                       (131072, 32), (3001, 160)])
+def test_backward_of_tall_narrow_tensors(mx, rows, cols, dtype):
+    """Both forms of dgamma beside the border between them, and far from it."""
+    dy, s, g, rstd, d = make_backward(rows, cols, dtype, True)
+    dx, dg = mx.mx_rmsnorm_backward(dev(dy), dev(s), dev(g), dev(rstd), dsum=dev(d))
+    torch.cuda.synchronize()
+    check_backward(dx, dg, dy, s, g, rstd, d)
+    only, _ = mx.mx_rmsnorm_backward(dev(dy), dev(s), dev(g), dev(rstd), dsum=dev(d),
+                                     with_dgamma=False)
+    assert torch.equal(only, dx)
+
+
 def test_backward_against_differences(mx):
     """d/dh of L = sum dy y(s + h v, gamma + h w) at 0, by central differences of the forward
     pass in fp32. Its noise is the rounding of y (half a step each) over h and the difference

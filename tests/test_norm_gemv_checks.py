@@ -106,6 +106,17 @@ def test_backward_workspace_size(m):
         assert f(rows, cols) % (4 * cols) == 0 and 0 < f(rows, cols) <= min(rows, 1536) * 4 * cols
 
 
+@pytest.mark.parametrize("rows,cols", [(4097, 32), (8192, 512), (16384, 256), (32768, 128),
+                                       (131072, 32)])
+def test_backward_of_tall_narrow_tensors_wants_a_workspace(m, rows, cols):
+    """Without one, cols / 32 workgroups would walk over all these rows."""
+    size = m.lib().mx_rmsnorm_backward_workspace(rows, cols)
+    assert size > 0 and size % (4 * cols) == 0 and size <= 1536 * 4 * cols
+    ld = dict(lddy=cols, ldds=cols, lds=cols, lddx=cols)
+    assert backward_call(m, rows=rows, cols=cols, size=size - 1, **ld) == m.MX_ERR_ARG
+    assert backward_call(m, rows=rows, cols=cols, work=None, **ld) == m.MX_ERR_NULL
+
+
 def gemv_call(m, **kw):
     v = dict(x=A, dtype=1, ldx=64, wq=A, ws=A, gw=1, T=3, N=10, K=64, had=0, mask=0, alpha=0,
              odt=1, y=A, ldy=10, work=None, size=0)
