@@ -268,12 +268,13 @@ mx_status mx_scale_mismatch_map(const void* x, int32_t dtype, int64_t rows, int6
  * once, to the nearest value, so a row's outputs depend on that row alone (not on how many rows
  * share the call). A row that holds an infinity or a NaN gives NaNs (or zeros beside an infinity),
  * as the formula does. sum and y may each be x or residual itself (same leading dimension), not
- * both the same one.
+ * both the same one; rows of theirs that share memory in another way are refused.
  * cols is a multiple of 32 and at most 32768 (MX_ERR_UNSUPPORTED beyond); pointers to rows and
  * gamma 16-byte aligned, rstd 4-byte, every leading dimension * element size a multiple of 16
  * bytes. Errors (nothing is launched): MX_ERR_NULL for a NULL x, gamma or y; MX_ERR_SHAPE for
  * negative sizes, a leading dimension below cols or the multiple-of rules; MX_ERR_ARG for a bad
- * type, a misaligned pointer or an eps that is negative or not finite. rows == 0 or cols == 0 is a
+ * type, a misaligned pointer, an eps that is negative or not finite, or outputs that overlap an
+ * operand. rows == 0 or cols == 0 is a
  * no-op. */
 mx_status mx_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t dtype,
                      int64_t rows, int64_t cols, const void* gamma, int32_t gamma_dtype, float eps,
@@ -303,11 +304,11 @@ mx_status mx_rmsnorm_quant_mxfp8(const void* x, int64_t ldx, const void* residua
  *   dx = rstd * (u - z * c) + dsum     (the gradient of x and of residual alike),
  *   dgamma[j] = sum over the rows of dy * z   (fp32; may be NULL).
  * fp32 throughout, dx rounded to dtype at the end; the order of every sum is fixed by the sizes.
- * dx may be dsum itself (same leading dimension), or without dgamma dy. With dgamma, workspace
+ * dx may be dsum itself (same leading dimension), or without dgamma dy or s. With dgamma, workspace
  * holds at least mx_rmsnorm_backward_workspace(rows, cols) bytes (0 for small tensors), 16-byte
- * aligned; its contents are scratch, and calls that may run at the same time need one each. Sizes, alignment and errors as for
- * mx_rmsnorm; MX_ERR_ARG also for a workspace that is too small and for dx on dy or s with
- * dgamma. rows == 0 writes a zero dgamma. */
+ * aligned; its contents are scratch, and calls that may run at the same time need one each. Sizes,
+ * alignment and errors as for mx_rmsnorm; MX_ERR_ARG also for a workspace that is too small and for
+ * dx that shares memory with dy or s when there is a dgamma. rows == 0 writes a zero dgamma. */
 int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
 mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, int64_t ldds,
                               const void* s, int64_t lds, int32_t dtype, int64_t rows,
@@ -335,7 +336,7 @@ mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, in
  * beyond bf16's range, 2^128 or more (scale bytes 253 and 254), counts as infinity: with fp32 or
  * rotated tokens, or zeros in x, its output may be NaN. Scale byte 255 is NaN.
  * Errors (nothing is launched): MX_ERR_SHAPE, MX_ERR_ARG (types, granularity, hadamard, alpha_exp
- * outside [-126, 127], alignment, a workspace that is too small), MX_ERR_NULL, MX_ERR_LAUNCH (N
+ * outside [-126, 127], alignment, a workspace that is too small, a y that overlaps x), MX_ERR_NULL, MX_ERR_LAUNCH (N
  * above 2^26 or T above 2^19 rows). T == 0 or N == 0 is a no-op; K == 0 writes zeros. */
 int64_t mx_gemv_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, int32_t hadamard,
                           int32_t out_dtype);

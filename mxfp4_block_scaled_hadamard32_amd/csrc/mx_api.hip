@@ -67,6 +67,42 @@ mx_status check_norm_sizes(int32_t dtype, int64_t rows, int64_t cols, int32_t ga
   return cols > kNormMaxCols ? MX_ERR_UNSUPPORTED : MX_OK;
 }
 
+// `rows` rows of `width` bytes, `pitch` bytes apart
+struct Rows {
+  const void* p;
+  int64_t pitch, width;
+};
+
+// Whether two operands have a byte in common. Rows that lie between one another (halves of one
+// buffer) have none. A row of b starts v bytes after one of a; they meet when -b.width < v < a.width.
+bool meet(const Rows& a, const Rows& b, int64_t rows) {
+  if (!a.p || !b.p || rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+  typedef __int128 wide;  // a caller's nonsense may pass 64 bits
+  if (d >= (wide)(rows - 1) * a.pitch + a.width || -d >= (wide)(rows - 1) * b.pitch + b.width)
+    return false;
+  auto first = [&](int64_t from, int64_t least) {  // the least k >= least with from + k b.pitch > -b.width
+    const int64_t x = -b.width - from;             // k > x / b.pitch
+    const int64_t k = (x >= 0 ? x / b.pitch : -((-x + b.pitch - 1) / b.pitch)) + 1;
+    return k > least ? k : least;
+  };
+  if (a.pitch == b.pitch) {  // only the difference of the rows' indexes matters
+    const int64_t k = first(d, 1 - rows);
+    return k < rows && d + k * b.pitch < a.width;
+  }
+  for (int64_t i = 0; i < rows; ++i) {
+    const int64_t from = d - i * a.pitch, k = first(from, 0);
+    if (k < rows && from + k * b.pitch < a.width) return true;
+  }
+  return false;
+}
+
+// an output may be an input itself, or share nothing with it
+bool clash(const Rows& out, const Rows& in, int64_t rows) {
+  const bool same = out.p == in.p && (out.pitch == in.pitch || rows == 1);
+  return !same && meet(out, in, rows);
+}
+
 // fmt 0: y only (required); 1, 2, 3: E2M1, E4M3, E5M2 codes, y optional
 mx_status rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t dtype,
                   int64_t rows, int64_t cols, const void* gamma, int32_t gamma_dtype, float eps,
@@ -85,6 +121,12 @@ mx_status rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
   if (rows == 0 || cols == 0) return MX_OK;
   if (!x || !gamma) return MX_ERR_NULL;
   if (fmt == 0 ? !y : (!codes || !scales)) return MX_ERR_NULL;
+  const int64_t esize = dtype == MX_BF16 ? 2 : 4, width = cols * esize;
+  const Rows rx{x, ldx * esize, width}, rr{residual, ldr * esize, width}, rs{sum, lds * esize, width},
+      ry{y, ldy * esize, width};
+  if (meet(rs, ry, rows) || clash(rs, rx, rows) || clash(rs, rr, rows) || clash(ry, rx, rows) ||
+      clash(ry, rr, rows))
+    return MX_ERR_ARG;
   NormArgs a{};
   a.x = x;
   a.residual = residual;
@@ -332,11 +374,17 @@ mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, in
   if (cols == 0 || (rows == 0 && !dgamma)) return MX_OK;
   if (rows > 0) {
     if (!dy || !s || !gamma || !rstd || !dx) return MX_ERR_NULL;
-    // dgamma reads dy beside the rows that are written
-    if (dgamma && (dx == dy || dx == s)) return MX_ERR_ARG;
     const int64_t need = dgamma ? mx_rmsnorm_backward_workspace(rows, cols) : 0;
     if (need > 0 && !workspace) return MX_ERR_NULL;
     if (workspace_bytes < need) return MX_ERR_ARG;
+    const int64_t esize = dtype == MX_BF16 ? 2 : 4, width = cols * esize;
+    const Rows rdx{dx, lddx * esize, width}, rdy{dy, lddy * esize, width}, rs{s, lds * esize, width},
+        rds{dsum, ldds * esize, width};
+    // dgamma reads dy and s beside the rows that are written
+    if (dgamma ? meet(rdx, rdy, rows) || meet(rdx, rs, rows)
+               : clash(rdx, rdy, rows) || clash(rdx, rs, rows))
+      return MX_ERR_ARG;
+    if (clash(rdx, rds, rows)) return MX_ERR_ARG;
   }
   NormBackwardArgs a{dy,   dsum, s,    gamma, rstd, dx,   dgamma, dgamma ? (float*)workspace : nullptr,
                      rows, cols, lddy, ldds,  lds,  lddx, dtype == MX_BF16,
@@ -359,6 +407,8 @@ mx_status mx_gemv(const void* x, int32_t dtype, int64_t ldx, const uint8_t* wq, 
   if (!aligned(y, out_dtype == MX_BF16 ? 2 : 4) || !aligned(wq, 16)) return MX_ERR_ARG;
   if (T == 0 || N == 0) return MX_OK;
   if (!y || (K > 0 && (!x || !wq || !ws))) return MX_ERR_NULL;
+  const int64_t esize = dtype == MX_BF16 ? 2 : 4, osize = out_dtype == MX_BF16 ? 2 : 4;
+  if (meet(Rows{x, ldx * esize, K * esize}, Rows{y, ldy * osize, N * osize}, T)) return MX_ERR_ARG;
   const int64_t need = mx_gemv_workspace(dtype, T, N, K, hadamard, out_dtype);
   if (workspace && need > 0 && (workspace_bytes < need || !aligned(workspace, 16)))
     return MX_ERR_ARG;

@@ -146,6 +146,41 @@ def test_leading_dimensions_and_aliasing(mx, rows, cols, dtype):
     assert torch.equal(wx, s0) and torch.equal(y, y0) and torch.equal(wr, r)
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 64), (6, 96), (5, 4128)])
+def test_rows_that_lie_between_one_another(mx, rows, cols):
+    """x, residual, sum and y as the quarters of one buffer's rows, as rows taken in turn, and with
+    leading dimensions that differ; outputs that overlap are refused and left alone."""
+    x, r, g = (dev(t) for t in make(rows, cols, "bf16", True))
+    y0, s0, r0 = mx.mx_rmsnorm(x, g, r)
+    buf = torch.zeros((rows, 4 * cols), dtype=x.dtype, device=DEV)
+    turns = torch.zeros((rows, 4, cols), dtype=x.dtype, device=DEV)
+    for wx, wr, ws, wy in ((buf[:, i * cols:(i + 1) * cols] for i in range(4)),
+                           (turns[:, i] for i in range(4))):
+        wx.copy_(x)
+        wr.copy_(r)
+        mx.mx_rmsnorm(wx, g, wr, sum=ws, y=wy)
+        assert torch.equal(wx, x) and torch.equal(wr, r)
+        assert torch.equal(ws, s0) and torch.equal(wy, y0)
+        dx, _ = mx.mx_rmsnorm_backward(wr, ws, g, r0, dsum=wx)
+        mx.mx_rmsnorm_backward(wr, ws, g, r0, dsum=wx, dx=wy)
+        assert torch.equal(wy, dx)
+    # y's short rows inside one long row of x's buffer, between the ends of x's rows
+    flat = torch.zeros(8 * rows * cols, dtype=x.dtype, device=DEV)
+    wx = flat.as_strided((rows, cols), (4 * cols, 1))
+    wx.copy_(x)
+    wy = flat.as_strided((min(rows, 2), cols), (cols, 1), cols)
+    mx.mx_rmsnorm(wx[:min(rows, 2)], g, r[:min(rows, 2)], y=wy)
+    assert torch.equal(wy, y0[:2])
+    before = flat.clone()
+    with pytest.raises(mx.MxError):
+        mx.mx_rmsnorm(wx, g, r, y=flat[16:].as_strided((rows, cols), (4 * cols, 1), 16))
+    with pytest.raises(mx.MxError):
+        mx.mx_rmsnorm(wx, g, r, sum=wy if rows == 1 else flat[:rows * cols].view(rows, cols), y=wy
+                      if rows == 1 else None)
+    torch.cuda.synchronize()
+    assert torch.equal(flat, before)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_special_rows(mx, orc, dtype):
     """Zero, huge, tiny, infinite and NaN rows; the others are as they are alone."""

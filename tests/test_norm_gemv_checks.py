@@ -70,6 +70,54 @@ def test_norm_output_refusals(m):
     assert norm_call(m, rows=0, residual=None, ldr=1, sum=None, lds=1) == m.MX_OK
 
 
+def ptr(address):
+    return ctypes.c_void_p(address)
+
+
+# x, residual, sum and y of 4 rows of 64 bf16 values, 128 bytes apart where nothing else is said
+@pytest.mark.parametrize("kw", [
+    dict(sum=ptr(0x20000), y=ptr(0x20000)),                                   # both on one buffer
+    dict(sum=ptr(0x20000), y=ptr(0x20010)),                                   # a few bytes apart
+    dict(x=ptr(0x20000), sum=ptr(0x20000), lds=128),                          # x, other rows
+    dict(residual=ptr(0x20000), y=ptr(0x20000), ldy=72),                      # residual, other rows
+    dict(x=ptr(0x20000), y=ptr(0x20080)),                                     # a row further
+    dict(x=ptr(0x20000), y=ptr(0x1FF80)),                                     # a row before
+    dict(x=ptr(0x20000), ldx=128, sum=ptr(0x20070), lds=128),                 # the gap, and a bit
+    dict(x=ptr(0x20000), ldx=128, sum=ptr(0x20300), lds=72),                  # into the last row
+    dict(x=ptr(0x20000), ldx=128, rows=1 << 20, sum=ptr(0x20000 + (1 << 27)), lds=64),
+])
+def test_norm_refuses_overlapping_outputs(m, kw):
+    v = dict(x=ptr(0x1000000000), residual=ptr(0x2000000000), sum=ptr(0x3000000000),
+             y=ptr(0x4000000000))
+    v.update(kw)
+    for name in ("mx_rmsnorm", "mx_rmsnorm_quant", "mx_rmsnorm_quant_mxfp8"):
+        assert norm_call(m, name, **v) == m.MX_ERR_ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dx=ptr(0x20000), dsum=ptr(0x20000), ldds=128),
+    dict(dx=ptr(0x20000), dsum=ptr(0x20010)),
+    dict(dx=ptr(0x20000), dy=ptr(0x20010)),
+    dict(dx=ptr(0x20000), s=ptr(0x20080)),
+    dict(dx=ptr(0x20000), s=ptr(0x20000), dgamma=ptr(0x5000000000)),
+    dict(dx=ptr(0x20000), dy=ptr(0x20000), lddy=72),
+    dict(dx=ptr(0x20000), dy=ptr(0x1FF80), dgamma=ptr(0x5000000000)),
+])
+def test_backward_refuses_overlapping_outputs(m, kw):
+    v = dict(rows=4, dy=ptr(0x1000000000), dsum=ptr(0x2000000000), s=ptr(0x3000000000),
+             dx=ptr(0x4000000000), dgamma=None, work=None, size=0)
+    v.update(kw)
+    assert backward_call(m, **v) == m.MX_ERR_ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(N=64, ldy=64), dict(y=ptr(0x10010)), dict(y=ptr(0x1017E)), dict(x=ptr(0x10030)),
+    dict(odt=0, T=1, y=ptr(0x1007C)), dict(ldx=128, y=ptr(0x1007E), ldy=128),
+])
+def test_gemv_refuses_an_output_on_its_input(m, kw):
+    assert gemv_call(m, **kw) == m.MX_ERR_ARG
+
+
 def backward_call(m, **kw):
     v = dict(dy=A, lddy=64, dsum=B, ldds=64, s=A, lds=64, dtype=1, rows=1 << 20, cols=64, gamma=A,
              gdt=0, rstd=A, dx=B, lddx=64, dgamma=A, work=A, size=1 << 20)
