@@ -336,8 +336,8 @@ mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, in
  * beyond bf16's range, 2^128 or more (scale bytes 253 and 254), counts as infinity: with fp32 or
  * rotated tokens, or zeros in x, its output may be NaN. Scale byte 255 is NaN.
  * Errors (nothing is launched): MX_ERR_SHAPE, MX_ERR_ARG (types, granularity, hadamard, alpha_exp
- * outside [-126, 127], alignment, a workspace that is too small, a y that overlaps x), MX_ERR_NULL, MX_ERR_LAUNCH (N
- * above 2^26 or T above 2^19 rows). T == 0 or N == 0 is a no-op; K == 0 writes zeros. */
+ * outside [-126, 127], alignment, a workspace that is too small, a y that overlaps x), MX_ERR_NULL,
+ * MX_ERR_UNSUPPORTED (N above 2^26 or T above 2^19 rows, whatever the other sizes). T == 0 or N == 0 is a no-op; K == 0 writes zeros. */
 int64_t mx_gemv_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, int32_t hadamard,
                           int32_t out_dtype);
 mx_status mx_gemv(const void* x, int32_t dtype, int64_t ldx, const uint8_t* wq, const uint8_t* ws,

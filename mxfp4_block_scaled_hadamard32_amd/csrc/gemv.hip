@@ -702,7 +702,6 @@ __global__ __launch_bounds__(256) void gemv_zero_kernel(const GemvArgs a) {
 template <bool BF16, bool HAD, int NT, int RT>
 hipError_t launch_direct(const GemvArgs& a) {
   const int64_t gx = (a.N + 16 * RT - 1) / (16 * RT), gy = (a.T + 15) / 16;
-  if (gx > (1 << 22) || gy > 32768) return hipErrorInvalidValue;
   hipLaunchKernelGGL((gemv_direct_kernel<BF16, HAD, NT, RT>), dim3((unsigned)gx, (unsigned)gy),
                      dim3(512), 0, (hipStream_t)a.stream, a);
   return hipGetLastError();
@@ -719,7 +718,6 @@ int segment_blocks(const GemvArgs& a, int nt, int rows, int bytes) {
 template <bool BF16, bool HAD, int NT, int RT, int WV>
 hipError_t launch_gemv(const GemvArgs& a, int bytes) {
   const int64_t gx = (a.N + 16 * RT - 1) / (16 * RT);
-  if (gx > (1 << 22)) return hipErrorInvalidValue;
   const int seg = segment_blocks(a, NT, 16 * RT, bytes);
   const int srows = a.gw == 1 ? 16 * RT : (16 * RT + a.gw - 1) / a.gw;
   const size_t use = (size_t)NT * seg * 64 * a.T + (size_t)srows * scale_pitch(seg);
@@ -740,7 +738,6 @@ template <bool BF16, bool HAD, int NT, int MT, int RT>
 hipError_t launch_shared(const GemvArgs& a, float* part, int splits) {
   constexpr int kRows = 128 * RT;
   const int64_t gx = (a.N + kRows - 1) / kRows, gy = (a.T + 16 * MT - 1) / (16 * MT);
-  if (gx > (1 << 22) || gy > 32768) return hipErrorInvalidValue;
   hipLaunchKernelGGL((gemv_shared_kernel<BF16, HAD, NT, MT, RT>),
                      dim3((unsigned)gx, (unsigned)gy, (unsigned)splits), dim3(512), 0,
                      (hipStream_t)a.stream, a, part, splits);

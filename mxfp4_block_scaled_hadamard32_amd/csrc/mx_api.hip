@@ -406,6 +406,7 @@ mx_status mx_gemv(const void* x, int32_t dtype, int64_t ldx, const uint8_t* wq, 
   if (alpha_exp < -126 || alpha_exp > 127) return MX_ERR_ARG;
   if (!aligned(y, out_dtype == MX_BF16 ? 2 : 4) || !aligned(wq, 16)) return MX_ERR_ARG;
   if (T == 0 || N == 0) return MX_OK;
+  if (T > kGemvMaxTokens || N > kGemvMaxRows) return MX_ERR_UNSUPPORTED;
   if (!y || (K > 0 && (!x || !wq || !ws))) return MX_ERR_NULL;
   const int64_t esize = dtype == MX_BF16 ? 2 : 4, osize = out_dtype == MX_BF16 ? 2 : 4;
   if (meet(Rows{x, ldx * esize, K * esize}, Rows{y, ldy * osize, N * osize}, T)) return MX_ERR_ARG;
@@ -420,7 +421,7 @@ mx_status mx_gemv(const void* x, int32_t dtype, int64_t ldx, const uint8_t* wq, 
 
 int64_t mx_gemv_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, int32_t hadamard,
                           int32_t out_dtype) {
-  if (T <= 0 || N <= 0 || K <= 0) return 0;
+  if (T <= 0 || N <= 0 || K <= 0 || T > kGemvMaxTokens || N > kGemvMaxRows) return 0;
   return mx_gemv_workspace_bytes(T, N, K, dtype == MX_BF16, hadamard == 1, out_dtype == MX_BF16);
 }
 

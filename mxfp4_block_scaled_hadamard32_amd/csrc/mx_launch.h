@@ -117,7 +117,9 @@ int64_t mx_norm_backward_blocks(int64_t rows, int64_t cols);
 hipError_t mx_launch_rmsnorm_backward(const NormBackwardArgs& a);
 
 // y[t][n] = 2^alpha * sum_k x[t][k] * W[n][k]; x bf16 or fp32, W packed E2M1 with scales
-// [N/gw][K/32].
+// [N/gw][K/32]. The limits keep every shape's grid (16 tokens by 16 rows a workgroup at least)
+// within 2^22 x 2^15 workgroups.
+constexpr int64_t kGemvMaxTokens = (int64_t)1 << 19, kGemvMaxRows = (int64_t)1 << 26;
 struct GemvArgs {
   const void* x;
   const uint8_t* w;

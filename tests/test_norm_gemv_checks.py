@@ -201,6 +201,18 @@ def test_gemv_workspace(m):
             assert f(dtype, 0, 8192, 28672, had, 1) == 0
 
 
+@pytest.mark.parametrize("T,N,K", [((1 << 19) + 1, 128, 4096), (1 << 20, 128, 4096),
+                                   (1, (1 << 26) + 1, 32), (16, 1 << 27, 1024),
+                                   ((1 << 19) + 1, 32, 0), (1 << 40, 1 << 40, 4096)])
+def test_gemv_size_limits(m, T, N, K):
+    """The documented limits hold whichever kernel the other sizes would choose."""
+    ld = dict(T=T, N=N, K=K, ldx=K, ldy=N)
+    assert gemv_call(m, **ld) == m.MX_ERR_UNSUPPORTED
+    for dtype in (0, 1):
+        for had in (0, 1):
+            assert m.lib().mx_gemv_workspace(dtype, T, N, K, had, 1) == 0
+
+
 def test_gemv_nothing_to_do(m):
     assert gemv_call(m, T=0, x=None, y=None) == m.MX_OK
     assert gemv_call(m, N=0, wq=None, ws=None, y=None) == m.MX_OK
