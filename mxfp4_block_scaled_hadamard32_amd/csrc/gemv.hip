@@ -715,22 +715,15 @@ int segment_blocks(const GemvArgs& a, int nt, int rows, int bytes) {
   return (int)(seg < nb4 ? seg : nb4);
 }
 
-template <bool BF16, bool HAD, int NT, int RT, int WV>
+template <bool BF16, bool HAD, int NT, int RT, int WV, bool ONE = true>
 hipError_t launch_gemv(const GemvArgs& a, int bytes) {
   const int64_t gx = (a.N + 16 * RT - 1) / (16 * RT);
   const int seg = segment_blocks(a, NT, 16 * RT, bytes);
   const int srows = a.gw == 1 ? 16 * RT : (16 * RT + a.gw - 1) / a.gw;
   const size_t use = (size_t)NT * seg * 64 * a.T + (size_t)srows * scale_pitch(seg);
   const size_t join = (size_t)WV * RT * 1024;
-  const dim3 grid((unsigned)gx), block(64 * WV);
-  if (a.T == 1) {
-    hipLaunchKernelGGL((gemv_kernel<BF16, HAD, NT, RT, WV, true>), grid, block,
-                       use > join ? use : join, (hipStream_t)a.stream, a, seg);
-    return hipGetLastError();
-  }
-  if constexpr (NT > 1 && RT == 1 && WV == 8)  // takes_lds
-    hipLaunchKernelGGL((gemv_kernel<BF16, HAD, NT, RT, WV, false>), grid, block,
-                       use > join ? use : join, (hipStream_t)a.stream, a, seg);
+  hipLaunchKernelGGL((gemv_kernel<BF16, HAD, NT, RT, WV, ONE>), dim3((unsigned)gx), dim3(64 * WV),
+                     use > join ? use : join, (hipStream_t)a.stream, a, seg);
   return hipGetLastError();
 }
 
@@ -836,6 +829,8 @@ Plan plan_gemv(int64_t T, int64_t N, int64_t K, int nt, bool workspace) {
 template <bool BF16, bool HAD, int NT>
 hipError_t pick_gemv(const GemvArgs& a) {
   if (takes_lds(a.T, a.N, a.K, NT)) {
+    if constexpr (NT > 1)
+      if (a.T > 1) return launch_gemv<BF16, HAD, NT, 1, 8, false>(a, kLds);
     // Few workgroups need 8 waves each to keep enough codes coming (one bf16 token, N 8192, K 28672:
     // 26.8 us, 30.6 with 4 waves); with many, 4 waves and in the end one row tile do better (N
     // 14336, K 4096: 9.2 us with 2 tiles of 4 waves, 10.1 with 8; N 28672, K 8192: 30.2 us with 1

@@ -219,6 +219,20 @@ def test_offsets_past_32_bits(mx, orc):
     check_gemm(y[:, p], C, Cabs, rel=bound(K))
 
 
+@pytest.mark.parametrize("T,N,K,dtype", [(1 << 19, 17, 64, "bf16"), (1 << 19, 1, 544, "f32"),
+                                         (1, 1 << 26, 32, "bf16"), (2, 1 << 26, 64, "bf16")])
+def test_the_largest_counts(mx, orc, T, N, K, dtype):
+    """As many tokens and rows as the entry takes: the first and last ones against float64."""
+    x = torch.randn((T, K), device=DEV).to(DT[dtype])
+    q = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV)
+    s = torch.randint(117, 137, (N, K // 32), dtype=torch.uint8, device=DEV)
+    y = mx.mx_gemv(x, q, s, out_dtype=torch.float32)
+    rows, cols = (torch.from_numpy(np.unique(np.r_[0:min(n, 40), max(n - 40, 0):n])).to(DEV)
+                  for n in (T, N))
+    C, Cabs = expected(orc, x[rows].cpu(), q[cols].cpu().numpy(), s[cols].cpu().numpy(), 1)
+    check_gemm(y[rows][:, cols], C, Cabs, rel=bound(K))
+
+
 def test_streams_and_graph_replays(mx):
     """Three captured products (two of them with workspaces) on streams of their own replayed at once, beside eager calls."""
     K, N = 8192, 4112
