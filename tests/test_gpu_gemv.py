@@ -111,6 +111,141 @@ def test_rotated_weights(mx, orc, T, N, K, dtype):
     assert rel < 0.25, rel
 
 
+def some(N, n=48):
+    """The first, some middle and the last of N outputs."""
+    return np.unique(np.r_[0:min(n, N), N // 2:min(N // 2 + n, N), max(N - n, 0):N])
+
+
+def check_outputs(orc, y, x, wq, ws, had):
+    """y against float64, within the documented bound; wq, ws the rows of y's columns."""
+    T, K = x.shape
+    C, Cabs = expected(orc, x, wq, ws, 1, had, MASK, -5 * had)
+    b = bound(K) * Cabs
+    if had:
+        if x.dtype == torch.bfloat16 and y.dtype == torch.bfloat16:
+            b = b + 2.0 ** -17 * Cabs  # 16 bits of each rotated value
+        W = np.abs(orc.dequantize_f64(wq, ws, wq.shape[0], K, 1))  # five fp32 stages, as above
+        A = np.abs(x.double().numpy()).reshape(T, K // 32, 32).sum(2).repeat(32, axis=1) @ W.T / 32
+        b = b + 5 * 2.0 ** -24 * A
+    check_gemm(y, C, b, rel=1.0)
+
+
+# sizes that between them take each shape of the kernels for rotated tokens, with the number of parts
+# of K for two bf16 terms (bf16 tokens and outputs) and for three: the choice is an estimate's, and
+# a test that no longer reaches its kernel has to say so
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"),
+                                       ("f32", "bf16")])
+@pytest.mark.parametrize("T,N,K,parts2,parts3", [
+    (38, 24992, 832, 1, 1), (23, 16416, 11232, 3, 1), (30, 2551, 20032, 12, 6),
+    (3, 12495, 6784, 5, 5), (16, 28672, 8192, 2, 2), (40, 8200, 8224, 2, 2),
+    (64, 2049, 16416, 7, 7), (2, 500, 2080, 0, 0), (1, 7000, 2080, 0, 0), (1, 9700, 1056, 0, 0),
+    (1, 17000, 1056, 0, 0), (1, 5000, 28672, 0, 0), (1, 300, 28672, 0, 0)])
+def test_every_shape_for_rotated_tokens(mx, orc, T, N, K, parts2, parts3, dtype, out):
+    parts = parts2 if (dtype, out) == ("bf16", "bf16") else parts3
+    size = mx.lib().mx_gemv_workspace(int(dtype == "bf16"), T, N, K, 1, int(out == "bf16"))
+    assert size == (4 * T * N * parts if parts > 1 else 0)
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    q = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV, generator=gen)
+    s = torch.randint(117, 137, (N, K // 32), dtype=torch.uint8, device=DEV, generator=gen)
+    x = tokens(T, K, dtype)
+    y = mx.mx_gemv(x.to(DEV), q, s, hadamard=1, sign_mask=MASK, alpha_exp=-5, out_dtype=DT[out])
+    p = torch.from_numpy(some(N, 130)).to(DEV)
+    check_outputs(orc, y[:, p], x, q[p].cpu().numpy(), s[p].cpu().numpy(), 1)
+
+
+# one-token, direct and shared kernels, whole chunks and blocks left over, one part of K and several
+KERNELS = [(1, 40, 4128), (1, 9300, 1056), (2, 500, 2080), (6, 40, 1184), (16, 5000, 256),
+           (20, 1003, 12320), (16, 4096, 8192), (50, 12900, 1600), (64, 4100, 8256),
+           (9, 12900, 4128)]
+
+
+@pytest.mark.parametrize("had", [0, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N,K", KERNELS)
+def test_special_values_in_every_kernel(mx, orc, T, N, K, dtype, had):
+    """Infinities and NaNs of a token in its first and last block stay in that token, NaN scales in
+    their outputs, zeros give zeros, and the tokens beside them their products."""
+    wq, ws = weights(N, K)
+    wq[wq & 7 == 0] |= 1  # no zero weights: infinity times zero is a NaN
+    wq[wq & 0x70 == 0] |= 0x10
+    bad = [5, N - 2]
+    ws[5, 0] = ws[N - 2, K // 32 - 1] = 255
+    q, s = up(wq, ws)
+    cols = some(N)
+    W = orc.dequantize_f64(wq[cols], ws[cols], len(cols), K, 1)
+    fine = ~np.isin(cols, bad)
+    kinds = ["zero", "inf", "-inf", "nan", "late nan", "plain"]
+    for shift in range(0, len(kinds), T):
+        kind = [kinds[(shift + t) % len(kinds)] for t in range(T)]
+        x = tokens(T, K, dtype, seed=shift + 1)
+        for t, k in enumerate(kind):
+            if k == "zero":
+                x[t] = 0.0
+            elif k != "plain":
+                at = {"inf": 3, "-inf": K - 1, "nan": 20, "late nan": K - 2}[k]
+                x[t, at] = float(k.split()[-1])
+        for out in (torch.float32, torch.bfloat16):
+            y = mx.mx_gemv(x.to(DEV), q, s, hadamard=had, sign_mask=MASK, alpha_exp=-5 * had,
+                           out_dtype=out)[:, torch.from_numpy(cols).to(DEV)]
+            v = y.double().cpu().numpy()
+            assert np.isnan(v[:, ~fine]).all()
+            for t, k in enumerate(kind):
+                row = v[t, fine]
+                if k == "zero":
+                    assert (row == 0).all()
+                elif k.endswith("nan"):
+                    assert np.isnan(row).all()
+                elif k.endswith("inf"):
+                    if had:
+                        assert not np.isfinite(row).any()
+                    else:
+                        at, sign = (3, 1.0) if k == "inf" else (K - 1, -1.0)
+                        assert (row == sign * np.sign(W[fine, at]) * np.inf).all()
+            plain = [t for t, k in enumerate(kind) if k == "plain"]
+            if plain:
+                f = torch.from_numpy(fine)
+                check_outputs(orc, y.cpu()[plain][:, f], x[plain], wq[cols[fine]], ws[cols[fine]],
+                              had)
+
+
+@pytest.mark.parametrize("had", [0, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N,K", KERNELS)
+def test_scales_at_the_ends_of_their_range(mx, orc, T, N, K, dtype, had):
+    """Bytes 0 (2^-127, bf16 subnormals) to 2 and 250 to 252 in every block, against tokens that
+    bring the products into range; 253 and 254 with weights that bf16 holds, and with ones beyond."""
+    rng = np.random.default_rng(3)
+    wq, _ = weights(N, K)
+    cols = some(N)
+    p = torch.from_numpy(cols).to(DEV)
+    for low, power in ((0, 60), (250, -60)):
+        ws = rng.integers(low, low + 3, (N, K // 32), dtype=np.uint8)
+        x = tokens(T, K, dtype)
+        x = (x.double() * 2.0 ** power).to(x.dtype)
+        x[x == 0] = 2.0 ** power
+        fine = np.ones(len(cols), dtype=bool)
+        if low:
+            wq[3] &= 0xDD           # magnitudes 0, 1/2, 2, 3: 3 x 2^126 is below 2^128
+            wq[N - 3] &= 0xBB       # magnitudes 0, 1/2, 1, 3/2
+            ws[3], ws[N - 3] = 253, 254
+            wq[6], ws[6] = 0x11, 250
+            wq[6, K // 2 - 1] = 0x17  # one weight of 6 x 2^126 in the last block
+            ws[6, K // 32 - 1] = 253
+            fine[cols == 6] = False
+        q, s = up(wq, ws)
+        for out in (torch.float32, torch.bfloat16):
+            y = mx.mx_gemv(x.to(DEV), q, s, hadamard=had, sign_mask=MASK, alpha_exp=-5 * had,
+                           out_dtype=out)[:, p]
+            check_outputs(orc, y[:, torch.from_numpy(fine).to(DEV)], x, wq[cols[fine]],
+                          ws[cols[fine]], had)
+            if low:
+                over = y[:, torch.from_numpy(~fine).to(DEV)]
+                assert not torch.isfinite(over).any()
+                if dtype == "bf16" and not had:
+                    assert (over[:, 0].cpu().float()
+                            == torch.sign(x[:, K - 2].float()) * float("inf")).all()
+
+
 @pytest.mark.parametrize("g", [32, 64])
 @pytest.mark.parametrize("T,N,K", [(1, 192, 256), (20, 4096, 320), (20, 8192, 4096),
                                    (1, 6464, 4640), (1, 9664, 320), (1, 16448, 544),
