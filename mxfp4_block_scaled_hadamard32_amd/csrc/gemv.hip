@@ -715,16 +715,42 @@ int segment_blocks(const GemvArgs& a, int nt, int rows, int bytes) {
   return (int)(seg < nb4 ? seg : nb4);
 }
 
+constexpr int kLds = 128 * 1024;         // of a workgroup, at most
+constexpr int kLdsOfUnit = 160 * 1024;  // of a compute unit
+
+// LDS of a workgroup of gemv_kernel whose segments have `seg` blocks: terms and scale bytes, later the
+// waves' sums
+int lds_bytes(const GemvArgs& a, int nt, int rt, int wv, int seg) {
+  const int srows = a.gw == 1 ? 16 * rt : (16 * rt + a.gw - 1) / a.gw;
+  const int use = nt * seg * 64 * (int)a.T + srows * scale_pitch(seg), join = wv * rt * 1024;
+  return use > join ? use : join;
+}
+
 template <bool BF16, bool HAD, int NT, int RT, int WV, bool ONE = true>
-hipError_t launch_gemv(const GemvArgs& a, int bytes) {
+hipError_t launch_gemv(const GemvArgs& a) {
   const int64_t gx = (a.N + 16 * RT - 1) / (16 * RT);
-  const int seg = segment_blocks(a, NT, 16 * RT, bytes);
-  const int srows = a.gw == 1 ? 16 * RT : (16 * RT + a.gw - 1) / a.gw;
-  const size_t use = (size_t)NT * seg * 64 * a.T + (size_t)srows * scale_pitch(seg);
-  const size_t join = (size_t)WV * RT * 1024;
+  const int seg = segment_blocks(a, NT, 16 * RT, kLds);
   hipLaunchKernelGGL((gemv_kernel<BF16, HAD, NT, RT, WV, ONE>), dim3((unsigned)gx), dim3(64 * WV),
-                     use > join ? use : join, (hipStream_t)a.stream, a, seg);
+                     lds_bytes(a, NT, RT, WV, seg), (hipStream_t)a.stream, a, seg);
   return hipGetLastError();
+}
+
+// One token: how many codes are on the way is a matter of how many waves a compute unit holds, and
+// that of how many workgroups of 16 rows there are for it and how many its LDS has room for. Where it
+// would hold two workgroups at most, they have 8 waves, else 4. Where a single one fills LDS and
+// there are more of them than compute units, two row tiles halve the number of times that the
+// activations are brought in, rotated and split. (us with 4 waves | 8 waves | 8 waves and two tiles:
+// bf16 N 4096, K 8192 9.2 | 8.5 | 9.1; N 11008, K 4096 8.1 | 10.0 | 11.1; N 20480, K 28672 74 | 58 |
+// 70; rotated N 16384, K 8192 20.4 | 24.7 | 22.7; fp32 N 8192, K 14336 27.8 | 21.3 | 17.9.) Of 546
+// sizes (N 256 to 40960, K 512 to 28672, every type) it is 0.4% (bf16), 3.4% (rotated) and 1.1%
+// (fp32) from the best of these and two tiles with 4 waves, 1.44 times at worst (rotated, K 512).
+template <bool BF16, bool HAD, int NT>
+hipError_t launch_one(const GemvArgs& a) {
+  const int64_t wanted = (a.N + 16 * 256 - 1) / (16 * 256);
+  const int room = kLdsOfUnit / lds_bytes(a, NT, 1, 4, segment_blocks(a, NT, 16, kLds));
+  if (room == 1 && wanted > 1) return launch_gemv<BF16, HAD, NT, 2, 8>(a);
+  if (room <= 2 || wanted <= 2) return launch_gemv<BF16, HAD, NT, 1, 8>(a);
+  return launch_gemv<BF16, HAD, NT, 1, 4>(a);
 }
 
 template <bool BF16, bool HAD, int NT, int MT, int RT>
@@ -740,9 +766,6 @@ hipError_t launch_shared(const GemvArgs& a, float* part, int splits) {
                      0, (hipStream_t)a.stream, a, part, splits);
   return hipGetLastError();
 }
-
-constexpr int kLds = 128 * 1024;
-constexpr int64_t kWorkgroups = 200;  // about one a compute unit
 
 // All activations through LDS in one piece: for one token always (N 14336, K 4096: rotated 10.9 us,
 // 14.2 read directly; fp32 11.9 and 14.8; bf16, N 8192, K 28672: 26.9 and 30.1), and for very few
@@ -828,18 +851,9 @@ Plan plan_gemv(int64_t T, int64_t N, int64_t K, int nt, bool workspace) {
 
 template <bool BF16, bool HAD, int NT>
 hipError_t pick_gemv(const GemvArgs& a) {
-  if (takes_lds(a.T, a.N, a.K, NT)) {
-    if constexpr (NT > 1)
-      if (a.T > 1) return launch_gemv<BF16, HAD, NT, 1, 8, false>(a, kLds);
-    // Few workgroups need 8 waves each to keep enough codes coming (one bf16 token, N 8192, K 28672:
-    // 26.8 us, 30.6 with 4 waves); with many, 4 waves and in the end one row tile do better (N
-    // 14336, K 4096: 9.2 us with 2 tiles of 4 waves, 10.1 with 8; N 28672, K 8192: 30.2 us with 1
-    // tile of 4, 32.1 with 2, over 34 with 2 of 8)
-    if (a.N < 16 * 2 * kWorkgroups) return launch_gemv<BF16, HAD, NT, 1, 8>(a, kLds);
-    if (a.N < 16 * 3 * kWorkgroups) return launch_gemv<BF16, HAD, NT, 2, 8>(a, kLds);
-    if (a.N < 16 * 5 * kWorkgroups) return launch_gemv<BF16, HAD, NT, 2, 4>(a, kLds);
-    return launch_gemv<BF16, HAD, NT, 1, 4>(a, kLds);
-  }
+  if (a.T == 1) return launch_one<BF16, HAD, NT>(a);
+  if constexpr (NT > 1)
+    if (takes_lds(a.T, a.N, a.K, NT)) return launch_gemv<BF16, HAD, NT, 1, 8, false>(a);
   const Plan p = plan_gemv(a.T, a.N, a.K, NT, a.part != nullptr);
   if (p.parts == 0) {
     if constexpr (NT == 1)
