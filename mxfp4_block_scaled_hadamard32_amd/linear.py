@@ -221,6 +221,8 @@ class MXRMSNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, gamma, eps, quant=None):
         ctx.set_materialize_grads(False)
+        x, gamma = _readable(x), _readable(gamma)
+        residual = None if residual is None else _readable(residual)
         codes = scales = None
         if quant is None:
             y, s, rstd = mx_rmsnorm(x, gamma, residual, eps=eps)
@@ -251,19 +253,27 @@ class MXRMSNormFunction(torch.autograd.Function):
             (dg.to(gamma.dtype) if need_g else None), None, None
 
 
+def _readable(t: torch.Tensor) -> torch.Tensor:
+    """t (one or two dimensions) in a layout that the kernels read, a copy where it has to be: rows
+    without gaps between their elements, at 16-byte addresses (a view into a flat buffer may start
+    anywhere), one after the other (an expanded tensor repeats one)."""
+    row = t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else t.shape[-1]
+    if ((t.stride(-1) == 1 or t.shape[-1] <= 1) and t.data_ptr() % 16 == 0 and row >= t.shape[-1]
+            and (t.dim() == 1 or t.shape[0] <= 1 or row * t.element_size() % 16 == 0)):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 def _rows_of(grad: torch.Tensor, like: torch.Tensor) -> torch.Tensor:
-    """A gradient in the layout and type that the kernels read (an expanded one has no rows, a view
-    into a flat buffer may start anywhere)."""
-    grad = grad.to(like.dtype).contiguous()
-    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+    """A gradient in the layout and type that the kernels read."""
+    return _readable(grad.to(like.dtype))
 
 
 def _flat(t: torch.Tensor | None):
-    """[..., n] as [rows][n] with contiguous rows."""
+    """[..., n] as [rows][n]."""
     if t is None:
         return None
-    t = t.reshape(-1, t.shape[-1])
-    return t if t.stride(1) == 1 or t.shape[1] <= 1 else t.contiguous()
+    return t.reshape(-1, t.shape[-1])
 
 
 class MXRMSNorm(torch.nn.Module):
@@ -316,7 +326,7 @@ class MXDecodeLinear(torch.nn.Module):
             raise ValueError("w_block must be 1, 32 or 64")
         if w_block > 1 and spec.hadamard:
             raise ValueError("tiles are quantized without the Hadamard rotation")
-        w = weight.detach()
+        w = _readable(weight.detach())
         if w_block > 1:
             q, s = mx_quantize_2d_blocks(w, block=w_block, scale_rule=spec.scale_rule,
                                          transposed=False)[:2]
@@ -335,6 +345,6 @@ class MXDecodeLinear(torch.nn.Module):
 
     @torch.no_grad()
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        y = mx_gemv(_flat(x), self.codes, self.scales, self.w_block, hadamard=self.spec.hadamard,
+        y = mx_gemv(_readable(_flat(x)), self.codes, self.scales, self.w_block, hadamard=self.spec.hadamard,
                     sign_mask=self.spec.sign_mask, alpha_exp=_alpha(self.spec), out_dtype=x.dtype)
         return y.view(*x.shape[:-1], y.shape[1])

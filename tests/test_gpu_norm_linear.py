@@ -160,6 +160,57 @@ def test_norm_gradient_views_and_second_order(lin):
         dx.sum().backward()
 
 
+@pytest.mark.parametrize("layout", ["flat", "expanded", "odd", "windows", "columns"])
+def test_inputs_and_weights_in_any_layout(mx, lin, layout):
+    """Inputs and weights that are views into a flat buffer at any element, rows repeated or with
+    odd distances: outputs and gradients as for contiguous copies."""
+    T, K, N = 64, 128, 96
+
+    def lay(t):
+        if layout == "flat":
+            v = torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)
+            assert v.data_ptr() % 16
+        elif t.dim() == 1:
+            v = t
+        elif layout == "expanded":
+            v = t[:1].expand(t.shape)
+        elif layout == "odd":
+            v = torch.cat([t, t.new_zeros(t.shape[0], 3)], 1)[:, :K]
+        elif layout == "windows":
+            v = t.reshape(-1)[:K + 8 * (t.shape[0] - 1)].as_strided(t.shape, (8, 1))
+        else:
+            v = t.t().contiguous().t()
+        return v
+
+    x, r, _, dsum = (t.detach() for t in tensors(T, K, N))
+    dout = wl.normal((T, N), 1e-2, seed=8).to(torch.bfloat16).to(DEV)
+    gamma = (1.0 + wl.normal((1, K), 0.2, seed=9)[0]).to(DEV)
+    layer = lin.MXNormLinear(K, N, lin.MXLinearConfig())
+    vx, vr, vg = lay(x), lay(r), lay(gamma)
+
+    def step(x, r, g):
+        layer.norm.weight = torch.nn.Parameter(g)
+        layer.linear.cfg.seed = 5
+        x, r = x.detach().requires_grad_(True), r.detach().requires_grad_(True)
+        out, s = layer(x, r)
+        y, s2 = layer.norm(x.view(4, -1, K) if x.is_contiguous() else x, r.view(4, -1, K)
+                           if x.is_contiguous() else r)
+        alone = layer.norm(x)
+        grads = torch.autograd.grad((out, s, alone), (x, r, layer.norm.weight,
+                                                      layer.linear.weight), (dout, dsum, dsum))
+        return (out, s, y.reshape(T, K), s2.reshape(T, K), alone) + grads
+
+    for a, b in zip(step(vx, vr, vg), step(vx.clone(memory_format=torch.contiguous_format),
+                                           vr.clone(memory_format=torch.contiguous_format),
+                                           vg.clone())):
+        assert torch.equal(a, b)
+    w = layer.linear.weight.detach()
+    decode, plain = lin.MXDecodeLinear(lay(w)), lin.MXDecodeLinear(lay(w).clone(
+        memory_format=torch.contiguous_format))
+    assert torch.equal(decode.codes, plain.codes)
+    assert torch.equal(decode(vx), decode(vx.clone(memory_format=torch.contiguous_format)))
+
+
 def test_training_step_in_a_graph(lin):
     """Forward and backward of the half-layer captured once and replayed on new inputs; no eager
     graph of the same leaves is alive meanwhile."""
