@@ -362,6 +362,14 @@ def _scratch(size: int, device, stream):
         return torch.empty(size, dtype=torch.uint8, device=device)
 
 
+def _workspace(t, device) -> int:
+    """Bytes of a caller's workspace, after the checks of _buf."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    _buf(t, "workspace", (t.numel(),), _U8, device)
+    return t.numel()
+
+
 def _data(t):
     return None if t is None else t.data_ptr()
 
@@ -474,8 +482,7 @@ def mx_rmsnorm_backward(dy, s, gamma, rstd, dsum=None, with_dgamma: bool = True,
         else:
             _buf(dgamma, "dgamma", (cols,), _F32, dev)
         if workspace is not None:
-            size = workspace.numel()
-            _buf(workspace, "workspace", (size,), _U8, dev)
+            size = _workspace(workspace, dev)
         else:
             size = lib().mx_rmsnorm_backward_workspace(rows, cols)
             if size:  # small tensors want none
@@ -506,8 +513,7 @@ def mx_gemv(x, wq, ws, gw: int = 1, hadamard: int = 0, sign_mask: int = 0, alpha
         ldy = out.stride(0) if T > 1 else N
     dtype, size = _CODE[x.dtype], 0
     if workspace is not None:
-        size = workspace.numel()
-        _buf(workspace, "workspace", (size,), _U8, dev)
+        size = _workspace(workspace, dev)
     elif T > 1:  # one token wants none
         size = lib().mx_gemv_workspace(dtype, T, N, K, hadamard, code)
         if size:

@@ -288,6 +288,42 @@ def test_workspace(mx, orc, dtype):
     assert torch.equal(z, y)
 
 
+def test_a_workspace_that_is_none(mx):
+    """The binding's errors for workspaces of another kind, type, shape or device."""
+    x = torch.ones((4, 64), dtype=torch.bfloat16, device=DEV)
+    q, s = up(*weights(32, 64))
+    g, r = torch.ones(64, device=DEV), torch.ones(4, device=DEV)
+    for bad, error in ((b"0" * 64, TypeError), (64, TypeError),
+                       (torch.zeros(64, device=DEV), TypeError),
+                       (torch.zeros((8, 8), dtype=torch.uint8, device=DEV), ValueError),
+                       (torch.zeros(64, dtype=torch.uint8), ValueError),
+                       (torch.zeros(64, dtype=torch.uint8, device=DEV)[::2], ValueError)):
+        with pytest.raises(error):
+            mx.mx_gemv(x, q, s, workspace=bad)
+        with pytest.raises(error):
+            mx.mx_rmsnorm_backward(x, x, g, r, workspace=bad)
+
+
+@pytest.mark.parametrize("g", [1, 32, 64])
+@pytest.mark.parametrize("dtype,had", [("bf16", 0), ("bf16", 1), ("f32", 0), ("f32", 1)])
+@pytest.mark.parametrize("N,K", [(320, 2080),       # few workgroups
+                                 (9280, 1056),      # many, short rows
+                                 (12352, 28672),    # two or fewer in a compute unit's LDS
+                                 (4288, 40032)])    # a single one, K in several segments
+def test_shapes_for_one_token(mx, orc, N, K, dtype, had, g):
+    x = tokens(1, K, dtype)
+    gen = torch.Generator(device=DEV).manual_seed(N)
+    q = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV, generator=gen)
+    s = torch.randint(117, 137, (N // g, K // 32), dtype=torch.uint8, device=DEV, generator=gen)
+    cols = some(N)
+    p = torch.from_numpy(cols).to(DEV)
+    wq, ws = q[p].cpu().numpy(), s[p // g].cpu().numpy()
+    for out in (torch.float32, torch.bfloat16):
+        y = mx.mx_gemv(x.to(DEV), q, s, g, hadamard=had, sign_mask=MASK, alpha_exp=-5 * had,
+                       out_dtype=out)
+        check_outputs(orc, y[:, p], x, wq, ws, had)
+
+
 @pytest.mark.parametrize("T", [1, 18, 50])
 def test_leading_dimensions(mx, orc, T):
     K, N = 288, 77
