@@ -305,10 +305,11 @@ mx_status mx_rmsnorm_quant_mxfp8(const void* x, int64_t ldx, const void* residua
  *   dgamma[j] = sum over the rows of dy * z   (fp32; may be NULL).
  * fp32 throughout, dx rounded to dtype at the end; the order of every sum is fixed by the sizes.
  * dx may be dsum itself (same leading dimension), or without dgamma dy or s. With dgamma, workspace
- * holds at least mx_rmsnorm_backward_workspace(rows, cols) bytes (0 for small tensors), 16-byte
- * aligned; its contents are scratch, and calls that may run at the same time need one each. Sizes,
- * alignment and errors as for mx_rmsnorm; MX_ERR_ARG also for a workspace that is too small and for
- * dx that shares memory with dy or s when there is a dgamma. rows == 0 writes a zero dgamma. */
+ * holds at least mx_rmsnorm_backward_workspace(rows, cols) bytes (0 for small tensors of few
+ * rows), 16-byte aligned; its contents are scratch, and calls that may run at the same time need
+ * one each. Sizes, alignment and errors as for mx_rmsnorm; MX_ERR_ARG also for a workspace that is
+ * too small and for dx that shares memory with dy or s when there is a dgamma. rows == 0 writes a
+ * zero dgamma. */
 int64_t mx_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
 mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* dsum, int64_t ldds,
                               const void* s, int64_t lds, int32_t dtype, int64_t rows,

@@ -18,6 +18,11 @@ in the library's HIP kernels.
                   its result in the input's type and / or quantized in 1x32 blocks
   mx_rmsnorm_backward   gradients of the norm's input and weight
   mx_gemv         product of a few tokens (bf16 / fp32, not quantized) with MXFP4 weights
+
+Each takes the stream to run on (None: the current one). Outputs that a call allocates belong to the
+current stream's pool, scratch to that of the stream it runs on: a caller who passes another stream
+lets it wait for the current one before the call, and the current one for it before the outputs are
+used or freed.
 """
 from __future__ import annotations
 

@@ -767,8 +767,8 @@ hipError_t launch_shared(const GemvArgs& a, float* part, int splits) {
   return hipGetLastError();
 }
 
-// All activations through LDS in one piece: for one token always (N 14336, K 4096: rotated 10.9 us,
-// 14.2 read directly; fp32 11.9 and 14.8; bf16, N 8192, K 28672: 26.9 and 30.1), and for very few
+// All activations through LDS in one piece: for one token always (N 14336, K 4096: rotated 10.4 us,
+// 14.2 read directly; fp32 11.8 and 14.8; bf16, N 8192, K 28672: 26.3 and 30.1), and for very few
 // tokens that have to be rotated or split, few rows and a K that is not short, as long as two
 // workgroups a compute unit hold them (4 rotated tokens, N 4096, K 4128: 8.8 us, 10.7 with
 // gemv_shared_kernel; N 5120, K 512: 7.7 and 4.6; N 28672, K 1024: 15.5 and 7.5).
@@ -791,8 +791,11 @@ struct Plan {
 // estimated, in us, from what a workgroup does one after the other (chunks of 512 of K, in rounds of
 // 256 workgroups), what the machine does in all (codes), the blocks after the last chunk, and the
 // join. The constants are fitted to 2550 sizes (2 to 100 tokens, N 64 to 40960, K 256 to 28672, all
-// types; every shape of either kernel timed): the choice is 1 to 4% from the best one on average and
-// 1.5 times at worst, where thresholds on N and K were at 11 to 13% and up to 6 times.
+// types; every shape of either kernel timed), of which the choice is 1 to 4% from the best one on
+// average, where thresholds on N and K were at 11 to 13% and up to 6 times. Of 660 other sizes from
+// the same ranges it is 2.1% (bf16), 1.7% (rotated) and 0.2% (fp32) from the best; among those with
+// more than 40 MB of weights 4 to 7%, 1.3 to 1.5 times at worst, where K in parts would help more
+// than 128 groups too (8 bf16 tokens, N 34227, K 11456: 80.6 us, 60.3 in 8 parts of 128 rows).
 // Workgroups of 7 or 16 waves for gemv_shared_kernel were no better (16 rotated tokens, N 28672, K
 // 8192: 43.6 and 40.4 us, 37.4 with 8), nor more parts than one workgroup a compute unit (42.7).
 double shared_time(int64_t T, int64_t N, int64_t K, int nt, int tiles, int rt, int64_t parts) {

@@ -244,7 +244,8 @@ __device__ __forceinline__ RawChunk<BF16> raw_of(const float (&v)[8]) {
 // stores in it.
 // Bound by HBM: 16384 x 8192 bf16 with residual, y and E4M3 codes 205 to 228 us from card to card
 // (5.3 to 5.9 TB/s of 9 bytes an element; 225 to 231 on one with 4 to 12 waves a SIMD), 8192 x 4096
-// 58 us; rows of 128 by the vector ALU (26 us for 262144, 3.9 TB/s).
+// 59 us; rows of 128 by the vector ALU (25 to 28 us for 262144, 3.9 TB/s), as are stochastic rounding
+// and the rotation: to MXFP4 without y, 8192 x 4096, 43 us nearest, 59 stochastic, 79 and 87 rotated.
 template <bool BF16, int T, int V, int FMT, bool SR, bool RES>
 __global__ __launch_bounds__(T > 256 ? T : 256) void rmsnorm_kernel(const NormArgs a) {
   constexpr int kThreads = T > 256 ? T : 256;
@@ -425,8 +426,8 @@ hipError_t pick_norm_format(const NormArgs& a) {
 // A workgroup walks over rows like the forward kernel and keeps its columns' sums of dy z in
 // registers; rmsnorm_dgamma_kernel joins the workgroups' sums, partial[block][cols], in a fixed
 // order. Two rows and more a workgroup halve what it has to read.
-// Bound by HBM: 16384 x 8192 bf16 with dsum 194 us (5.5 TB/s of 8 bytes an element), 8192 x 4096 54
-// us, the join 4-6 us of either.
+// Bound by HBM: 16384 x 8192 bf16 with dsum 192 to 201 us (5.3 to 5.6 TB/s of 8 bytes an element),
+// 8192 x 4096 50 us; the join of either 4 to 5 us more.
 // SMALL (below): 512 threads also for narrow rows, for the columns' sake (4096 x 32 bf16: 6.1 us, 8.8
 // with 256 threads).
 template <bool BF16, int T, bool SMALL>
