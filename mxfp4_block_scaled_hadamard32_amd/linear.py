@@ -253,10 +253,12 @@ class MXRMSNormFunction(torch.autograd.Function):
             (dg.to(gamma.dtype) if need_g else None), None, None
 
 
-def _readable(t: torch.Tensor) -> torch.Tensor:
-    """t (one or two dimensions) in a layout that the kernels read, a copy where it has to be: rows
-    without gaps between their elements, at 16-byte addresses (a view into a flat buffer may start
-    anywhere), one after the other (an expanded tensor repeats one)."""
+def _readable(t):
+    """t (one or two dimensions; the binding refuses others) in a layout that the kernels read, a
+    copy where it has to be: rows without gaps between their elements, at 16-byte addresses (a view
+    into a flat buffer may start anywhere), one after the other (an expanded tensor repeats one)."""
+    if not isinstance(t, torch.Tensor) or t.dim() not in (1, 2):
+        return t
     row = t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else t.shape[-1]
     if ((t.stride(-1) == 1 or t.shape[-1] <= 1) and t.data_ptr() % 16 == 0 and row >= t.shape[-1]
             and (t.dim() == 1 or t.shape[0] <= 1 or row * t.element_size() % 16 == 0)):

@@ -231,6 +231,16 @@ def mx(monkeypatch):
     return mod
 
 
+def test_layers_refuse_what_the_binding_refuses(mx):
+    from mxfp4_block_scaled_hadamard32_amd import linear
+    layer = linear.MXNormLinear(64, 32, device="cpu")
+    for bad, error in ((None, TypeError), ([1.0], TypeError), (torch.zeros(2, 64).half(), TypeError),
+                       (torch.tensor(1.0), ValueError), (torch.zeros(64), ValueError),
+                       (torch.zeros(2, 64), ValueError), (torch.zeros(1, 2, 64), ValueError)):
+        with pytest.raises(error):
+            layer(bad)
+
+
 def test_binding_refuses_host_tensors_and_other_types(mx):
     x = torch.zeros((2, 64), dtype=torch.bfloat16)
     g, r = torch.ones(64), torch.ones(2)
