@@ -346,6 +346,85 @@ mx_status mx_gemv(const void* x, int32_t dtype, int64_t ldx, const uint8_t* wq, 
                   uint32_t sign_mask, int32_t alpha_exp, int32_t out_dtype, void* y, int64_t ldy,
                   void* workspace, int64_t workspace_bytes, void* stream);
 
+/* A paged cache of keys and values in 8 bits (decoding), and the sequences that one call is about.
+ * Codes are E4M3 or E5M2 (fmt, as for mx_quantize_mxfp8); one E8M0 scale serves a block of 32 tokens
+ * of one head. A page holds page_size tokens (a multiple of 32, at most 2048) of every head:
+ *   kq [n_pages][heads][page_size][dim]          a token's channels next to one another
+ *   vq [n_pages][heads][page_size / 32][dim][32] a channel's 32 tokens next to one another
+ *   ks, vs [n_pages][heads][page_size / 32]
+ * pages [seqs][table_width]: page p of a sequence holds its tokens p * page_size and following. An
+ * entry outside [0, n_pages) is no page: its tokens are not written, read as zeros and not attended
+ * to; so are tokens beyond the table. Sequences may share pages that nobody writes to.
+ * lengths [seqs]: tokens of each sequence, those of the call among them. offsets [seqs + 1]: rows
+ * offsets[b] .. offsets[b + 1] - 1 of the call's T rows are the newest tokens of sequence b, the last
+ * of them at position lengths[b] - 1; NULL: one row each, row b (T == seqs then). Rows that belong to
+ * no sequence (before the first, behind the last) are neither read nor written. offsets must not
+ * fall; pages, lengths and offsets are device memory, whose contents are not checked, but no content
+ * leads outside the tensors.
+ * dim is 64, 128, 192 or 256. kq and vq 16-byte aligned, the tables 4-byte. */
+typedef struct {
+  uint8_t* kq;
+  uint8_t* ks;
+  uint8_t* vq;
+  uint8_t* vs;
+  const int32_t* pages;
+  const int32_t* lengths;
+  const int32_t* offsets;
+  int64_t n_pages, seqs, table_width;
+  int32_t heads, dim, page_size, fmt;
+} mx_cache;
+
+/* Rows of keys, values, queries or outputs of a call: [T][heads][dim], `token` and `head` elements
+ * from one token and from one head to the next; channels contiguous. Pointers 16-byte aligned, both
+ * distances multiples of 16 bytes, at least dim (heads), and neither makes rows overlap. */
+typedef struct {
+  const void* p;
+  int64_t token, head;
+} mx_rows;
+
+/* Quantizes the keys and values of a call's T rows (dtype MX_BF16 or MX_F32) into the cache, round to
+ * nearest even. A block that receives tokens takes the scale byte of their largest magnitude
+ * (scale_rule, as for mx_quantize_mxfp8), or keeps its own where it already holds older tokens of the
+ * sequence and that is larger; where it grows the older codes are rounded again, to code * 2^(old -
+ * new). Scales are powers of two, so that changes a code only below the format's least normal. A
+ * token with an infinity or NaN makes its block's scale 0xFF and its tokens' codes zero, for good.
+ * Slots of a block behind its last token keep what they hold. Two rows of a call must not fall into
+ * one block from two sequences.
+ * Errors (nothing is launched): MX_ERR_NULL; MX_ERR_SHAPE (negative sizes, T != seqs without
+ * offsets, a distance below the rules); MX_ERR_ARG (dtype, fmt, scale_rule, page_size, alignment,
+ * rows inside the cache); MX_ERR_UNSUPPORTED (dim, more than 2^20 sequences, 2^24 rows, 65535 heads
+ * or 2^31 - 1 pages). T == 0 or heads == 0 is a no-op. */
+mx_status mx_cache_write(const mx_rows* k, const mx_rows* v, int32_t dtype, int64_t T,
+                         const mx_cache* cache, int32_t scale_rule, void* stream);
+
+/* The T newest tokens' keys and values back as code * 2^(scale - 127), rounded to dtype once; NaN
+ * where the scale is 0xFF, zeros where there is no page, or no token (more rows than the sequence
+ * has). Errors as for mx_cache_write, and MX_ERR_ARG for k and v that overlap. */
+mx_status mx_cache_read(const mx_rows* k, const mx_rows* v, int32_t dtype, int64_t T,
+                        const mx_cache* cache, void* stream);
+
+/* Causal attention of the T rows' q_heads query heads over the cache: query head h reads head
+ * h / (q_heads / heads) of it, and the row of position i the tokens 0 .. i:
+ *   out = sum_j p_j v_j,  p = softmax(scale * q . k_j).
+ * q and out: dtype, [T][q_heads][dim]; lse (optional, [T][q_heads] fp32, contiguous): the natural
+ * logarithm of the sum of exp(scale * q . k_j). A row that sees no token gets zeros and -infinity.
+ * Keys and values are exact; q . k is formed in fp32 from exact products (bf16 q, or fp32 q as three
+ * bf16 terms); the statistics and sums are fp32; the probabilities keep 16 bits for a bf16 output and
+ * 24 for fp32. Tokens whose scale is 0xFF make the rows that see them NaN (their lse with that of the
+ * keys), and only those. Codes of NaN or infinity, which mx_cache_write does not leave, are not provided for.
+ * Lengths are read on the device, and long contexts are divided there: a call may be captured and
+ * replayed with other lengths, pages and offsets. The order of the sums depends on the lengths of all
+ * sequences of the call.
+ * workspace: mx_cache_attention_workspace(...) bytes, 16-byte aligned, scratch: calls that may run at
+ * the same time need one each (or -1 for arguments that the call refuses).
+ * Errors as for mx_cache_write; MX_ERR_SHAPE for q_heads that is no multiple of heads; MX_ERR_ARG for
+ * a scale that is not finite, a workspace that is too small, and an out or lse that overlaps q or the
+ * other; MX_ERR_UNSUPPORTED for more than 65535 query heads. */
+int64_t mx_cache_attention_workspace(int64_t T, int64_t q_heads, const mx_cache* cache);
+mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, int32_t dtype,
+                             int64_t T, int64_t q_heads, float scale, const mx_cache* cache,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* mx_status_string(int32_t status);
 

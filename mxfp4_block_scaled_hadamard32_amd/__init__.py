@@ -18,6 +18,9 @@ in the library's HIP kernels.
                   its result in the input's type and / or quantized in 1x32 blocks
   mx_rmsnorm_backward   gradients of the norm's input and weight
   mx_gemv         product of a few tokens (bf16 / fp32, not quantized) with MXFP4 weights
+  mx_cache_write / mx_cache_read   keys and values into a paged cache of 8-bit codes with one scale
+                  for 32 tokens of a head, and back
+  mx_cache_attention   causal attention of each sequence's newest tokens over that cache
 
 Each takes the stream to run on (None: the current one). Outputs that a call allocates belong to the
 current stream's pool, scratch to that of the stream it runs on: a caller who passes another stream
@@ -32,12 +35,13 @@ import torch
 
 from . import _lib
 from ._lib import (MX_BF16, MX_E4M3, MX_E5M2, MX_F32, MX_ROUND_RNE, MX_ROUND_SR, MX_SCALE_CEIL,
-                   MX_SCALE_FLOOR, MxError, check, lib, mx_quant_opts)
+                   MX_SCALE_FLOOR, MxError, check, lib, mx_cache, mx_quant_opts, mx_rows)
 
 __all__ = ["mx_quantize", "mx_quantize_2d", "mx_dequantize", "mx_gemm_fprop", "mx_gemm_dgrad",
            "mx_gemm_wgrad", "mx_gemm_fprop_quant", "mx_quantize_mxfp8", "mx_gemm_mxfp8", "mx_quantize_2d_blocks",
            "mx_scale_mismatch_map", "mx_rmsnorm", "mx_rmsnorm_quant", "mx_rmsnorm_quant_mxfp8",
-           "mx_rmsnorm_backward", "mx_gemv", "MxError",
+           "mx_rmsnorm_backward", "mx_gemv", "mx_cache_write", "mx_cache_read",
+           "mx_cache_attention", "MxError",
            "MX_SCALE_FLOOR", "MX_SCALE_CEIL", "MX_ROUND_RNE", "MX_ROUND_SR", "MX_E4M3", "MX_E5M2",
            "lib"]
 
@@ -527,3 +531,128 @@ def mx_gemv(x, wq, ws, gw: int = 1, hadamard: int = 0, sign_mask: int = 0, alpha
             N, K, hadamard, sign_mask & 0xFFFFFFFF, alpha_exp, code, out.data_ptr(), ldy,
             _data(workspace), size)
     return out
+
+
+_I32 = (torch.int32,)
+
+
+def _cache(kq, ks, vq, vs, pages, lengths, offsets, T, fmt):
+    """Checks a cache and the tables of a call with T rows; returns its C view."""
+    if not isinstance(kq, torch.Tensor) or kq.dim() != 4 or not kq.is_cuda:
+        raise ValueError("kq must be a CUDA tensor [pages][heads][page][dim]")
+    n, H, P, D = kq.shape
+    dev = kq.device
+    if P % 32:
+        raise ValueError("a page holds a multiple of 32 tokens")
+    _buf(kq, "kq", (n, H, P, D), _U8, dev)
+    _buf(vq, "vq", (n, H, P // 32, D, 32), _U8, dev)
+    _buf(ks, "ks", (n, H, P // 32), _U8, dev)
+    _buf(vs, "vs", (n, H, P // 32), _U8, dev)
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 2:
+        raise ValueError("pages must be a tensor [sequences][pages]")
+    B, width = pages.shape
+    _buf(pages, "pages", (B, width), _I32, dev)
+    _buf(lengths, "lengths", (B,), _I32, dev)
+    if offsets is not None:
+        _buf(offsets, "offsets", (B + 1,), _I32, dev)
+    elif T != B:
+        raise ValueError(f"{T} rows for {B} sequences: offsets say which are whose")
+    return mx_cache(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), pages.data_ptr(),
+                    lengths.data_ptr(), _data(offsets), n, B, width, H, D, P, fmt)
+
+
+def _heads(t, name: str, heads, dim, device, like=None):
+    """A [T][heads][dim] CUDA tensor of bf16 or fp32 with contiguous channels (like: of that one's
+    shape and type); returns its C view."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _CODE:
+        raise TypeError(f"{name} must be bfloat16 or float32")
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [tokens][heads][dim] with contiguous channels")
+    if t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [T, "
+                         f"{'heads' if heads is None else heads}, {dim}]")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if like is not None and t.shape != like.shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    if like is not None and t.dtype != like.dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {like.dtype}")
+    return mx_rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _row_count(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens][heads][dim]")
+    return t.shape[0]
+
+
+def mx_cache_write(k, v, kq, ks, vq, vs, pages, lengths, offsets=None, fmt: int = MX_E4M3,
+                   scale_rule: int = MX_SCALE_FLOOR, stream=None) -> None:
+    """Quantizes keys and values [T][heads][dim] (bf16 or fp32, any distance of tokens and heads) into
+    a cache: kq [pages][heads][page][dim], vq [pages][heads][page / 32][dim][32] codes, ks, vs
+    [pages][heads][page / 32] scales, all uint8. pages [B][..] int32 is the page table, lengths [B]
+    int32 counts the sequences' tokens with these; rows offsets[b] .. offsets[b + 1] (int32, [B + 1])
+    are the newest of sequence b, without offsets row b is. A block of 32 tokens whose scale has to
+    grow rounds its older codes again."""
+    c = _cache(kq, ks, vq, vs, pages, lengths, offsets, _row_count(k, "k"), fmt)
+    T, H, D = k.shape[0], c.heads, c.dim
+    rk = _heads(k, "k", H, D, kq.device)
+    rv = _heads(v, "v", H, D, kq.device, k)
+    _launch("mx_cache_write", kq.device, stream, rk, rv, _CODE[k.dtype], T, c, scale_rule)
+
+
+def mx_cache_read(kq, ks, vq, vs, pages, lengths, offsets=None, rows=None, fmt: int = MX_E4M3,
+                  out_dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """Keys and values of the sequences' newest tokens back from a cache (as for mx_cache_write) ->
+    (k, v), [rows][heads][dim] of out_dtype. rows: how many there are, offsets[B] (without offsets one
+    for each sequence); rows of no sequence are left as they are, rows without a token are zeros."""
+    if k is None and rows is None:
+        if offsets is not None:
+            raise ValueError("with offsets, rows (or k and v) says how many rows there are")
+        rows = lengths.shape[0] if isinstance(lengths, torch.Tensor) and lengths.dim() == 1 else 0
+    T = rows if k is None else _row_count(k, "k")
+    c = _cache(kq, ks, vq, vs, pages, lengths, offsets, T, fmt)
+    H, D, dev = c.heads, c.dim, kq.device
+    if k is None or v is None:
+        if (k if k is not None else v) is not None:
+            raise ValueError("k and v are given together")
+        if out_dtype not in _CODE:
+            raise TypeError("out_dtype must be bfloat16 or float32")
+        k, v = torch.empty((2, T, H, D), dtype=out_dtype, device=dev)
+    rk, rv = _heads(k, "k", H, D, dev), _heads(v, "v", H, D, dev, k)
+    _launch("mx_cache_read", dev, stream, rk, rv, _CODE[k.dtype], T, c)
+    return k, v
+
+
+def mx_cache_attention(q, kq, ks, vq, vs, pages, lengths, offsets=None, scale=None,
+                       fmt: int = MX_E4M3, out=None, lse=None, with_lse: bool = False,
+                       workspace=None, stream=None):
+    """Causal attention of each sequence's newest tokens over its cache (as for mx_cache_write): q
+    [T][query heads][dim] bf16 or fp32, query head h over head h / (query heads / heads) of the cache,
+    each row over the tokens up to its own -> out of q's shape and type, or (out, lse [T][query heads]
+    fp32) with with_lse or an lse buffer. scale: dim ** -0.5 when None. workspace: a uint8 buffer of at
+    least lib().mx_cache_attention_workspace(...) bytes, allocated per call when None."""
+    c = _cache(kq, ks, vq, vs, pages, lengths, offsets, _row_count(q, "q"), fmt)
+    dev = kq.device
+    rq = _heads(q, "q", None, c.dim, dev)
+    T, heads = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    ro = _heads(out, "out", None, c.dim, dev, q)
+    if lse is not None:
+        _buf(lse, "lse", (T, heads), _F32, dev)
+    elif with_lse:
+        lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
+    if workspace is not None:
+        size = _workspace(workspace, dev)
+    else:
+        size = lib().mx_cache_attention_workspace(T, heads, c)
+        if size > 0:
+            workspace = _scratch(size, dev, stream)
+    _launch("mx_cache_attention", dev, stream, rq, ro, _data(lse), _CODE[q.dtype], T, heads,
+            c.dim ** -0.5 if scale is None else scale, c, _data(workspace), size)
+    return out if lse is None else (out, lse)

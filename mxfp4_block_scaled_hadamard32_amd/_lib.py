@@ -24,6 +24,17 @@ class mx_quant_opts(ctypes.Structure):
                 ("seed", ctypes.c_uint64)]
 
 
+class mx_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("kq", "ks", "vq", "vs", "pages", "lengths",
+                                               "offsets")] + \
+               [(n, ctypes.c_int64) for n in ("n_pages", "seqs", "table_width")] + \
+               [(n, ctypes.c_int32) for n in ("heads", "dim", "page_size", "fmt")]
+
+
+class mx_rows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
 class MxError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -72,10 +83,17 @@ def lib() -> ctypes.CDLL:
                           vp, i64, vp]
     L.mx_gemv_workspace.argtypes = [i32, i64, i64, i64, i32, i32]
     L.mx_gemv_workspace.restype = i64
+    cache, rows = ctypes.POINTER(mx_cache), ctypes.POINTER(mx_rows)
+    L.mx_cache_write.argtypes = [rows, rows, i32, i64, cache, i32, vp]
+    L.mx_cache_read.argtypes = [rows, rows, i32, i64, cache, vp]
+    L.mx_cache_attention.argtypes = [rows, rows, vp, i32, i64, i64, f32, cache, vp, i64, vp]
+    L.mx_cache_attention_workspace.argtypes = [i64, i64, cache]
+    L.mx_cache_attention_workspace.restype = i64
     for name in ("mx_quantize", "mx_quantize_2d", "mx_dequantize", "mx_gemm_fprop",
                  "mx_gemm_dgrad", "mx_gemm_wgrad", "mx_gemm_fprop_quant", "mx_quantize_mxfp8",
                  "mx_gemm_mxfp8", "mx_quantize_2d_blocks", "mx_scale_mismatch_map", "mx_rmsnorm",
-                 "mx_rmsnorm_quant", "mx_rmsnorm_quant_mxfp8", "mx_rmsnorm_backward", "mx_gemv"):
+                 "mx_rmsnorm_quant", "mx_rmsnorm_quant_mxfp8", "mx_rmsnorm_backward", "mx_gemv",
+                 "mx_cache_write", "mx_cache_read", "mx_cache_attention"):
         getattr(L, name).restype = ctypes.c_int
     L.mx_status_string.argtypes = [i32]
     L.mx_status_string.restype = ctypes.c_char_p

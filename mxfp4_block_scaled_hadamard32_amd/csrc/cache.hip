@@ -1,0 +1,915 @@
+// cache.hip — keys and values in a paged cache of 8-bit codes for gfx950: written as they come, read
+// back, and attended to.
+//
+// The cache is blocks of 32 tokens x one head: block (page * heads + head) * (page_size / 32) + i
+// holds 32 * dim code bytes (E4M3 or E5M2) of keys and as many of values, and one E8M0 scale byte
+// each. Key codes lie token after token ([32][dim]: the scores sum over dim), value codes channel
+// after channel ([dim][32]: the output sums over tokens), so that either product finds its
+// reduction index contiguous in memory and the attention transposes nothing.
+//
+// A block's scale serves all its 32 tokens, and tokens come one at a time: a block that already
+// holds some takes the larger of its scale and the new tokens' one. Scales are powers of two and
+// codes floating, so older codes are rounded again only where they fall below the least normal.
+#include "mx_device.h"
+#include "mx_launch.h"
+
+using namespace mxd;
+
+namespace {
+
+// the sequence of a call's rows: `n` newest tokens at rows row0 .. , `length` tokens in all
+struct Sequence {
+  int row0, n, length;
+};
+
+// Tables are device data: whatever they hold, rows stay inside [0, T) and pages inside the cache.
+__device__ __forceinline__ Sequence sequence_of(const CacheArgs& c, int b, int rows) {
+  Sequence s;
+  if (c.offsets) {
+    const int from = c.offsets[b], to = c.offsets[b + 1];
+    s.row0 = min(max(from, 0), rows);
+    s.n = max(min(to, rows) - s.row0, 0);
+  } else {
+    s.row0 = b;
+    s.n = b < rows ? 1 : 0;
+  }
+  s.length = max(c.lengths[b], 0);
+  return s;
+}
+
+// The block that holds positions 32 bn .. of sequence b, -1 where the table has no such page.
+// bn / page_blocks by a product: bn < 2^26 and page_blocks <= 64 keep it exact.
+__device__ __forceinline__ int64_t block_of(const CacheArgs& c, int b, int bn, int head) {
+  const int slot = c.page_blocks == 1 ? bn : (int)__umulhi((uint32_t)bn, c.page_magic);
+  if (bn < 0 || slot >= c.table_width) return -1;
+  const int page = c.pages[(int64_t)b * c.table_width + slot];
+  if (page < 0 || page >= c.n_pages) return -1;
+  return ((int64_t)page * c.heads + head) * c.page_blocks + (bn - slot * c.page_blocks);
+}
+
+// Which block of which sequence a workgroup of mx_cache_write or mx_cache_read has. A sequence whose
+// rows begin at o takes the units from o / 32 + 2 b on: n tokens touch (n + 30) / 32 + 1 blocks at
+// most, which fits below the next sequence's first unit.
+struct Piece {
+  int b, bn, lo, hi;  // slots lo .. hi - 1 of the block are rows row .. of the call
+  int row;
+};
+
+__device__ __forceinline__ bool piece_of(const CacheArgs& c, int unit, int rows, Piece& o) {
+  __shared__ int found;
+  int b = unit, j = 0;
+  if (c.offsets) {
+    if (threadIdx.x == 0) found = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < c.seqs; i += blockDim.x) {
+      const int first = (c.offsets[i] >> 5) + 2 * i, next = (c.offsets[i + 1] >> 5) + 2 * i + 2;
+      if (first <= unit && unit < next) found = i;
+    }
+    __syncthreads();
+    b = __builtin_amdgcn_readfirstlane(found);
+    if (b < 0) return false;
+    j = unit - ((c.offsets[b] >> 5) + 2 * b);
+  }
+  const Sequence s = sequence_of(c, b, rows);
+  const int start = s.length - s.n;  // negative with more rows than tokens
+  o.b = b;
+  o.bn = (start >> 5) + j;
+  o.lo = max(start - 32 * o.bn, 0);
+  o.hi = min(s.length - 32 * o.bn, 32);
+  o.row = s.row0 + 32 * o.bn - start;  // of slot 0
+  return o.lo < o.hi;
+}
+
+// 8 values of a row
+template <bool BF16>
+__device__ __forceinline__ void load8(const uint8_t* p, float (&v)[8]) {
+  if constexpr (BF16) {
+    widen_bf16x8(*reinterpret_cast<const u32x4*>(p), v);
+  } else {
+    const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(uint8_t* p, const float (&v)[8]) {
+  if constexpr (BF16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bf16x2_t t = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
+      w[i] = __builtin_bit_cast(uint32_t, t);
+    }
+    *reinterpret_cast<u32x4*>(p) = u32x4{w[0], w[1], w[2], w[3]};
+  } else {
+    reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
+    reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+  }
+}
+
+// four codes as they stand in a word, exact in fp32
+template <int FMT>
+__device__ __forceinline__ void decode4(uint32_t w, float (&v)[4]) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const f32x2 a = FMT == 0 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false)
+                           : __builtin_amdgcn_cvt_pk_f32_bf8((int)w, false);
+  const f32x2 b = FMT == 0 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true)
+                           : __builtin_amdgcn_cvt_pk_f32_bf8((int)w, true);
+  v[0] = a.x;
+  v[1] = a.y;
+  v[2] = b.x;
+  v[3] = b.y;
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  return fp8_rne_pair<FMT>(a, b) | (fp8_rne_pair<FMT>(c, d) << 16);
+}
+
+// 2^(byte - 127), exact, byte 0 .. 254 (0: the subnormal 2^-127)
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return byte ? __uint_as_float(byte << 23) : 0x1p-127f;
+}
+
+template <int N>
+__device__ __forceinline__ uint32_t workgroup_max(uint32_t m) {
+  __shared__ uint32_t part[N];
+#pragma unroll
+  for (int i = 1; i < 64; i *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, i));
+  if constexpr (N > 1) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = part[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) m = max(m, part[i]);
+  }
+  return m;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Writing. A workgroup of dim threads has the keys or the values of one block; a thread 32 of its
+// elements: of the keys four runs of 8 in a row, of the values 4 tokens x 8 channels, which make 8
+// words of a channel's 4 tokens each.
+// ---------------------------------------------------------------------------------------------
+template <int D, int FMT, bool BF16, bool CEIL>
+__global__ __launch_bounds__(D) void cache_write_kernel(const CacheArgs c, const CacheRows k,
+                                                        const CacheRows v) {
+  Piece p;
+  if (!piece_of(c, blockIdx.x, c.rows, p)) return;
+  const int head = blockIdx.y;
+  const bool values = blockIdx.z != 0;
+  const int64_t block = block_of(c, p.b, p.bn, head);
+  if (block < 0) return;
+  const CacheRows src = values ? v : k;
+  const int esize = BF16 ? 2 : 4;
+  const uint8_t* rows = static_cast<const uint8_t*>(src.p) + (int64_t)head * src.head * esize;
+  uint8_t* codes = (values ? c.vq : c.kq) + block * (32 * D);
+  uint8_t* scale = (values ? c.vs : c.ks) + block;
+  const int tid = threadIdx.x;
+  // token slot of run i, and its first channel
+  auto slot = [&](int i) { return values ? 4 * (tid & 7) + i : (tid + i * D) / (D / 8); };
+  auto channel = [&](int i) { return 8 * (values ? tid >> 3 : (tid + i * D) % (D / 8)); };
+  float w[4][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int s = slot(i);
+    if (s >= p.lo && s < p.hi)
+      load8<BF16>(rows + ((int64_t)(p.row + s) * src.token + channel(i)) * esize, w[i]);
+    else
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[i][j] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(w[i][j]));
+  }
+  const uint32_t was = p.lo > 0 ? *scale : 0u;
+  m = workgroup_max<D / 64>(m);
+  const uint32_t sb = max(scale_byte_fp8<CEIL, FMT>(m), was);
+  const bool bad = sb == 0xFFu;  // every code is zero
+  // 2^(127 - sb) for what is new; for what is there already 2^(was - sb), at most a flush to zero
+  const float up = bad ? 0.0f : __uint_as_float((254u - sb) << 23);
+  auto encode = [&](float a, float b, float cc, float d) {
+    return bad ? 0u : sb < 254u ? encode4<FMT>(a * up, b * up, cc * up, d * up)
+                                : encode4<FMT>(a * 0x1p-127f, b * 0x1p-127f, cc * 0x1p-127f, d * 0x1p-127f);
+  };
+  if (!values) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = slot(i);
+      if (s >= p.lo && s < p.hi)
+        *reinterpret_cast<uint2*>(codes + s * D + channel(i)) =
+            make_uint2(encode(w[i][0], w[i][1], w[i][2], w[i][3]),
+                       encode(w[i][4], w[i][5], w[i][6], w[i][7]));
+    }
+  } else {
+    const int s0 = slot(0), ch = channel(0);
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = encode(w[0][j], w[1][j], w[2][j], w[3][j]);
+    if (s0 >= p.lo && s0 + 4 <= p.hi) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) *reinterpret_cast<uint32_t*>(codes + (ch + j) * 32 + s0) = o[j];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (s0 + i >= p.lo && s0 + i < p.hi)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) codes[(ch + j) * 32 + s0 + i] = (uint8_t)(o[j] >> (8 * i));
+    }
+  }
+  if (sb != was || p.lo == 0) {
+    if (tid == 0) *scale = (uint8_t)sb;
+    // older codes, rounded to the larger scale
+    const float again = bad ? 0.0f : ldexpf(1.0f, (int)was - (int)sb);
+    auto coarser = [&](uint32_t word) {
+      float t[4];
+      decode4<FMT>(word, t);
+      return bad ? 0u : encode4<FMT>(t[0] * again, t[1] * again, t[2] * again, t[3] * again);
+    };
+    if (!values) {
+      for (int i = tid; i < p.lo * (D / 4); i += D) {
+        uint32_t* at = reinterpret_cast<uint32_t*>(codes) + i;
+        *at = coarser(*at);
+      }
+    } else {
+      // words of 4 tokens; in the last one the new tokens' bytes are other threads' to write
+      const int words = (p.lo + 3) / 4;
+      for (int i = tid; i < words * D; i += D) {
+        const int q = i / D, ch = i % D, left = min(p.lo - 4 * q, 4);
+        uint8_t* at = codes + ch * 32 + 4 * q;
+        const uint32_t o = coarser(*reinterpret_cast<const uint32_t*>(at));
+        if (left == 4)
+          *reinterpret_cast<uint32_t*>(at) = o;
+        else
+          for (int j = 0; j < left; ++j) at[j] = (uint8_t)(o >> (8 * j));
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Reading back: the same pieces. Positions that have no page (before the first token, too) are zeros.
+// ---------------------------------------------------------------------------------------------
+template <int D, int FMT, bool BF16>
+__global__ __launch_bounds__(D) void cache_read_kernel(const CacheArgs c, const CacheRows k,
+                                                       const CacheRows v) {
+  Piece p;
+  if (!piece_of(c, blockIdx.x, c.rows, p)) return;
+  const int head = blockIdx.y;
+  const bool values = blockIdx.z != 0;
+  const int64_t block = block_of(c, p.b, p.bn, head);
+  const CacheRows dst = values ? v : k;
+  const int esize = BF16 ? 2 : 4;
+  uint8_t* rows = static_cast<uint8_t*>(const_cast<void*>(dst.p)) + (int64_t)head * dst.head * esize;
+  const int tid = threadIdx.x;
+  const uint8_t* codes = block < 0 ? nullptr : (values ? c.vq : c.kq) + block * (32 * D);
+  const uint32_t sb = block < 0 ? 127u : (values ? c.vs : c.ks)[block];
+  const float f = sb == 0xFFu ? __uint_as_float(0x7FC00000u) : scale_of(sb);
+  float w[4][8];
+  if (block < 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[i][j] = 0.0f;
+  } else if (!values) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint2 q = *reinterpret_cast<const uint2*>(codes + 8 * (tid + i * D));
+      float a[4], b[4];
+      decode4<FMT>(q.x, a);
+      decode4<FMT>(q.y, b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[i][j] = a[j] * f;
+        w[i][4 + j] = b[j] * f;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float a[4];
+      decode4<FMT>(*reinterpret_cast<const uint32_t*>(codes + (8 * (tid >> 3) + j) * 32 + 4 * (tid & 7)), a);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i][j] = a[i] * f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int s = values ? 4 * (tid & 7) + i : (tid + i * D) / (D / 8);
+    const int ch = 8 * (values ? tid >> 3 : (tid + i * D) % (D / 8));
+    if (s >= p.lo && s < p.hi)
+      store8<BF16>(rows + ((int64_t)(p.row + s) * dst.token + ch) * esize, w[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Attention of a sequence's newest tokens over its cache.
+//
+// The rows that share a head of the cache, n tokens x `group` query heads, go 16 to a matrix
+// product; a wave takes TS tokens of the cache a step:
+//   S^T [tokens][rows] = K q^T     a 16 x 16 x 32 product's A row i is a token, its k 8 channels a lane
+//   O^T [channels][rows] += V^T P^T   A row i is a channel, k tokens
+// Lane (i, g) = (lane & 15, lane >> 4) gets of S^T the column (query row) i and 4 tokens of each of
+// its 16-token tiles. Tile t's row i is token (TS / 4) (i / 4) + 4 t + i % 4 of the step, so that lane
+// group g has the TS / 4 tokens from (TS / 4) g on: as P^T it is where the second product wants it, and
+// the value codes of a channel's same tokens are contiguous. Nothing is transposed or exchanged but
+// the maximum of a row, which four lanes hold.
+//
+// Codes become bf16 with their block's scale in the converter (exact: 4 bits and a power of two).
+// q goes in as it is (bf16) or as three bf16 terms that add up to the fp32 value; P as two terms,
+// 16 bits, for a bf16 result (its rounding, 2^-9, would otherwise be felt beside the result's own) and
+// as three for fp32. Sums and the softmax's statistics are fp32, exponentials to the base 2.
+//
+// Work is cut where the lengths say so, on the device: a sequence's rows, R = 16 WR at a time, are
+// an item; an item's steps are cut into chunks of c = (all items' steps) / target, a workgroup each.
+// The partial results of an item with several chunks go to the workspace, which a second kernel joins.
+// ---------------------------------------------------------------------------------------------
+constexpr int kWaves = 4;
+// chunks wanted over all heads: two workgroups for each of 256 compute units
+constexpr int kTarget = 512;
+
+// 4 channels of an output row: o / sum rounded to the output's type, and once a row its log sum of
+// exponentials; a row that sees no token is zeros, -inf
+template <bool BF16>
+__device__ __forceinline__ void store_row(const AttentionArgs& a, int64_t t, int qhead, int ch,
+                                          const f32x4& o, float base, float sum) {
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint8_t* p = static_cast<uint8_t*>(a.out) +
+               (t * a.out_token + (int64_t)qhead * a.out_head + ch) * (BF16 ? 2 : 4);
+  if constexpr (BF16) {
+    const bf16x2_t x = {(__bf16)(o[0] * f), (__bf16)(o[1] * f)};
+    const bf16x2_t y = {(__bf16)(o[2] * f), (__bf16)(o[3] * f)};
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y));
+  } else {
+    *reinterpret_cast<f32x4*>(p) = f32x4{o[0] * f, o[1] * f, o[2] * f, o[3] * f};
+  }
+  if (a.lse && ch == 0)
+    a.lse[t * a.heads + qhead] =
+        sum == 0.0f ? -__builtin_inff() : (base + __builtin_log2f(sum)) * 0.6931471805599453f;
+}
+
+__device__ __forceinline__ int64_t wave_sum(int64_t v) {
+#pragma unroll
+  for (int i = 1; i < 64; i *= 2) v += __shfl_xor(v, i);
+  return v;
+}
+
+// a workgroup's part: rows from `row` on of sequence b (R of them), chunk `kc` of `chunks`
+struct Unit {
+  int b, row, kc, chunks, chunk_steps;
+  int first, stride;  // the item's units: first, first + stride, ..
+};
+
+template <int R, int TS>
+__device__ __forceinline__ bool unit_of(const CacheArgs& c, const AttentionArgs& a, int unit, Unit& o) {
+  __shared__ int64_t sums[kWaves];
+  __shared__ int counts[kWaves], got[3];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  auto items = [&](const Sequence& s) { return (s.n * a.group + R - 1) / R; };
+  auto steps = [&](const Sequence& s) { return (min(s.length, c.max_tokens) + TS - 1) / TS; };
+  if (c.seqs == 1) {
+    const Sequence s = sequence_of(c, 0, c.rows);
+    const int n = items(s), st = steps(s);
+    const int cs = max((int)(((int64_t)n * st + a.target - 1) / a.target), 1);
+    o.chunks = max((st + cs - 1) / cs, 1);
+    if (unit >= n * o.chunks) return false;
+    o.b = 0;
+    o.kc = unit / n;
+    o.first = unit % n;
+    o.row = o.first * R;
+    o.stride = n;
+    o.chunk_steps = cs;
+    return true;
+  }
+  int64_t all = 0;
+  for (int b = tid; b < c.seqs; b += 64 * kWaves) {
+    const Sequence s = sequence_of(c, b, c.rows);
+    all += (int64_t)items(s) * steps(s);
+  }
+  all = wave_sum(all);
+  if (lane == 0) sums[wave] = all;
+  if (tid == 0) got[0] = -1;
+  __syncthreads();
+  all = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) all += sums[i];
+  const int cs = max((int)min((all + a.target - 1) / a.target, (int64_t)1 << 30), 1);
+  int before = 0;
+  for (int b0 = 0; b0 < c.seqs; b0 += 64 * kWaves) {  // the same turns in every wave
+    const int b = b0 + tid;
+    int n = 0, chunks = 1;
+    if (b < c.seqs) {
+      const Sequence s = sequence_of(c, b, c.rows);
+      n = items(s);
+      chunks = max((steps(s) + cs - 1) / cs, 1);
+    }
+    int end = n * chunks;
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) {
+      const int t = __shfl_up(end, i);
+      if (lane >= i) end += t;
+    }
+    if (lane == 63) counts[wave] = end;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      if (i < wave) end += counts[i];
+      total += counts[i];
+    }
+    end += before;
+    if (unit < end && unit >= end - n * chunks) {
+      got[0] = b;
+      got[1] = end - n * chunks;
+      got[2] = chunks;
+    }
+    before += total;
+    __syncthreads();
+    if (got[0] >= 0) break;
+  }
+  o.b = __builtin_amdgcn_readfirstlane(got[0]);
+  if (o.b < 0) return false;
+  const int n = items(sequence_of(c, o.b, c.rows));
+  const int base = __builtin_amdgcn_readfirstlane(got[1]), local = unit - base;
+  o.chunks = __builtin_amdgcn_readfirstlane(got[2]);
+  o.kc = local / n;
+  o.first = base + local % n;
+  o.row = local % n * R;
+  o.stride = n;
+  o.chunk_steps = cs;
+  return true;
+}
+
+// 16 codes as bf16 values times the scale
+template <int FMT>
+__device__ __forceinline__ bf16x8_t codes_of(uint32_t lo, uint32_t hi, float f) {
+  if constexpr (FMT == 0) {
+    const u32x4 o = {
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, false)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, f, true)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, false)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, f, true))};
+    return __builtin_bit_cast(bf16x8_t, o);
+  } else {
+    const u32x4 o = {
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, f, false)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, f, true)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, f, false)),
+        __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, f, true))};
+    return __builtin_bit_cast(bf16x8_t, o);
+  }
+}
+
+__device__ __forceinline__ f32x4 mfma(bf16x8_t a, bf16x8_t b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// the larger of a row's values, which lanes i, i + 16, i + 32 and i + 48 hold
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// what a step reads of the cache: key codes of its tokens, value codes, two scales
+template <int D, int TS>
+struct Step {
+  u32x4 k[TS / 16][D / 64];
+  uint32_t v[D / 16][TS / 16];
+  uint32_t ks, vs;  // this lane's block of keys and of values (the same two bytes in other lanes)
+  bool has[TS / 32];
+};
+
+template <int D, int FMT, bool BF16, int WR, int TS>
+__global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_kernel(const CacheArgs c,
+                                                                         const AttentionArgs a) {
+  constexpr int R = 16 * WR, TW = kWaves / WR;  // rows a workgroup; waves that share a row's tokens
+  constexpr int NQ = BF16 ? 1 : 3, NP = BF16 ? 2 : 3, KT = TS / 16, NB = TS / 32, PER = TS / 4;
+  __shared__ __attribute__((aligned(16))) float part[kWaves][16][D + 4];
+  __shared__ float stat[kWaves][16][2];
+  Unit u;
+  if (!unit_of<R, TS>(c, a, blockIdx.x, u)) return;
+  const int head = blockIdx.y;
+  const Sequence s = sequence_of(c, u.b, c.rows);
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wr = wave % WR, wt = wave / WR;
+  const int rows = s.n * a.group;               // of this sequence and head
+  const int row = u.row + 16 * wr + i;          // this lane's
+  const int token = min(row, rows - 1) / a.group, qhead = head * a.group + min(row, rows - 1) % a.group;
+  // how many tokens a row sees; rows past the end see what the last one does and are not stored
+  const int seen = min(s.length - s.n + token + 1, c.max_tokens);
+  const int wg_last = (min(u.row + R, rows) - 1) / a.group;  // the last token of the unit's rows
+  const int most = min(s.length - s.n + wg_last + 1, c.max_tokens);
+  const int first_token = min(u.row + 16 * wr, rows - 1) / a.group;
+  const int least = min(s.length - s.n + first_token + 1, c.max_tokens);  // of this wave's rows
+  const int end = u.row + 16 * wr < rows  // a wave may have no rows
+                      ? min((u.kc + 1) * u.chunk_steps, (max(most, 0) + TS - 1) / TS) : 0;
+
+  bf16x8_t q[NQ][D / 32];
+  {
+    const uint8_t* p = static_cast<const uint8_t*>(a.q) +
+                       ((int64_t)(s.row0 + token) * a.q_token + (int64_t)qhead * a.q_head) * (BF16 ? 2 : 4);
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {  // channels 64 (j / 2) + 16 g + 8 (j % 2) ..
+      const int ch = 64 * (j / 2) + 16 * g + 8 * (j % 2);
+      if constexpr (BF16) {
+        q[0][j] = *reinterpret_cast<const bf16x8_t*>(p + ch * 2);
+      } else {
+        float t[8];
+        load8<false>(p + ch * 4, t);
+        uint32_t o[4][3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_pair<3>(t[2 * e], t[2 * e + 1], o[e]);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+          q[n][j] = __builtin_bit_cast(bf16x8_t, u32x4{o[0][n], o[1][n], o[2][n], o[3][n]});
+      }
+    }
+  }
+
+  f32x4 acc[D / 16];
+#pragma unroll
+  for (int d = 0; d < D / 16; ++d) acc[d] = f32x4{0, 0, 0, 0};
+  float m = -__builtin_inff(), l = 0.0f;
+
+  auto load = [&](int step, Step<D, TS>& o) {
+    int64_t block[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int bn = NB * step + n;
+      block[n] = 32 * bn < most ? block_of(c, u.b, bn, head) : -1;
+      o.has[n] = block[n] >= 0;
+      block[n] = max(block[n], (int64_t)0);
+    }
+    const int64_t kb = NB == 1 ? block[0] : i >= 8 ? block[NB - 1] : block[0];
+    const int64_t vb = NB == 1 ? block[0] : g >= 2 ? block[NB - 1] : block[0];
+    o.ks = c.ks[kb];
+    o.vs = c.vs[vb];
+    const int krow = PER * ((i >> 2) & (NB == 1 ? 3 : 1)) + (i & 3);
+    const uint8_t* kp = c.kq + kb * (32 * D) + krow * D + 16 * g;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+        o.k[t][j] = *reinterpret_cast<const u32x4*>(kp + 4 * t * D + 64 * j);
+    const uint8_t* vp = c.vq + vb * (32 * D) + i * 32 + PER * (g & (NB == 1 ? 3 : 1));
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) {
+      if constexpr (KT == 4) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(vp + d * 512);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o.v[d][e] = w[e];
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(vp + d * 512);
+        o.v[d][0] = w.x;
+        o.v[d][1] = w.y;
+      }
+    }
+  };
+
+  auto use = [&](int step, Step<D, TS>& o) {
+    f32x4 sc[KT];
+    const bool nan_k = o.ks == 0xFFu, nan_v = o.vs == 0xFFu;
+    const float kf = nan_k ? 1.0f : scale_of(o.ks), vf = nan_v ? 1.0f : scale_of(o.vs);
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      sc[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const bf16x8_t k0 = codes_of<FMT>(o.k[t][j][0], o.k[t][j][1], kf);
+        const bf16x8_t k1 = codes_of<FMT>(o.k[t][j][2], o.k[t][j][3], kf);
+#pragma unroll
+        for (int n = NQ - 1; n >= 0; --n) {
+          sc[t] = mfma(k0, q[n][2 * j], sc[t]);
+          sc[t] = mfma(k1, q[n][2 * j + 1], sc[t]);
+        }
+      }
+    }
+    bool whole = (step + 1) * TS <= least;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) whole = whole && o.has[n];
+    // a block whose maximum was not finite: what sees it is NaN, and its codes are zero
+    const bool strange = __any(nan_k || nan_v);
+    float p[KT][4];
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) p[t][r] = sc[t][r] * a.scale_log2;
+    bool lost = false;  // this lane's tokens have no values
+    int here = PER;     // of this lane's tokens, those that its row sees
+    if (!whole || strange) {
+      // tokens PER g .. of the step are this lane's, in block g / 2 of two
+      const bool mine = NB == 1 ? o.has[0] : g >= 2 ? o.has[NB - 1] : o.has[0];
+      const int at = step * TS + PER * g;
+      here = mine ? min(seen - at, PER) : 0;
+      const int held = mine ? min(most - at, PER) : 0;  // that any row sees
+      // the scales of the block that this lane's scores come from
+      const uint32_t kb = NB == 1 ? o.ks : (uint32_t)__shfl((int)o.ks, g >= 2 ? 8 : 0);
+      const bool nan = kb == 0xFFu;
+      lost = nan_v;
+#pragma unroll
+      for (int t = 0; t < KT; ++t) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          p[t][r] = 4 * t + r < here ? nan ? __builtin_nanf("") : p[t][r] : -__builtin_inff();
+        const int left = nan_v ? 0 : min(max(held - 4 * t, 0), 4);
+        const uint32_t keep = left == 4 ? 0xFFFFFFFFu : (1u << (8 * left)) - 1u;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) o.v[d][t] &= keep;
+      }
+    }
+    float top = p[0][0];
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) top = fmaxf(top, p[t][r]);
+    top = row_max(top);
+    if (__any(top > m)) {
+      const float next = fmaxf(m, top);
+      const float f = next == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - next);
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[d][r] *= f;
+      m = next;
+    }
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        p[t][r] = __builtin_amdgcn_exp2f(p[t][r] - base);
+        l += p[t][r];
+      }
+    if (strange) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (lost && 4 * t + r < here) p[t][r] = __builtin_nanf("");
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {  // 8 tokens a lane: tiles 2b and 2b + 1
+      uint32_t w[4][NP];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        split_pair<NP>(p[2 * b + e / 2][2 * (e % 2)], p[2 * b + e / 2][2 * (e % 2) + 1], w[e]);
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        const bf16x8_t v = codes_of<FMT>(o.v[d][2 * b], o.v[d][2 * b + 1], vf);
+#pragma unroll
+        for (int n = NP - 1; n >= 0; --n)
+          acc[d] = mfma(v, __builtin_bit_cast(bf16x8_t, u32x4{w[0][n], w[1][n], w[2][n], w[3][n]}), acc[d]);
+      }
+    }
+  };
+
+  for (int step = u.kc * u.chunk_steps + wt; step < end; step += TW) {
+    Step<D, TS> o;
+    load(step, o);
+    use(step, o);
+  }
+
+  // the waves' parts of a row, joined in the waves' order
+  l = row_sum(l);
+  if (l != l) m = 0.0f;  // a NaN counts, whatever the maximum of the others
+  if (g == 0) {
+    stat[wave][i][0] = m;
+    stat[wave][i][1] = l;
+  }
+#pragma unroll
+  for (int d = 0; d < D / 16; ++d)
+    *reinterpret_cast<f32x4*>(&part[wave][i][16 * d + 4 * g]) = acc[d];
+  __syncthreads();
+  for (int e = tid; e < R * (D / 4); e += 64 * kWaves) {
+    const int r = e / (D / 4), ch = 4 * (e % (D / 4)), at = u.row + r;
+    if (at >= rows) break;
+    const int w0 = r / 16, ri = r % 16;
+    float top = -__builtin_inff(), sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < TW; ++w) top = fmaxf(top, stat[w0 + w * WR][ri][0]);
+    const float base = top == -__builtin_inff() ? 0.0f : top;
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < TW; ++w) {
+      const float f = __builtin_amdgcn_exp2f(stat[w0 + w * WR][ri][0] - base);
+      sum += stat[w0 + w * WR][ri][1] * f;
+      const f32x4 t = *reinterpret_cast<const f32x4*>(&part[w0 + w * WR][ri][ch]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] += t[x] * f;
+    }
+    const int64_t slot = ((int64_t)blockIdx.x * c.heads + head) * R + r;
+    if (u.chunks == 1) {
+      store_row<BF16>(a, (int64_t)s.row0 + at / a.group, head * a.group + at % a.group, ch, o, base, sum);
+    } else {
+      *reinterpret_cast<f32x4*>(a.part + slot * D + ch) = o;
+      if (ch == 0) {
+        a.stat[2 * slot] = top;
+        a.stat[2 * slot + 1] = sum;
+      }
+    }
+  }
+  if (u.kc == 0 && head == 0 && tid < R && u.row + tid < rows) {
+    const int at = u.row + tid;
+    a.where[(int64_t)s.row0 * a.group + at] = make_int4(u.first, u.stride, u.chunks, tid);
+  }
+}
+
+// The chunks of a row joined: a workgroup for each token and query head, 4 channels a thread, the
+// chunks among its groups of D / 4 threads.
+template <int D, bool BF16>
+__global__ __launch_bounds__(256) void cache_attention_join_kernel(const CacheArgs c,
+                                                                   const AttentionArgs a, int R,
+                                                                   int units) {
+  constexpr int PER = D / 4, GROUPS = 256 / PER;
+  __shared__ __attribute__((aligned(16))) float sums[GROUPS][D];
+  __shared__ float tops[4], all[GROUPS];
+  const int t = blockIdx.x, qhead = blockIdx.y, head = qhead / a.group, tid = threadIdx.x;
+  if (c.offsets && (t < c.offsets[0] || t >= c.offsets[c.seqs])) return;
+  const int4 w = a.where[(int64_t)t * a.group + qhead % a.group];
+  // one chunk: written already; and tables that are none (offsets that fall) end here
+  if (w.z <= 1 || w.x < 0 || w.y <= 0 || w.w < 0 || w.w >= R ||
+      (int64_t)w.x + (int64_t)(w.z - 1) * w.y >= units)
+    return;
+  auto slot = [&](int k) { return ((int64_t)(w.x + k * w.y) * c.heads + head) * R + w.w; };
+  float top = -__builtin_inff();
+  for (int k = tid; k < w.z; k += 256) top = fmaxf(top, a.stat[2 * slot(k)]);
+#pragma unroll
+  for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
+  if ((tid & 63) == 0) tops[tid >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+  const float base = top == -__builtin_inff() ? 0.0f : top;
+  const int group = tid / PER, ch = 4 * (tid % PER);
+  if (group < GROUPS) {
+    f32x4 o = {0, 0, 0, 0};
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int k = group; k < w.z; k += GROUPS) {
+      const int64_t s = slot(k);
+      const float f = __builtin_amdgcn_exp2f(a.stat[2 * s] - base);
+      sum += a.stat[2 * s + 1] * f;
+      const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + s * D + ch);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] += v[x] * f;
+    }
+    *reinterpret_cast<f32x4*>(&sums[group][ch]) = o;
+    if (ch == 0) all[group] = sum;
+  }
+  __syncthreads();
+  if (tid < PER) {
+    f32x4 o = {0, 0, 0, 0};
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < GROUPS; ++k) {
+      sum += all[k];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] += sums[k][4 * tid + x];
+    }
+    store_row<BF16>(a, t, qhead, 4 * tid, o, base, sum);
+  }
+}
+
+template <int D, int FMT, bool BF16>
+hipError_t launch_write(const CacheArgs& c, const CacheRows& k, const CacheRows& v, bool ceil,
+                        int64_t units, void* stream) {
+  const dim3 grid((unsigned)units, (unsigned)c.heads, 2);
+  if (ceil)
+    hipLaunchKernelGGL((cache_write_kernel<D, FMT, BF16, true>), grid, dim3(D), 0,
+                       (hipStream_t)stream, c, k, v);
+  else
+    hipLaunchKernelGGL((cache_write_kernel<D, FMT, BF16, false>), grid, dim3(D), 0,
+                       (hipStream_t)stream, c, k, v);
+  return hipGetLastError();
+}
+
+template <int D, int FMT, bool BF16>
+hipError_t launch_read(const CacheArgs& c, const CacheRows& k, const CacheRows& v, int64_t units,
+                       void* stream) {
+  hipLaunchKernelGGL((cache_read_kernel<D, FMT, BF16>), dim3((unsigned)units, (unsigned)c.heads, 2),
+                     dim3(D), 0, (hipStream_t)stream, c, k, v);
+  return hipGetLastError();
+}
+
+// dim, format and type of a call as template arguments
+template <template <int, int, bool> class F, int D, typename... A>
+hipError_t pick_type(const CacheArgs& c, bool bf16, A&&... args) {
+  if (c.fmt == 0) return bf16 ? F<D, 0, true>::run(c, args...) : F<D, 0, false>::run(c, args...);
+  return bf16 ? F<D, 1, true>::run(c, args...) : F<D, 1, false>::run(c, args...);
+}
+template <template <int, int, bool> class F, typename... A>
+hipError_t pick(const CacheArgs& c, bool bf16, A&&... args) {
+  switch (c.dim) {
+    case 64: return pick_type<F, 64>(c, bf16, args...);
+    case 128: return pick_type<F, 128>(c, bf16, args...);
+    case 192: return pick_type<F, 192>(c, bf16, args...);
+    default: return pick_type<F, 256>(c, bf16, args...);
+  }
+}
+
+template <int D, int FMT, bool BF16>
+struct Write {
+  static hipError_t run(const CacheArgs& c, const CacheRows& k, const CacheRows& v, bool ceil,
+                        int64_t units, void* stream) {
+    return launch_write<D, FMT, BF16>(c, k, v, ceil, units, stream);
+  }
+};
+template <int D, int FMT, bool BF16>
+struct Read {
+  static hipError_t run(const CacheArgs& c, const CacheRows& k, const CacheRows& v, int64_t units,
+                        void* stream) {
+    return launch_read<D, FMT, BF16>(c, k, v, units, stream);
+  }
+};
+
+// units of the calls' rows, see piece_of
+int64_t pieces(const CacheArgs& c) {
+  return c.offsets ? (int64_t)c.rows / 32 + 2 * (int64_t)c.seqs : c.seqs;
+}
+
+// tokens of a step: wider heads take fewer, for their registers
+constexpr int step_tokens(int dim) { return dim <= 128 ? 64 : 32; }
+
+struct AttentionPlan {
+  int wr;          // row tiles of a workgroup
+  int target;      // chunks wanted for each head, beside one for each item
+  int64_t units;   // workgroups for each head, at most
+  bool join;
+};
+
+AttentionPlan plan_attention(const CacheArgs& c, const AttentionArgs& a) {
+  AttentionPlan p;
+  const int64_t rows = (int64_t)c.rows * a.group;
+  const int64_t each = c.offsets ? (rows + c.seqs - 1) / c.seqs : a.group;
+  p.wr = each <= 16 ? 1 : each <= 32 ? 2 : 4;
+  const int64_t items = rows / (16 * p.wr) + c.seqs;
+  const int64_t steps = (c.max_tokens + step_tokens(c.dim) - 1) / step_tokens(c.dim);
+  p.target = (kTarget + c.heads - 1) / c.heads;
+  p.join = steps > 1;
+  p.units = p.join ? p.target + items : items;
+  if (p.join && items * steps < p.units) p.units = items * steps;
+  return p;
+}
+
+template <int D, int FMT, bool BF16>
+struct Attention {
+  template <int WR>
+  static void main(const CacheArgs& c, const AttentionArgs& a, const AttentionPlan& p) {
+    hipLaunchKernelGGL((cache_attention_kernel<D, FMT, BF16, WR, step_tokens(D)>),
+                       dim3((unsigned)p.units, (unsigned)c.heads), dim3(64 * kWaves), 0,
+                       (hipStream_t)a.stream, c, a);
+  }
+  static hipError_t run(const CacheArgs& c, const AttentionArgs& a, const AttentionPlan& p) {
+    if (p.wr == 1) main<1>(c, a, p);
+    else if (p.wr == 2) main<2>(c, a, p);
+    else main<4>(c, a, p);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess || !p.join) return e;
+    hipLaunchKernelGGL((cache_attention_join_kernel<D, BF16>), dim3((unsigned)c.rows, (unsigned)a.heads),
+                       dim3(256), 0, (hipStream_t)a.stream, c, a, 16 * p.wr, (int)p.units);
+    return hipGetLastError();
+  }
+};
+
+int64_t part_floats(const CacheArgs& c, const AttentionPlan& p) {
+  return p.join ? p.units * c.heads * 16 * p.wr : 0;
+}
+
+}  // namespace
+
+hipError_t mx_launch_cache_write(const CacheArgs& c, const CacheRows& k, const CacheRows& v,
+                                 bool bf16, bool ceil, void* stream) {
+  return pick<Write>(c, bf16, k, v, ceil, pieces(c), stream);
+}
+
+hipError_t mx_launch_cache_read(const CacheArgs& c, const CacheRows& k, const CacheRows& v,
+                                bool bf16, void* stream) {
+  return pick<Read>(c, bf16, k, v, pieces(c), stream);
+}
+
+int64_t mx_attention_units(const CacheArgs& c, const AttentionArgs& a) {
+  return plan_attention(c, a).units;
+}
+
+// [where: 16 bytes a row][part: D floats][stat: 2 floats] for each chunk's row
+int64_t mx_attention_workspace_bytes(const CacheArgs& c, const AttentionArgs& a) {
+  const AttentionPlan p = plan_attention(c, a);
+  return 16 * (int64_t)c.rows * a.group + part_floats(c, p) * (c.dim + 2) * 4;
+}
+
+hipError_t mx_launch_cache_attention(const CacheArgs& c, AttentionArgs a, void* workspace) {
+  const AttentionPlan p = plan_attention(c, a);
+  a.target = p.target;
+  a.where = static_cast<int4*>(workspace);
+  a.part = reinterpret_cast<float*>(a.where + (int64_t)c.rows * a.group);
+  a.stat = a.part + part_floats(c, p) * c.dim;
+  return pick<Attention>(c, a.bf16, a, p);
+}

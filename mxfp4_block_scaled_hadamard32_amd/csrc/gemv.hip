@@ -20,9 +20,6 @@ using namespace mxd;
 
 namespace {
 
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-
 // the 32 weights of a block (16 code bytes), times the block's scale: byte b is 2^(b - 127), byte 0
 // the subnormal 2^-127; byte 255 is an infinity here, which the converter takes as E8M0's NaN
 __device__ __forceinline__ void weights_of(u32x4 q, uint32_t scale, bf16x8_t (&w)[4]) {
@@ -44,26 +41,6 @@ __device__ __forceinline__ u32x4 load16_any(const uint8_t* p) {
   u32x4 v;
   __builtin_memcpy(&v, p, 16);
   return v;
-}
-
-// Two fp32 values as NT pairs of bf16 terms: a truncated first term, then what is left, truncated
-// again, then the rest; with NT = 3 the terms add up to the value exactly (down to bf16's least
-// subnormal), with NT = 2 the second one is rounded to nearest: 16 bits, 2^-17 of the value. The
-// remainder of an infinity is zero, not a NaN; a NaN stays one.
-template <int NT>
-__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&o)[NT]) {
-  const uint32_t ab = __float_as_uint(a), bb = __float_as_uint(b);
-  o[0] = __builtin_amdgcn_perm(bb, ab, 0x07060302u);
-  const float ah = __uint_as_float(ab & 0xFFFF0000u), bh = __uint_as_float(bb & 0xFFFF0000u);
-  float ar = a == ah ? 0.0f : a - ah, br = b == bh ? 0.0f : b - bh;
-  if constexpr (NT == 3) {
-    const uint32_t am = __float_as_uint(ar), bm = __float_as_uint(br);
-    o[1] = __builtin_amdgcn_perm(bm, am, 0x07060302u);
-    ar -= __uint_as_float(am & 0xFFFF0000u);
-    br -= __uint_as_float(bm & 0xFFFF0000u);
-  }
-  const bf16x2_t rest = {(__bf16)ar, (__bf16)br};
-  o[NT - 1] = __builtin_bit_cast(uint32_t, rest);
 }
 
 // a block's 32 values of x as they are in memory

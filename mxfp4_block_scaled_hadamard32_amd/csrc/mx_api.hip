@@ -157,6 +157,85 @@ mx_status rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
   return launch_status(mx_launch_rmsnorm(a));
 }
 
+// the cache of a call and its T rows, checked and as the kernels take it
+mx_status cache_args(const mx_cache* c, int64_t T, CacheArgs& o) {
+  if (!c) return MX_ERR_NULL;
+  if (T < 0 || c->n_pages < 0 || c->seqs < 0 || c->table_width < 0 || c->heads < 0) return MX_ERR_SHAPE;
+  if (c->fmt != MX_E4M3 && c->fmt != MX_E5M2) return MX_ERR_ARG;
+  if (c->page_size <= 0 || c->page_size % 32 || c->page_size > kCacheMaxPage) return MX_ERR_ARG;
+  if (c->dim != 64 && c->dim != 128 && c->dim != 192 && c->dim != 256) return MX_ERR_UNSUPPORTED;
+  if (c->seqs > ((int64_t)1 << 20) || T > ((int64_t)1 << 24) || c->heads > 65535 ||
+      c->n_pages > 0x7FFFFFFF || c->table_width > 0x7FFFFFFF)
+    return MX_ERR_UNSUPPORTED;
+  if (!c->offsets && T != c->seqs) return MX_ERR_SHAPE;
+  if (!aligned(c->kq, 16) || !aligned(c->vq, 16) || !aligned(c->pages, 4) ||
+      !aligned(c->lengths, 4) || !aligned(c->offsets, 4))
+    return MX_ERR_ARG;
+  if (T > 0 && c->seqs > 0 && c->heads > 0) {
+    if (!c->lengths || (c->table_width > 0 && !c->pages)) return MX_ERR_NULL;
+    if (c->n_pages > 0 && (!c->kq || !c->ks || !c->vq || !c->vs)) return MX_ERR_NULL;
+  }
+  o.kq = c->kq;
+  o.ks = c->ks;
+  o.vq = c->vq;
+  o.vs = c->vs;
+  o.pages = c->pages;
+  o.lengths = c->lengths;
+  o.offsets = c->offsets;
+  o.n_pages = (int)c->n_pages;
+  o.seqs = (int)c->seqs;
+  o.table_width = (int)c->table_width;
+  o.heads = c->heads;
+  o.dim = c->dim;
+  o.rows = (int)T;
+  o.page_blocks = c->page_size / 32;
+  o.page_magic = (uint32_t)((((uint64_t)1 << 32) + o.page_blocks - 1) / o.page_blocks);
+  const int64_t tokens = c->table_width * c->page_size, most = 0x7FFFFF00;
+  o.max_tokens = c->n_pages == 0 ? 0 : (int)(tokens < most ? tokens : most);
+  o.fmt = c->fmt;
+  return MX_OK;
+}
+
+// rows [T][heads][dim] and the bytes from the first to the last of them
+mx_status cache_rows(const mx_rows* r, int32_t dtype, int64_t T, int64_t heads, int64_t dim,
+                     CacheRows& o, Rows& span) {
+  if (!r) return MX_ERR_NULL;
+  if (dtype != MX_F32 && dtype != MX_BF16) return MX_ERR_ARG;
+  const int64_t esize = dtype == MX_BF16 ? 2 : 4, most = (int64_t)1 << 40;
+  if (!aligned(r->p, 16)) return MX_ERR_ARG;
+  if (r->token > most || r->head > most) return MX_ERR_SHAPE;
+  if (T > 0 && heads > 1 && (r->head < dim || (r->head * esize) % 16)) return MX_ERR_SHAPE;
+  if (heads > 0 && T > 1 && (r->token < dim || (r->token * esize) % 16)) return MX_ERR_SHAPE;
+  // one of the two distances holds all rows of the other: [T][heads] or [heads][T]
+  if (T > 1 && heads > 1 && r->token < (heads - 1) * r->head + dim &&
+      r->head < (T - 1) * r->token + dim)
+    return MX_ERR_SHAPE;
+  if (T > 0 && heads > 0 && !r->p) return MX_ERR_NULL;
+  o = CacheRows{r->p, T > 1 ? r->token : 0, heads > 1 ? r->head : 0};
+  span = T > 0 && heads > 0
+             ? Rows{r->p, 1, ((T - 1) * o.token + (heads - 1) * o.head + dim) * esize}
+             : Rows{nullptr, 1, 0};
+  return MX_OK;
+}
+
+// the T rows of two operands share a byte: whole extents, but rows that lie between one another
+// (token after token in one buffer, at the same distance) may
+bool rows_meet(const CacheRows& a, const Rows& sa, int64_t ha, const CacheRows& b, const Rows& sb,
+               int64_t hb, int64_t T, int64_t dim, int64_t esize) {
+  const int64_t wa = ((ha - 1) * a.head + dim) * esize, wb = ((hb - 1) * b.head + dim) * esize;
+  if (!sa.p || !sb.p) return false;
+  if (T > 1 && wa <= a.token * esize && wb <= b.token * esize)
+    return meet(Rows{a.p, a.token * esize, wa}, Rows{b.p, b.token * esize, wb}, T);
+  return meet(sa, sb, 1);
+}
+
+// rows inside the cache
+bool meets_cache(const Rows& span, const CacheArgs& c) {
+  const int64_t blocks = (int64_t)c.n_pages * c.heads * c.page_blocks, bytes = blocks * 32 * c.dim;
+  return meet(span, Rows{c.kq, 1, bytes}, 1) || meet(span, Rows{c.vq, 1, bytes}, 1) ||
+         meet(span, Rows{c.ks, 1, blocks}, 1) || meet(span, Rows{c.vs, 1, blocks}, 1);
+}
+
 }  // namespace
 
 extern "C" {
@@ -423,6 +502,80 @@ int64_t mx_gemv_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, int32_
                           int32_t out_dtype) {
   if (T <= 0 || N <= 0 || K <= 0 || T > kGemvMaxTokens || N > kGemvMaxRows) return 0;
   return mx_gemv_workspace_bytes(T, N, K, dtype == MX_BF16, hadamard == 1, out_dtype == MX_BF16);
+}
+
+mx_status mx_cache_write(const mx_rows* k, const mx_rows* v, int32_t dtype, int64_t T,
+                         const mx_cache* cache, int32_t scale_rule, void* stream) {
+  if (scale_rule != MX_SCALE_FLOOR && scale_rule != MX_SCALE_CEIL) return MX_ERR_ARG;
+  CacheArgs c{};
+  CacheRows rk, rv;
+  Rows sk, sv;
+  mx_status s = cache_args(cache, T, c);
+  if (s != MX_OK) return s;
+  if ((s = cache_rows(k, dtype, T, c.heads, c.dim, rk, sk)) != MX_OK) return s;
+  if ((s = cache_rows(v, dtype, T, c.heads, c.dim, rv, sv)) != MX_OK) return s;
+  if (meets_cache(sk, c) || meets_cache(sv, c)) return MX_ERR_ARG;
+  if (T == 0 || c.seqs == 0 || c.heads == 0 || c.max_tokens == 0) return MX_OK;
+  return launch_status(mx_launch_cache_write(c, rk, rv, dtype == MX_BF16, scale_rule == MX_SCALE_CEIL,
+                                             stream));
+}
+
+mx_status mx_cache_read(const mx_rows* k, const mx_rows* v, int32_t dtype, int64_t T,
+                        const mx_cache* cache, void* stream) {
+  CacheArgs c{};
+  CacheRows rk, rv;
+  Rows sk, sv;
+  mx_status s = cache_args(cache, T, c);
+  if (s != MX_OK) return s;
+  if ((s = cache_rows(k, dtype, T, c.heads, c.dim, rk, sk)) != MX_OK) return s;
+  if ((s = cache_rows(v, dtype, T, c.heads, c.dim, rv, sv)) != MX_OK) return s;
+  const int64_t esize = dtype == MX_BF16 ? 2 : 4;
+  if (meets_cache(sk, c) || meets_cache(sv, c) ||
+      rows_meet(rk, sk, c.heads, rv, sv, c.heads, T, c.dim, esize))
+    return MX_ERR_ARG;
+  if (T == 0 || c.seqs == 0 || c.heads == 0) return MX_OK;
+  return launch_status(mx_launch_cache_read(c, rk, rv, dtype == MX_BF16, stream));
+}
+
+int64_t mx_cache_attention_workspace(int64_t T, int64_t q_heads, const mx_cache* cache) {
+  CacheArgs c{};
+  if (cache_args(cache, T, c) != MX_OK || q_heads < 0 || q_heads > 65535) return -1;
+  if (T == 0 || q_heads == 0 || c.seqs == 0) return 0;
+  if (c.heads == 0 || q_heads % c.heads) return -1;
+  AttentionArgs a{};
+  a.heads = (int)q_heads;
+  a.group = (int)q_heads / c.heads;
+  return mx_attention_workspace_bytes(c, a);
+}
+
+mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, int32_t dtype,
+                             int64_t T, int64_t q_heads, float scale, const mx_cache* cache,
+                             void* workspace, int64_t workspace_bytes, void* stream) {
+  CacheArgs c{};
+  CacheRows rq, ro;
+  Rows sq, so;
+  mx_status s = cache_args(cache, T, c);
+  if (s != MX_OK) return s;
+  if (q_heads < 0) return MX_ERR_SHAPE;
+  if (q_heads > 65535) return MX_ERR_UNSUPPORTED;
+  if (c.heads == 0 ? q_heads != 0 : q_heads % c.heads != 0) return MX_ERR_SHAPE;
+  if (!(scale >= -3.402823466e+38f && scale <= 3.402823466e+38f)) return MX_ERR_ARG;
+  if ((s = cache_rows(q, dtype, T, q_heads, c.dim, rq, sq)) != MX_OK) return s;
+  if ((s = cache_rows(out, dtype, T, q_heads, c.dim, ro, so)) != MX_OK) return s;
+  if (!aligned(lse, 4) || !aligned(workspace, 16)) return MX_ERR_ARG;
+  if (T == 0 || q_heads == 0 || c.seqs == 0) return MX_OK;
+  const int64_t esize = dtype == MX_BF16 ? 2 : 4;
+  const Rows sl{lse, 1, T * q_heads * 4};
+  if (rows_meet(rq, sq, q_heads, ro, so, q_heads, T, c.dim, esize) || meets_cache(so, c) ||
+      meets_cache(sl, c) || meet(sl, so, 1) || meet(sl, sq, 1))
+    return MX_ERR_ARG;
+  AttentionArgs a{rq.p, const_cast<void*>(ro.p), lse, rq.token, rq.head, ro.token, ro.head,
+                  (int)q_heads, (int)q_heads / c.heads, scale * 1.4426950408889634f,
+                  dtype == MX_BF16, stream, 0, nullptr, nullptr, nullptr};
+  if (mx_attention_units(c, a) > 0x7FFFFFFF) return MX_ERR_UNSUPPORTED;
+  if (!workspace) return MX_ERR_NULL;
+  if (workspace_bytes < mx_attention_workspace_bytes(c, a)) return MX_ERR_ARG;
+  return launch_status(mx_launch_cache_attention(c, a, workspace));
 }
 
 const char* mx_status_string(int32_t status) {

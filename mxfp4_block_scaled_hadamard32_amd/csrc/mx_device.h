@@ -18,6 +18,8 @@ namespace mxd {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 // ---------------------------------------------------------------------------------------------
 // lane exchange inside a quad (4 consecutive lanes) through DPP quad_perm
@@ -48,6 +50,26 @@ __device__ __forceinline__ void widen_bf16x8(const u32x4 raw, float (&v)[8]) {
     v[2 * i] = __uint_as_float(w[i] << 16);
     v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
+}
+
+// Two fp32 values as NT pairs of bf16 terms: a truncated first term, then what is left, truncated
+// again, then the rest; with NT = 3 the terms add up to the value exactly (down to bf16's least
+// subnormal), with NT = 2 the second one is rounded to nearest: 16 bits, 2^-17 of the value. The
+// remainder of an infinity is zero, not a NaN; a NaN stays one.
+template <int NT>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&o)[NT]) {
+  const uint32_t ab = __float_as_uint(a), bb = __float_as_uint(b);
+  o[0] = __builtin_amdgcn_perm(bb, ab, 0x07060302u);
+  const float ah = __uint_as_float(ab & 0xFFFF0000u), bh = __uint_as_float(bb & 0xFFFF0000u);
+  float ar = a == ah ? 0.0f : a - ah, br = b == bh ? 0.0f : b - bh;
+  if constexpr (NT == 3) {
+    const uint32_t am = __float_as_uint(ar), bm = __float_as_uint(br);
+    o[1] = __builtin_amdgcn_perm(bm, am, 0x07060302u);
+    ar -= __uint_as_float(am & 0xFFFF0000u);
+    br -= __uint_as_float(bm & 0xFFFF0000u);
+  }
+  const bf16x2_t rest = {(__bf16)ar, (__bf16)br};
+  o[NT - 1] = __builtin_bit_cast(uint32_t, rest);
 }
 
 // ---------------------------------------------------------------------------------------------

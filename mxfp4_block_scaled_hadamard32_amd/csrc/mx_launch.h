@@ -1,5 +1,5 @@
 // mx_launch.h — internal interface between the C ABI layer (mx_api.hip) and the kernel
-// launchers (quant.hip, gemm.hip, norm.hip, gemv.hip). Arguments are already validated when these are called.
+// launchers (quant.hip, gemm.hip, norm.hip, gemv.hip, cache.hip, lora.hip). Arguments are already validated when these are called.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -135,3 +135,51 @@ struct GemvArgs {
 int64_t mx_gemv_workspace_bytes(int64_t T, int64_t N, int64_t K, bool bf16, bool hadamard,
                                 bool out_bf16);
 hipError_t mx_launch_gemv(const GemvArgs& a);
+
+// A paged cache of 8-bit keys and values (mx_cache of mx.h) and the rows of one call on it. Row r of
+// the call belongs to sequence r, or with offsets rows offsets[b] .. offsets[b + 1] to sequence b.
+struct CacheArgs {
+  uint8_t* kq;
+  uint8_t* ks;
+  uint8_t* vq;
+  uint8_t* vs;
+  const int32_t* pages;    // [seqs][table_width]
+  const int32_t* lengths;  // [seqs]
+  const int32_t* offsets;  // [seqs + 1] or NULL
+  int n_pages, seqs, table_width, heads, dim, rows;
+  int page_blocks;         // page size / 32, at most kCacheMaxPage / 32
+  uint32_t page_magic;     // 2^32 / page_blocks, rounded up
+  int max_tokens;          // what the table holds of a sequence, 0 without pages
+  int fmt;                 // 0 = E4M3, 1 = E5M2
+};
+constexpr int64_t kCacheMaxPage = 2048;
+
+// rows of keys, values, queries or outputs: [T][heads][dim] at any distance of tokens and heads
+struct CacheRows {
+  const void* p;
+  int64_t token, head;  // distances in elements
+};
+
+hipError_t mx_launch_cache_write(const CacheArgs& c, const CacheRows& k, const CacheRows& v,
+                                 bool bf16, bool ceil, void* stream);
+hipError_t mx_launch_cache_read(const CacheArgs& c, const CacheRows& k, const CacheRows& v,
+                                bool bf16, void* stream);
+
+struct AttentionArgs {
+  const void* q;
+  void* out;
+  float* lse;  // [T][heads] or NULL
+  int64_t q_token, q_head, out_token, out_head;
+  int heads, group;  // query heads, and how many share a head of the cache
+  float scale_log2;
+  bool bf16;
+  void* stream;
+  // set by the launcher
+  int target;
+  int4* where;
+  float* part;
+  float* stat;
+};
+int64_t mx_attention_units(const CacheArgs& c, const AttentionArgs& a);
+int64_t mx_attention_workspace_bytes(const CacheArgs& c, const AttentionArgs& a);
+hipError_t mx_launch_cache_attention(const CacheArgs& c, AttentionArgs a, void* workspace);
