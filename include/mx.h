@@ -425,6 +425,30 @@ mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, i
                              int64_t T, int64_t q_heads, float scale, const mx_cache* cache,
                              void* workspace, int64_t workspace_bytes, void* stream);
 
+/* Low-rank adapters of many requests beside a shared projection (mx_gemv's y, or any other base):
+ *   out[t] = base[t] + scaling[e] * B[e] (A[e] x[t]),   e = index[t],
+ * a [adapters][rank][K] and b [adapters][N][rank], contiguous, of x's type (MX_BF16 or MX_F32); index
+ * [T] int32 in any order: a token whose index is outside [0, adapters) gets base alone. scaling
+ * [adapters] fp32 may be NULL (1), and base may be NULL (0). x [T][ldx], base [T][ldb] and out [T][ldo]
+ * have types and leading dimensions of their own; out may be base itself. K and rank are multiples of
+ * 8, rank at most 128, T, N and the number of adapters arbitrary. x and its rows 16-byte aligned, a
+ * and b 16-byte, base and out aligned to their elements (rows at 16-byte addresses are faster).
+ * A x, the sum over the rank, scaling and the addition are fp32, rounded once, to out's type; A x of
+ * bf16 operands has exact products. A token's output depends on its own adapter and the call's sizes,
+ * not on the other tokens.
+ * workspace: mx_lora_workspace(...) bytes, 16-byte aligned, scratch: calls that may run at the same
+ * time need one each.
+ * Errors (nothing is launched): MX_ERR_SHAPE, MX_ERR_ARG (types, alignment, a workspace that is too
+ * small, an out that overlaps x or, without being it, base), MX_ERR_NULL, MX_ERR_UNSUPPORTED (rank
+ * above 128, T above 2^21, N, K or adapters above 2^26). T == 0 or N == 0 is a no-op; no adapters, or
+ * K == 0 or rank == 0, leave base alone. */
+int64_t mx_lora_workspace(int64_t T, int64_t K, int64_t adapters, int64_t rank);
+mx_status mx_lora(const void* x, int32_t dtype, int64_t ldx, const void* a, const void* b,
+                  int64_t adapters, int64_t rank, const int32_t* index, const float* scaling,
+                  const void* base, int32_t base_dtype, int64_t ldb, int64_t T, int64_t N, int64_t K,
+                  int32_t out_dtype, void* out, int64_t ldo, void* workspace,
+                  int64_t workspace_bytes, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* mx_status_string(int32_t status);
 

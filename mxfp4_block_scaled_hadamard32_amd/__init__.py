@@ -21,6 +21,7 @@ in the library's HIP kernels.
   mx_cache_write / mx_cache_read   keys and values into a paged cache of 8-bit codes with one scale
                   for 32 tokens of a head, and back
   mx_cache_attention   causal attention of each sequence's newest tokens over that cache
+  mx_lora         low-rank adapters, each token its own, beside a shared projection
 
 Each takes the stream to run on (None: the current one). Outputs that a call allocates belong to the
 current stream's pool, scratch to that of the stream it runs on: a caller who passes another stream
@@ -41,7 +42,7 @@ __all__ = ["mx_quantize", "mx_quantize_2d", "mx_dequantize", "mx_gemm_fprop", "m
            "mx_gemm_wgrad", "mx_gemm_fprop_quant", "mx_quantize_mxfp8", "mx_gemm_mxfp8", "mx_quantize_2d_blocks",
            "mx_scale_mismatch_map", "mx_rmsnorm", "mx_rmsnorm_quant", "mx_rmsnorm_quant_mxfp8",
            "mx_rmsnorm_backward", "mx_gemv", "mx_cache_write", "mx_cache_read",
-           "mx_cache_attention", "MxError",
+           "mx_cache_attention", "mx_lora", "MxError",
            "MX_SCALE_FLOOR", "MX_SCALE_CEIL", "MX_ROUND_RNE", "MX_ROUND_SR", "MX_E4M3", "MX_E5M2",
            "lib"]
 
@@ -656,3 +657,52 @@ def mx_cache_attention(q, kq, ks, vq, vs, pages, lengths, offsets=None, scale=No
     _launch("mx_cache_attention", dev, stream, rq, ro, _data(lse), _CODE[q.dtype], T, heads,
             c.dim ** -0.5 if scale is None else scale, c, _data(workspace), size)
     return out if lse is None else (out, lse)
+
+
+def mx_lora(x, a, b, index, base=None, scaling=None, out_dtype=None, out=None, workspace=None,
+            stream=None):
+    """out[t] = base[t] + scaling[e] b[e] (a[e] x[t]) with e = index[t], each token's own adapter: x
+    [T][K], a [E][rank][K], b [E][N][rank] bf16 or fp32 of one type (K and rank multiples of 8, rank
+    at most 128), index [T] int32 (outside [0, E): base alone), base [T][N] bf16 or fp32 or None
+    (zeros), scaling [E] fp32 or None (ones) -> out [T][N] of out_dtype (base's type when None, x's
+    without a base). out may be base itself. workspace: a uint8 buffer of at least
+    lib().mx_lora_workspace(T, K, E, rank) bytes, allocated per call when None."""
+    T, K, ldx = _rows(x, "x")
+    dev = x.device
+    for t, name in ((a, "a"), (b, "b")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != 3:
+            raise ValueError(f"{name} must have three dimensions")
+    E, rank, N = a.shape[0], a.shape[1], b.shape[1]
+    same = (x.dtype,)
+    _buf(a, "a", (E, rank, K), same, dev)
+    _buf(b, "b", (E, N, rank), same, dev)
+    _buf(index, "index", (T,), _I32, dev)
+    if scaling is not None:
+        _buf(scaling, "scaling", (E,), _F32, dev)
+    base_code = ldb = 0
+    if base is not None:
+        rows, cols, ldb = _rows(base, "base")
+        if (rows, cols) != (T, N):
+            raise ValueError(f"base has shape {tuple(base.shape)}, expected {(T, N)}")
+        if base.device != dev:
+            raise ValueError(f"base is on {base.device}, expected {dev}")
+        base_code = _CODE[base.dtype]
+    if out is None and out_dtype is None:
+        out_dtype = x.dtype if base is None else base.dtype
+    if out is None and out_dtype in _CODE:
+        out, code, ldo = torch.empty(T, N, dtype=out_dtype, device=dev), _CODE[out_dtype], N
+    else:
+        out, code = _out(out, T, N, out.dtype if out_dtype is None else out_dtype, dev)
+        ldo = out.stride(0) if T > 1 else N
+    if workspace is not None:
+        size = _workspace(workspace, dev)
+    else:
+        size = lib().mx_lora_workspace(T, K, E, rank)
+        if size:
+            workspace = _scratch(size, dev, stream)
+    _launch("mx_lora", dev, stream, x.data_ptr(), _CODE[x.dtype], ldx if K else 0, a.data_ptr(), b.data_ptr(), E,
+            rank, index.data_ptr(), _data(scaling), _data(base), base_code, ldb, T, N, K, code,
+            out.data_ptr(), ldo, _data(workspace), size)
+    return out

@@ -89,11 +89,15 @@ def lib() -> ctypes.CDLL:
     L.mx_cache_attention.argtypes = [rows, rows, vp, i32, i64, i64, f32, cache, vp, i64, vp]
     L.mx_cache_attention_workspace.argtypes = [i64, i64, cache]
     L.mx_cache_attention_workspace.restype = i64
+    L.mx_lora.argtypes = [vp, i32, i64, vp, vp, i64, i64, vp, vp, vp, i32, i64, i64, i64, i64, i32,
+                          vp, i64, vp, i64, vp]
+    L.mx_lora_workspace.argtypes = [i64, i64, i64, i64]
+    L.mx_lora_workspace.restype = i64
     for name in ("mx_quantize", "mx_quantize_2d", "mx_dequantize", "mx_gemm_fprop",
                  "mx_gemm_dgrad", "mx_gemm_wgrad", "mx_gemm_fprop_quant", "mx_quantize_mxfp8",
                  "mx_gemm_mxfp8", "mx_quantize_2d_blocks", "mx_scale_mismatch_map", "mx_rmsnorm",
                  "mx_rmsnorm_quant", "mx_rmsnorm_quant_mxfp8", "mx_rmsnorm_backward", "mx_gemv",
-                 "mx_cache_write", "mx_cache_read", "mx_cache_attention"):
+                 "mx_cache_write", "mx_cache_read", "mx_cache_attention", "mx_lora"):
         getattr(L, name).restype = ctypes.c_int
     L.mx_status_string.argtypes = [i32]
     L.mx_status_string.restype = ctypes.c_char_p

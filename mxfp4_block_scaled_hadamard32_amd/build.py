@@ -12,7 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmx.so")
-SOURCES = ["mx_api.hip", "quant.hip", "gemm.hip", "norm.hip", "gemv.hip", "cache.hip"]
+SOURCES = ["mx_api.hip", "quant.hip", "gemm.hip", "norm.hip", "gemv.hip", "cache.hip", "lora.hip"]
 # measurement aid for the matrix-core roofline (include/mx_probe.h), a library of its own
 PROBE_LIB = os.path.join(HERE, "libmx_probe.so")
 PROBE_SOURCES = ["mfma_probe.hip"]

@@ -183,3 +183,25 @@ struct AttentionArgs {
 int64_t mx_attention_units(const CacheArgs& c, const AttentionArgs& a);
 int64_t mx_attention_workspace_bytes(const CacheArgs& c, const AttentionArgs& a);
 hipError_t mx_launch_cache_attention(const CacheArgs& c, AttentionArgs a, void* workspace);
+
+// out[t] = base[t] + scaling[e] B[e] (A[e] x[t]), e = index[t]; a [E][r][K] and b [E][N][r] of x's type
+constexpr int64_t kLoraMaxTokens = (int64_t)1 << 21, kLoraMaxRank = 128, kLoraMaxSize = (int64_t)1 << 26;
+struct LoraArgs {
+  const void* x;
+  const void* a;
+  const void* b;
+  const int32_t* index;
+  const float* scaling;  // [E] or NULL
+  const void* base;      // or NULL
+  void* out;
+  float* h;              // workspace: [parts][T][r]
+  int64_t ldx, ldb, ldo;
+  int T, N, K, E, r;
+  bool bf16, base_bf16, out_bf16, base_wide, out_wide;  // wide: rows at 16-byte addresses
+  bool in_place;         // out is base
+  void* stream;
+  int candidates, parts;  // set by the launcher, as by_token
+  bool by_token;
+};
+int64_t mx_lora_workspace_bytes(int64_t T, int64_t K, int64_t E, int64_t r);
+hipError_t mx_launch_lora(LoraArgs a);
