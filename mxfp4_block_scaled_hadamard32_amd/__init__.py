@@ -31,12 +31,13 @@ used or freed.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
 from . import _lib
 from ._lib import (MX_BF16, MX_E4M3, MX_E5M2, MX_F32, MX_ROUND_RNE, MX_ROUND_SR, MX_SCALE_CEIL,
-                   MX_SCALE_FLOOR, MxError, check, lib, mx_cache, mx_quant_opts, mx_rows)
+                   MX_SCALE_FLOOR, MxError, check, lib, mx_quant_opts)
 
 __all__ = ["mx_quantize", "mx_quantize_2d", "mx_dequantize", "mx_gemm_fprop", "mx_gemm_dgrad",
            "mx_gemm_wgrad", "mx_gemm_fprop_quant", "mx_quantize_mxfp8", "mx_gemm_mxfp8", "mx_quantize_2d_blocks",
@@ -535,10 +536,44 @@ def mx_gemv(x, wq, ws, gw: int = 1, hadamard: int = 0, sign_mask: int = 0, alpha
 
 
 _I32 = (torch.int32,)
+# mx_cache and mx_rows of mx.h as bytes: a third of the time that ctypes structures take
+_pack_cache = struct.Struct("@7P3q4i").pack
+_pack_rows = struct.Struct("@P2q").pack
 
 
 def _cache(kq, ks, vq, vs, pages, lengths, offsets, T, fmt):
-    """Checks a cache and the tables of a call with T rows; returns its C view."""
+    """Checks a cache and the tables of a call with T rows; returns its C view, its heads and dim and
+    the device's index."""
+    u8, i32 = torch.uint8, torch.int32
+    try:
+        n, H, P, D = kq.shape
+        B, width = pages.shape
+        at, block = kq.get_device(), (n, H, P >> 5)
+        good = (kq.dtype is u8 and ks.dtype is u8 and vq.dtype is u8 and vs.dtype is u8
+                and pages.dtype is i32 and lengths.dtype is i32 and P & 31 == 0
+                and ks.shape == block and vs.shape == block and vq.shape == block + (D, 32)
+                and lengths.shape == (B,) and at >= 0 and ks.get_device() == at
+                and vq.get_device() == at and vs.get_device() == at and pages.get_device() == at
+                and lengths.get_device() == at and kq.is_contiguous() and ks.is_contiguous()
+                and vq.is_contiguous() and vs.is_contiguous() and pages.is_contiguous()
+                and lengths.is_contiguous())
+        if offsets is None:
+            good, table = good and T == B, 0
+        else:
+            good = (good and offsets.dtype is i32 and offsets.shape == (B + 1,)
+                    and offsets.get_device() == at and offsets.is_contiguous())
+            table = offsets.data_ptr()
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _cache_refusal(kq, ks, vq, vs, pages, lengths, offsets, T)
+    return _pack_cache(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(),
+                       pages.data_ptr(), lengths.data_ptr(), table, n, B, width, H, D, P,
+                       fmt), H, D, at
+
+
+def _cache_refusal(kq, ks, vq, vs, pages, lengths, offsets, T):
+    """Says what is wrong with a cache and its tables."""
     if not isinstance(kq, torch.Tensor) or kq.dim() != 4 or not kq.is_cuda:
         raise ValueError("kq must be a CUDA tensor [pages][heads][page][dim]")
     n, H, P, D = kq.shape
@@ -556,39 +591,58 @@ def _cache(kq, ks, vq, vs, pages, lengths, offsets, T, fmt):
     _buf(lengths, "lengths", (B,), _I32, dev)
     if offsets is not None:
         _buf(offsets, "offsets", (B + 1,), _I32, dev)
-    elif T != B:
-        raise ValueError(f"{T} rows for {B} sequences: offsets say which are whose")
-    return mx_cache(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), pages.data_ptr(),
-                    lengths.data_ptr(), _data(offsets), n, B, width, H, D, P, fmt)
+    raise ValueError(f"{T} rows for {B} sequences: offsets say which are whose")
 
 
-def _heads(t, name: str, heads, dim, device, like=None):
-    """A [T][heads][dim] CUDA tensor of bf16 or fp32 with contiguous channels (like: of that one's
-    shape and type); returns its C view."""
+def _heads(t, name: str, heads, dim, at, like=None):
+    """A [T][heads][dim] tensor of bf16 or fp32 on device `at` with contiguous channels (like: of that
+    one's shape and type); returns its C view."""
+    try:
+        _, n, d = t.shape
+        token, head, one = t.stride()
+        if (t.dtype in _CODE and d == dim and one == 1 and t.get_device() == at
+                and (n == heads if like is None else t.shape == like.shape and t.dtype is like.dtype)):
+            return _pack_rows(t.data_ptr(), token, head)
+    except (AttributeError, TypeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _CODE:
         raise TypeError(f"{name} must be bfloat16 or float32")
     if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
         raise ValueError(f"{name} must be [tokens][heads][dim] with contiguous channels")
-    if t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [T, "
-                         f"{'heads' if heads is None else heads}, {dim}]")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if like is not None and t.shape != like.shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
     if like is not None and t.dtype != like.dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {like.dtype}")
-    return mx_rows(t.data_ptr(), t.stride(0), t.stride(1))
+    want = ("T", heads, dim) if like is None else tuple(like.shape)
+    if t.shape[2] != dim or t.shape[1] != want[1] or (like is not None and tuple(t.shape) != want):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {want}")
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{at}")
 
 
 def _row_count(t, name):
+    try:
+        T, heads, _ = t.shape
+        return T, heads
+    except (AttributeError, TypeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens][heads][dim]")
-    return t.shape[0]
+    raise ValueError(f"{name} must be [tokens][heads][dim]")
+
+
+_current_device = torch._C._cuda_getDevice
+
+
+def _call(function, at, stream, *args):
+    """_launch for a device's index and a function of the library."""
+    raw = _current_raw_stream(at) if stream is None else stream.cuda_stream
+    if at == _current_device():
+        status = function(*args, raw)
+    else:
+        with torch.cuda.device(at):
+            status = function(*args, raw)
+    if status:
+        check(status, function.__name__)
 
 
 def mx_cache_write(k, v, kq, ks, vq, vs, pages, lengths, offsets=None, fmt: int = MX_E4M3,
@@ -599,11 +653,11 @@ def mx_cache_write(k, v, kq, ks, vq, vs, pages, lengths, offsets=None, fmt: int 
     int32 counts the sequences' tokens with these; rows offsets[b] .. offsets[b + 1] (int32, [B + 1])
     are the newest of sequence b, without offsets row b is. A block of 32 tokens whose scale has to
     grow rounds its older codes again."""
-    c = _cache(kq, ks, vq, vs, pages, lengths, offsets, _row_count(k, "k"), fmt)
-    T, H, D = k.shape[0], c.heads, c.dim
-    rk = _heads(k, "k", H, D, kq.device)
-    rv = _heads(v, "v", H, D, kq.device, k)
-    _launch("mx_cache_write", kq.device, stream, rk, rv, _CODE[k.dtype], T, c, scale_rule)
+    T = _row_count(k, "k")[0]
+    c, H, D, at = _cache(kq, ks, vq, vs, pages, lengths, offsets, T, fmt)
+    rk = _heads(k, "k", H, D, at)
+    rv = _heads(v, "v", H, D, at, k)
+    _call(_lib.lib().mx_cache_write, at, stream, rk, rv, _CODE[k.dtype], T, c, scale_rule)
 
 
 def mx_cache_read(kq, ks, vq, vs, pages, lengths, offsets=None, rows=None, fmt: int = MX_E4M3,
@@ -615,17 +669,17 @@ def mx_cache_read(kq, ks, vq, vs, pages, lengths, offsets=None, rows=None, fmt: 
         if offsets is not None:
             raise ValueError("with offsets, rows (or k and v) says how many rows there are")
         rows = lengths.shape[0] if isinstance(lengths, torch.Tensor) and lengths.dim() == 1 else 0
-    T = rows if k is None else _row_count(k, "k")
-    c = _cache(kq, ks, vq, vs, pages, lengths, offsets, T, fmt)
-    H, D, dev = c.heads, c.dim, kq.device
-    if k is None or v is None:
-        if (k if k is not None else v) is not None:
-            raise ValueError("k and v are given together")
+    T = rows if k is None else _row_count(k, "k")[0]
+    c, H, D, at = _cache(kq, ks, vq, vs, pages, lengths, offsets, T, fmt)
+    if k is None and v is None:
         if out_dtype not in _CODE:
             raise TypeError("out_dtype must be bfloat16 or float32")
-        k, v = torch.empty((2, T, H, D), dtype=out_dtype, device=dev)
-    rk, rv = _heads(k, "k", H, D, dev), _heads(v, "v", H, D, dev, k)
-    _launch("mx_cache_read", dev, stream, rk, rv, _CODE[k.dtype], T, c)
+        k = torch.empty((T, H, D), dtype=out_dtype, device=kq.device)
+        v = torch.empty_like(k)
+    elif k is None or v is None:
+        raise ValueError("k and v are given together")
+    rk, rv = _heads(k, "k", H, D, at), _heads(v, "v", H, D, at, k)
+    _call(_lib.lib().mx_cache_read, at, stream, rk, rv, _CODE[k.dtype], T, c)
     return k, v
 
 
@@ -637,25 +691,26 @@ def mx_cache_attention(q, kq, ks, vq, vs, pages, lengths, offsets=None, scale=No
     each row over the tokens up to its own -> out of q's shape and type, or (out, lse [T][query heads]
     fp32) with with_lse or an lse buffer. scale: dim ** -0.5 when None. workspace: a uint8 buffer of at
     least lib().mx_cache_attention_workspace(...) bytes, allocated per call when None."""
-    c = _cache(kq, ks, vq, vs, pages, lengths, offsets, _row_count(q, "q"), fmt)
+    T, heads = _row_count(q, "q")
+    c, _, D, at = _cache(kq, ks, vq, vs, pages, lengths, offsets, T, fmt)
+    rq = _heads(q, "q", heads, D, at)
     dev = kq.device
-    rq = _heads(q, "q", None, c.dim, dev)
-    T, heads = q.shape[0], q.shape[1]
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    ro = _heads(out, "out", None, c.dim, dev, q)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    ro = _heads(out, "out", heads, D, at, q)
     if lse is not None:
         _buf(lse, "lse", (T, heads), _F32, dev)
     elif with_lse:
         lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
+    L = _lib.lib()
     if workspace is not None:
         size = _workspace(workspace, dev)
     else:
-        size = lib().mx_cache_attention_workspace(T, heads, c)
+        size = L.mx_cache_attention_workspace(T, heads, c)
         if size > 0:
             workspace = _scratch(size, dev, stream)
-    _launch("mx_cache_attention", dev, stream, rq, ro, _data(lse), _CODE[q.dtype], T, heads,
-            c.dim ** -0.5 if scale is None else scale, c, _data(workspace), size)
+    _call(L.mx_cache_attention, at, stream, rq, ro, _data(lse), _CODE[q.dtype], T, heads,
+          D ** -0.5 if scale is None else scale, c, _data(workspace), size)
     return out if lse is None else (out, lse)
 
 

@@ -83,7 +83,7 @@ def lib() -> ctypes.CDLL:
                           vp, i64, vp]
     L.mx_gemv_workspace.argtypes = [i32, i64, i64, i64, i32, i32]
     L.mx_gemv_workspace.restype = i64
-    cache, rows = ctypes.POINTER(mx_cache), ctypes.POINTER(mx_rows)
+    cache = rows = vp  # mx_cache and mx_rows: structures by reference, or their bytes
     L.mx_cache_write.argtypes = [rows, rows, i32, i64, cache, i32, vp]
     L.mx_cache_read.argtypes = [rows, rows, i32, i64, cache, vp]
     L.mx_cache_attention.argtypes = [rows, rows, vp, i32, i64, i64, f32, cache, vp, i64, vp]

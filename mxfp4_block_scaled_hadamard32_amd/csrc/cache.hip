@@ -37,12 +37,18 @@ __device__ __forceinline__ Sequence sequence_of(const CacheArgs& c, int b, int r
   return s;
 }
 
+// the place in a page table of the page that holds positions 32 bn ..: bn / page_blocks by a product,
+// exact for bn < 2^26 and page_blocks <= 64
+__device__ __forceinline__ int slot_of(const CacheArgs& c, int bn) {
+  return c.page_blocks == 1 ? bn : (int)__umulhi((uint32_t)bn, c.page_magic);
+}
+
 // The block that holds positions 32 bn .. of sequence b, -1 where the table has no such page.
-// bn / page_blocks by a product: bn < 2^26 and page_blocks <= 64 keep it exact.
-__device__ __forceinline__ int64_t block_of(const CacheArgs& c, int b, int bn, int head) {
-  const int slot = c.page_blocks == 1 ? bn : (int)__umulhi((uint32_t)bn, c.page_magic);
+__device__ __forceinline__ int64_t block_of(const CacheArgs& c, const int32_t* pages, int b, int bn,
+                                            int head) {
+  const int slot = slot_of(c, bn);
   if (bn < 0 || slot >= c.table_width) return -1;
-  const int page = c.pages[(int64_t)b * c.table_width + slot];
+  const int page = pages[(int64_t)b * c.table_width + slot];
   if (page < 0 || page >= c.n_pages) return -1;
   return ((int64_t)page * c.heads + head) * c.page_blocks + (bn - slot * c.page_blocks);
 }
@@ -162,7 +168,7 @@ __global__ __launch_bounds__(D) void cache_write_kernel(const CacheArgs c, const
   if (!piece_of(c, blockIdx.x, c.rows, p)) return;
   const int head = blockIdx.y;
   const bool values = blockIdx.z != 0;
-  const int64_t block = block_of(c, p.b, p.bn, head);
+  const int64_t block = block_of(c, c.pages, p.b, p.bn, head);
   if (block < 0) return;
   const CacheRows src = values ? v : k;
   const int esize = BF16 ? 2 : 4;
@@ -261,7 +267,7 @@ __global__ __launch_bounds__(D) void cache_read_kernel(const CacheArgs c, const 
   if (!piece_of(c, blockIdx.x, c.rows, p)) return;
   const int head = blockIdx.y;
   const bool values = blockIdx.z != 0;
-  const int64_t block = block_of(c, p.b, p.bn, head);
+  const int64_t block = block_of(c, c.pages, p.b, p.bn, head);
   const CacheRows dst = values ? v : k;
   const int esize = BF16 ? 2 : 4;
   uint8_t* rows = static_cast<uint8_t*>(const_cast<void*>(dst.p)) + (int64_t)head * dst.head * esize;
@@ -324,12 +330,16 @@ __global__ __launch_bounds__(D) void cache_read_kernel(const CacheArgs c, const 
 // 16 bits, for a bf16 result (its rounding, 2^-9, would otherwise be felt beside the result's own) and
 // as three for fp32. Sums and the softmax's statistics are fp32, exponentials to the base 2.
 //
-// Work is cut where the lengths say so, on the device: a sequence's rows, R = 16 WR at a time, are
-// an item; an item's steps are cut into chunks of c = (all items' steps) / target, a workgroup each.
-// The partial results of an item with several chunks go to the workspace, which a second kernel joins.
+// Work is divided where the lengths are known, on the device, and evenly: a sequence's rows, R = 16 WR
+// at a time, are an item, and the steps of all items, one after the other, are cut into as many equal
+// parts as there are workgroups (64 sequences of 500 to 16000 tokens: 181 us, 206 with a chunk of a
+// sequence for each workgroup). An item in one part is finished there; of the others each part goes to
+// the workspace, and a second kernel joins them.
 // ---------------------------------------------------------------------------------------------
 constexpr int kWaves = 4;
-// chunks wanted over all heads: two workgroups for each of 256 compute units
+// Workgroups over all heads: two for each of 256 compute units, which is what their registers allow.
+// More of them, or three at a time with fewer registers, read less at once of each page and are slower
+// (64 sequences of 8192 tokens: 170 us with 512, 181 with 768 and 180 with 1024).
 constexpr int kTarget = 512;
 
 // 4 channels of an output row: o / sum rounded to the output's type, and once a row its log sum of
@@ -359,89 +369,127 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
   return v;
 }
 
-// a workgroup's part: rows from `row` on of sequence b (R of them), chunk `kc` of `chunks`
-struct Unit {
-  int b, row, kc, chunks, chunk_steps;
-  int first, stride;  // the item's units: first, first + stride, ..
+// All steps of all items stand in one line, an item after the other, and workgroup u of a head's U
+// has the steps from all * u / U on. A workgroup's part of an item is a segment; segment (u, item) has
+// the slot u + item, which no other has: from one segment to the next either grows by one.
+struct Line {
+  int64_t all, at, end;  // steps in all; the workgroup's
+  int units;             // U
+  int b, tile;           // the item that step `at` is in: R rows of sequence b from tile * R on
+  int item;              // its number
+  int64_t first;         // its first step in the line
 };
 
+__device__ __forceinline__ int64_t bound_of(const Line& o, int u) { return o.all * u / o.units; }
+// the workgroup that has step x
+__device__ __forceinline__ int unit_at(const Line& o, int64_t x) {
+  int u = (int)(x * o.units / o.all);
+  while (bound_of(o, u + 1) <= x) ++u;
+  return u;
+}
+
+template <int R>
+__device__ __forceinline__ int items_of(const Sequence& s, int group) {
+  return (s.n * group + R - 1) / R;
+}
+// an item without tokens has a step as well: its rows are written
+template <int TS>
+__device__ __forceinline__ int steps_of(const CacheArgs& c, const Sequence& s) {
+  return max((min(s.length, c.max_tokens) + TS - 1) / TS, 1);
+}
+
 template <int R, int TS>
-__device__ __forceinline__ bool unit_of(const CacheArgs& c, const AttentionArgs& a, int unit, Unit& o) {
+__device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs& a, int unit, Line& o) {
   __shared__ int64_t sums[kWaves];
-  __shared__ int counts[kWaves], got[3];
+  __shared__ int64_t got_first;
+  __shared__ int got_b, got_item, counts[kWaves];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  auto items = [&](const Sequence& s) { return (s.n * a.group + R - 1) / R; };
-  auto steps = [&](const Sequence& s) { return (min(s.length, c.max_tokens) + TS - 1) / TS; };
+  auto bounds = [&]() {
+    o.units = (int)min((int64_t)gridDim.x, o.all);
+    if (unit >= o.units) return false;
+    o.at = bound_of(o, unit);
+    o.end = bound_of(o, unit + 1);
+    return true;
+  };
   if (c.seqs == 1) {
     const Sequence s = sequence_of(c, 0, c.rows);
-    const int n = items(s), st = steps(s);
-    const int cs = max((int)(((int64_t)n * st + a.target - 1) / a.target), 1);
-    o.chunks = max((st + cs - 1) / cs, 1);
-    if (unit >= n * o.chunks) return false;
+    const int st = steps_of<TS>(c, s);
+    o.all = (int64_t)items_of<R>(s, a.group) * st;
+    if (o.all == 0 || !bounds()) return false;
     o.b = 0;
-    o.kc = unit / n;
-    o.first = unit % n;
-    o.row = o.first * R;
-    o.stride = n;
-    o.chunk_steps = cs;
+    o.tile = o.item = (int)(o.at / st);
+    o.first = (int64_t)o.item * st;
     return true;
   }
   int64_t all = 0;
   for (int b = tid; b < c.seqs; b += 64 * kWaves) {
     const Sequence s = sequence_of(c, b, c.rows);
-    all += (int64_t)items(s) * steps(s);
+    all += (int64_t)items_of<R>(s, a.group) * steps_of<TS>(c, s);
   }
   all = wave_sum(all);
   if (lane == 0) sums[wave] = all;
-  if (tid == 0) got[0] = -1;
+  if (tid == 0) got_b = -1;
   __syncthreads();
-  all = 0;
+  o.all = 0;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) all += sums[i];
-  const int cs = max((int)min((all + a.target - 1) / a.target, (int64_t)1 << 30), 1);
-  int before = 0;
+  for (int i = 0; i < kWaves; ++i) o.all += sums[i];
+  if (o.all == 0 || !bounds()) return false;
+  int64_t before = 0;
+  int items_before = 0;
   for (int b0 = 0; b0 < c.seqs; b0 += 64 * kWaves) {  // the same turns in every wave
     const int b = b0 + tid;
-    int n = 0, chunks = 1;
+    int n = 0, st = 0;
     if (b < c.seqs) {
       const Sequence s = sequence_of(c, b, c.rows);
-      n = items(s);
-      chunks = max((steps(s) + cs - 1) / cs, 1);
+      n = items_of<R>(s, a.group);
+      st = steps_of<TS>(c, s);
     }
-    int end = n * chunks;
+    int64_t end = (int64_t)n * st;
+    int items = n;
 #pragma unroll
     for (int i = 1; i < 64; i *= 2) {
-      const int t = __shfl_up(end, i);
-      if (lane >= i) end += t;
+      const int64_t t = __shfl_up(end, i);
+      const int k = __shfl_up(items, i);
+      if (lane >= i) {
+        end += t;
+        items += k;
+      }
     }
-    if (lane == 63) counts[wave] = end;
     __syncthreads();
-    int total = 0;
+    if (lane == 63) {
+      sums[wave] = end;
+      counts[wave] = items;
+    }
+    __syncthreads();
+    int64_t total = 0;
+    int total_items = 0;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) {
-      if (i < wave) end += counts[i];
-      total += counts[i];
+      if (i < wave) {
+        end += sums[i];
+        items += counts[i];
+      }
+      total += sums[i];
+      total_items += counts[i];
     }
     end += before;
-    if (unit < end && unit >= end - n * chunks) {
-      got[0] = b;
-      got[1] = end - n * chunks;
-      got[2] = chunks;
+    const int64_t begin = end - (int64_t)n * st;
+    if (o.at >= begin && o.at < end) {
+      got_b = b;
+      got_item = items_before + items - n;
+      got_first = begin;
     }
     before += total;
+    items_before += total_items;
     __syncthreads();
-    if (got[0] >= 0) break;
+    if (got_b >= 0) break;
   }
-  o.b = __builtin_amdgcn_readfirstlane(got[0]);
+  o.b = __builtin_amdgcn_readfirstlane(got_b);
   if (o.b < 0) return false;
-  const int n = items(sequence_of(c, o.b, c.rows));
-  const int base = __builtin_amdgcn_readfirstlane(got[1]), local = unit - base;
-  o.chunks = __builtin_amdgcn_readfirstlane(got[2]);
-  o.kc = local / n;
-  o.first = base + local % n;
-  o.row = local % n * R;
-  o.stride = n;
-  o.chunk_steps = cs;
+  const int st = steps_of<TS>(c, sequence_of(c, o.b, c.rows));
+  o.tile = (int)((o.at - got_first) / st);
+  o.item = got_item + o.tile;
+  o.first = got_first + (int64_t)o.tile * st;
   return true;
 }
 
@@ -479,39 +527,65 @@ __device__ __forceinline__ float row_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-// what a step reads of the cache: key codes of its tokens, value codes, two scales
+// A load of what only this wave reads (STREAM): past the caches' order of replacement.
+template <bool STREAM, typename T>
+__device__ __forceinline__ T load_codes(const uint8_t* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
+  return *reinterpret_cast<const T*>(p);
+}
+
+// The codes of a step's tokens in a lane, and its block's scale (NB == 1: the lanes have one block)
 template <int D, int TS>
-struct Step {
-  u32x4 k[TS / 16][D / 64];
-  uint32_t v[D / 16][TS / 16];
-  uint32_t ks, vs;  // this lane's block of keys and of values (the same two bytes in other lanes)
-  bool has[TS / 32];
+struct Keys {
+  u32x4 w[TS / 16][D / 64];
+  uint32_t scale;
+};
+template <int D, int TS>
+struct Values {
+  uint32_t w[D / 16][TS / 16];
+  uint32_t scale;
+};
+// the step's blocks, of which `has` are in the cache (the others stand for block 0)
+template <int NB>
+struct Blocks {
+  int64_t at[NB];
+  bool has[NB];
 };
 
+template <int D>
+struct AttentionShared {
+  float part[kWaves][16][D + 4];
+  float stat[kWaves][16][2];
+};
+
+// One segment: the steps of an item that the workgroup has
 template <int D, int FMT, bool BF16, int WR, int TS>
-__global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_kernel(const CacheArgs c,
-                                                                         const AttentionArgs a) {
+__device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& a,
+                                       const int32_t* __restrict__ pages, const Line& line,
+                                       const Sequence& s, AttentionShared<D>& sh) {
   constexpr int R = 16 * WR, TW = kWaves / WR;  // rows a workgroup; waves that share a row's tokens
   constexpr int NQ = BF16 ? 1 : 3, NP = BF16 ? 2 : 3, KT = TS / 16, NB = TS / 32, PER = TS / 4;
-  __shared__ __attribute__((aligned(16))) float part[kWaves][16][D + 4];
-  __shared__ float stat[kWaves][16][2];
-  Unit u;
-  if (!unit_of<R, TS>(c, a, blockIdx.x, u)) return;
-  const int head = blockIdx.y;
-  const Sequence s = sequence_of(c, u.b, c.rows);
+  const int head = blockIdx.y, unit = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wr = wave % WR, wt = wave / WR;
-  const int rows = s.n * a.group;               // of this sequence and head
-  const int row = u.row + 16 * wr + i;          // this lane's
+  const int all_steps = steps_of<TS>(c, s);
+  const int from = (int)(line.at - line.first);
+  const int to = (int)min(line.end - line.first, (int64_t)all_steps);
+  // the item's segments are those of units first_unit .. last_unit
+  const int first_unit = from == 0 ? unit : unit_at(line, line.first);
+  const int last_unit = to == all_steps ? unit : unit_at(line, line.first + all_steps - 1);
+  const int row0 = line.tile * R;
+  const int rows = s.n * a.group;      // of this sequence and head
+  const int row = row0 + 16 * wr + i;  // this lane's
   const int token = min(row, rows - 1) / a.group, qhead = head * a.group + min(row, rows - 1) % a.group;
   // how many tokens a row sees; rows past the end see what the last one does and are not stored
   const int seen = min(s.length - s.n + token + 1, c.max_tokens);
-  const int wg_last = (min(u.row + R, rows) - 1) / a.group;  // the last token of the unit's rows
+  const int wg_last = (min(row0 + R, rows) - 1) / a.group;  // the last token of the unit's rows
   const int most = min(s.length - s.n + wg_last + 1, c.max_tokens);
-  const int first_token = min(u.row + 16 * wr, rows - 1) / a.group;
+  const int first_token = min(row0 + 16 * wr, rows - 1) / a.group;
   const int least = min(s.length - s.n + first_token + 1, c.max_tokens);  // of this wave's rows
-  const int end = u.row + 16 * wr < rows  // a wave may have no rows
-                      ? min((u.kc + 1) * u.chunk_steps, (max(most, 0) + TS - 1) / TS) : 0;
+  const int end = row0 + 16 * wr < rows  // a wave may have no rows
+                      ? min(to, (max(most, 0) + TS - 1) / TS) : 0;
 
   bf16x8_t q[NQ][D / 32];
   {
@@ -540,52 +614,76 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_kernel(const C
   for (int d = 0; d < D / 16; ++d) acc[d] = f32x4{0, 0, 0, 0};
   float m = -__builtin_inff(), l = 0.0f;
 
-  auto load = [&](int step, Step<D, TS>& o) {
-    int64_t block[NB];
+  // the page numbers of a step's blocks; past the end those of the table's first page
+  const int32_t* table = pages + (int64_t)line.b * c.table_width;
+  auto look = [&](int step, int (&page)[NB]) {
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      const int bn = NB * step + n;
-      block[n] = 32 * bn < most ? block_of(c, u.b, bn, head) : -1;
-      o.has[n] = block[n] >= 0;
-      block[n] = max(block[n], (int64_t)0);
+      const int slot = slot_of(c, NB * step + n);
+      page[n] = table[step < end && slot < c.table_width ? slot : 0];
     }
-    const int64_t kb = NB == 1 ? block[0] : i >= 8 ? block[NB - 1] : block[0];
-    const int64_t vb = NB == 1 ? block[0] : g >= 2 ? block[NB - 1] : block[0];
-    o.ks = c.ks[kb];
-    o.vs = c.vs[vb];
-    const int krow = PER * ((i >> 2) & (NB == 1 ? 3 : 1)) + (i & 3);
-    const uint8_t* kp = c.kq + kb * (32 * D) + krow * D + 16 * g;
+  };
+  auto find = [&](int step, const int (&page)[NB]) {
+    Blocks<NB> o;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int bn = NB * step + n, slot = slot_of(c, bn);
+      o.has[n] = step < end && 32 * bn < most && page[n] >= 0 && page[n] < c.n_pages;
+      o.at[n] = o.has[n] ? ((int64_t)page[n] * c.heads + head) * c.page_blocks + (bn - slot * c.page_blocks) : 0;
+    }
+    return o;
+  };
+  auto load_keys = [&](const Blocks<NB>& b, Keys<D, TS>& o) {
+    const int64_t at = NB == 1 ? b.at[0] : i >= 8 ? b.at[NB - 1] : b.at[0];
+    o.scale = c.ks[at];
+    const uint8_t* p = c.kq + at * (32 * D) + (PER * ((i >> 2) & (NB == 1 ? 3 : 1)) + (i & 3)) * D + 16 * g;
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j)
-        o.k[t][j] = *reinterpret_cast<const u32x4*>(kp + 4 * t * D + 64 * j);
-    const uint8_t* vp = c.vq + vb * (32 * D) + i * 32 + PER * (g & (NB == 1 ? 3 : 1));
+      for (int j = 0; j < D / 64; ++j) o.w[t][j] = load_codes<WR == 1, u32x4>(p + 4 * t * D + 64 * j);
+  };
+  auto load_values = [&](const Blocks<NB>& b, Values<D, TS>& o) {
+    const int64_t at = NB == 1 ? b.at[0] : g >= 2 ? b.at[NB - 1] : b.at[0];
+    o.scale = c.vs[at];
+    const uint8_t* p = c.vq + at * (32 * D) + i * 32 + PER * (g & (NB == 1 ? 3 : 1));
+    typedef uint32_t word __attribute__((ext_vector_type(TS / 16)));
 #pragma unroll
     for (int d = 0; d < D / 16; ++d) {
-      if constexpr (KT == 4) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(vp + d * 512);
+      const word w = load_codes<WR == 1, word>(p + d * 512);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o.v[d][e] = w[e];
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(vp + d * 512);
-        o.v[d][0] = w.x;
-        o.v[d][1] = w.y;
-      }
+      for (int t = 0; t < KT; ++t) o.w[d][t] = w[t];
     }
   };
 
-  auto use = [&](int step, Step<D, TS>& o) {
+  int step = from + wt;
+  Keys<D, TS> k;
+  Values<D, TS> v;
+  Blocks<NB> here, next;
+  if (step < end) {
+    int page[NB], page2[NB];
+    look(step, page);
+    look(step + TW, page2);
+    here = find(step, page);
+    load_keys(here, k);
+    load_values(here, v);
+    next = find(step + TW, page2);
+  }
+  // The next step's keys are on their way while this one's softmax and values are worked on, and its
+  // values during its scores, in the registers that have just become free.
+  for (; step < end; step += TW) {
+    int page[NB];
+    look(step + 2 * TW, page);
     f32x4 sc[KT];
-    const bool nan_k = o.ks == 0xFFu, nan_v = o.vs == 0xFFu;
-    const float kf = nan_k ? 1.0f : scale_of(o.ks), vf = nan_v ? 1.0f : scale_of(o.vs);
+    const uint32_t kscale = k.scale;
+    const bool nan_k = kscale == 0xFFu;
+    const float kf = nan_k ? 1.0f : scale_of(kscale);
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       sc[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
-        const bf16x8_t k0 = codes_of<FMT>(o.k[t][j][0], o.k[t][j][1], kf);
-        const bf16x8_t k1 = codes_of<FMT>(o.k[t][j][2], o.k[t][j][3], kf);
+        const bf16x8_t k0 = codes_of<FMT>(k.w[t][j][0], k.w[t][j][1], kf);
+        const bf16x8_t k1 = codes_of<FMT>(k.w[t][j][2], k.w[t][j][3], kf);
 #pragma unroll
         for (int n = NQ - 1; n >= 0; --n) {
           sc[t] = mfma(k0, q[n][2 * j], sc[t]);
@@ -593,9 +691,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_kernel(const C
         }
       }
     }
+    load_keys(next, k);
     bool whole = (step + 1) * TS <= least;
 #pragma unroll
-    for (int n = 0; n < NB; ++n) whole = whole && o.has[n];
+    for (int n = 0; n < NB; ++n) whole = whole && here.has[n];
+    const bool nan_v = v.scale == 0xFFu;
+    const float vf = nan_v ? 1.0f : scale_of(v.scale);
     // a block whose maximum was not finite: what sees it is NaN, and its codes are zero
     const bool strange = __any(nan_k || nan_v);
     float p[KT][4];
@@ -604,26 +705,26 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_kernel(const C
 #pragma unroll
       for (int r = 0; r < 4; ++r) p[t][r] = sc[t][r] * a.scale_log2;
     bool lost = false;  // this lane's tokens have no values
-    int here = PER;     // of this lane's tokens, those that its row sees
+    int mine = PER;     // of this lane's tokens, those that its row sees
     if (!whole || strange) {
       // tokens PER g .. of the step are this lane's, in block g / 2 of two
-      const bool mine = NB == 1 ? o.has[0] : g >= 2 ? o.has[NB - 1] : o.has[0];
+      const bool has = NB == 1 ? here.has[0] : g >= 2 ? here.has[NB - 1] : here.has[0];
       const int at = step * TS + PER * g;
-      here = mine ? min(seen - at, PER) : 0;
-      const int held = mine ? min(most - at, PER) : 0;  // that any row sees
+      mine = has ? min(seen - at, PER) : 0;
+      const int held = has ? min(most - at, PER) : 0;  // that any row sees
       // the scales of the block that this lane's scores come from
-      const uint32_t kb = NB == 1 ? o.ks : (uint32_t)__shfl((int)o.ks, g >= 2 ? 8 : 0);
+      const uint32_t kb = NB == 1 ? kscale : (uint32_t)__shfl((int)kscale, g >= 2 ? 8 : 0);
       const bool nan = kb == 0xFFu;
       lost = nan_v;
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          p[t][r] = 4 * t + r < here ? nan ? __builtin_nanf("") : p[t][r] : -__builtin_inff();
+          p[t][r] = 4 * t + r < mine ? nan ? __builtin_nanf("") : p[t][r] : -__builtin_inff();
         const int left = nan_v ? 0 : min(max(held - 4 * t, 0), 4);
         const uint32_t keep = left == 4 ? 0xFFFFFFFFu : (1u << (8 * left)) - 1u;
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) o.v[d][t] &= keep;
+        for (int d = 0; d < D / 16; ++d) v.w[d][t] &= keep;
       }
     }
     float top = p[0][0];
@@ -655,7 +756,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_kernel(const C
       for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (lost && 4 * t + r < here) p[t][r] = __builtin_nanf("");
+          if (lost && 4 * t + r < mine) p[t][r] = __builtin_nanf("");
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {  // 8 tokens a lane: tiles 2b and 2b + 1
@@ -665,50 +766,47 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_kernel(const C
         split_pair<NP>(p[2 * b + e / 2][2 * (e % 2)], p[2 * b + e / 2][2 * (e % 2) + 1], w[e]);
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
-        const bf16x8_t v = codes_of<FMT>(o.v[d][2 * b], o.v[d][2 * b + 1], vf);
+        const bf16x8_t x = codes_of<FMT>(v.w[d][2 * b], v.w[d][2 * b + 1], vf);
 #pragma unroll
         for (int n = NP - 1; n >= 0; --n)
-          acc[d] = mfma(v, __builtin_bit_cast(bf16x8_t, u32x4{w[0][n], w[1][n], w[2][n], w[3][n]}), acc[d]);
+          acc[d] = mfma(x, __builtin_bit_cast(bf16x8_t, u32x4{w[0][n], w[1][n], w[2][n], w[3][n]}), acc[d]);
       }
     }
-  };
-
-  for (int step = u.kc * u.chunk_steps + wt; step < end; step += TW) {
-    Step<D, TS> o;
-    load(step, o);
-    use(step, o);
+    load_values(next, v);
+    here = next;
+    next = find(step + 2 * TW, page);
   }
 
   // the waves' parts of a row, joined in the waves' order
   l = row_sum(l);
   if (l != l) m = 0.0f;  // a NaN counts, whatever the maximum of the others
   if (g == 0) {
-    stat[wave][i][0] = m;
-    stat[wave][i][1] = l;
+    sh.stat[wave][i][0] = m;
+    sh.stat[wave][i][1] = l;
   }
 #pragma unroll
   for (int d = 0; d < D / 16; ++d)
-    *reinterpret_cast<f32x4*>(&part[wave][i][16 * d + 4 * g]) = acc[d];
+    *reinterpret_cast<f32x4*>(&sh.part[wave][i][16 * d + 4 * g]) = acc[d];
   __syncthreads();
   for (int e = tid; e < R * (D / 4); e += 64 * kWaves) {
-    const int r = e / (D / 4), ch = 4 * (e % (D / 4)), at = u.row + r;
+    const int r = e / (D / 4), ch = 4 * (e % (D / 4)), at = row0 + r;
     if (at >= rows) break;
     const int w0 = r / 16, ri = r % 16;
     float top = -__builtin_inff(), sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < TW; ++w) top = fmaxf(top, stat[w0 + w * WR][ri][0]);
+    for (int w = 0; w < TW; ++w) top = fmaxf(top, sh.stat[w0 + w * WR][ri][0]);
     const float base = top == -__builtin_inff() ? 0.0f : top;
     f32x4 o = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < TW; ++w) {
-      const float f = __builtin_amdgcn_exp2f(stat[w0 + w * WR][ri][0] - base);
-      sum += stat[w0 + w * WR][ri][1] * f;
-      const f32x4 t = *reinterpret_cast<const f32x4*>(&part[w0 + w * WR][ri][ch]);
+      const float f = __builtin_amdgcn_exp2f(sh.stat[w0 + w * WR][ri][0] - base);
+      sum += sh.stat[w0 + w * WR][ri][1] * f;
+      const f32x4 t = *reinterpret_cast<const f32x4*>(&sh.part[w0 + w * WR][ri][ch]);
 #pragma unroll
       for (int x = 0; x < 4; ++x) o[x] += t[x] * f;
     }
-    const int64_t slot = ((int64_t)blockIdx.x * c.heads + head) * R + r;
-    if (u.chunks == 1) {
+    const int64_t slot = ((int64_t)(unit + line.item) * c.heads + head) * R + r;
+    if (first_unit == last_unit) {
       store_row<BF16>(a, (int64_t)s.row0 + at / a.group, head * a.group + at % a.group, ch, o, base, sum);
     } else {
       *reinterpret_cast<f32x4*>(a.part + slot * D + ch) = o;
@@ -718,31 +816,53 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_kernel(const C
       }
     }
   }
-  if (u.kc == 0 && head == 0 && tid < R && u.row + tid < rows) {
-    const int at = u.row + tid;
-    a.where[(int64_t)s.row0 * a.group + at] = make_int4(u.first, u.stride, u.chunks, tid);
+  if (from == 0 && head == 0 && tid < R && row0 + tid < rows) {
+    const int at = row0 + tid;
+    a.where[(int64_t)s.row0 * a.group + at] = make_int4(first_unit + line.item, last_unit - first_unit + 1, tid, 0);
   }
 }
 
-// The chunks of a row joined: a workgroup for each token and query head, 4 channels a thread, the
-// chunks among its groups of D / 4 threads.
+template <int D, int FMT, bool BF16, int WR, int TS>
+__global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_kernel(
+    const CacheArgs c, const AttentionArgs a, const int32_t* __restrict__ pages) {
+  __shared__ __attribute__((aligned(16))) AttentionShared<D> sh;
+  Line line;
+  if (!line_of<16 * WR, TS>(c, a, blockIdx.x, line)) return;
+  for (;;) {
+    // offsets that fall may make more items than the workspace has slots
+    if ((int64_t)blockIdx.x + line.item >= a.slots) return;
+    const Sequence s = sequence_of(c, line.b, c.rows);
+    attend<D, FMT, BF16, WR, TS>(c, a, pages, line, s, sh);
+    line.at = line.first + steps_of<TS>(c, s);
+    if (line.at >= line.end) return;
+    line.first = line.at;
+    ++line.item;
+    if (++line.tile * 16 * WR >= s.n * a.group) {
+      line.tile = 0;
+      do {
+        if (++line.b >= c.seqs) return;
+      } while (sequence_of(c, line.b, c.rows).n == 0);
+    }
+    __syncthreads();  // what the waves read of sh is written again
+  }
+}
+
+// The segments of a row joined: a workgroup for each token and query head, 4 channels a thread, the
+// segments among its groups of D / 4 threads.
 template <int D, bool BF16>
 __global__ __launch_bounds__(256) void cache_attention_join_kernel(const CacheArgs c,
-                                                                   const AttentionArgs a, int R,
-                                                                   int units) {
+                                                                   const AttentionArgs a, int R) {
   constexpr int PER = D / 4, GROUPS = 256 / PER;
   __shared__ __attribute__((aligned(16))) float sums[GROUPS][D];
   __shared__ float tops[4], all[GROUPS];
   const int t = blockIdx.x, qhead = blockIdx.y, head = qhead / a.group, tid = threadIdx.x;
   if (c.offsets && (t < c.offsets[0] || t >= c.offsets[c.seqs])) return;
   const int4 w = a.where[(int64_t)t * a.group + qhead % a.group];
-  // one chunk: written already; and tables that are none (offsets that fall) end here
-  if (w.z <= 1 || w.x < 0 || w.y <= 0 || w.w < 0 || w.w >= R ||
-      (int64_t)w.x + (int64_t)(w.z - 1) * w.y >= units)
-    return;
-  auto slot = [&](int k) { return ((int64_t)(w.x + k * w.y) * c.heads + head) * R + w.w; };
+  // one part: written already; and tables that are none (offsets that fall) end here
+  if (w.y <= 1 || w.x < 0 || w.z < 0 || w.z >= R || (int64_t)w.x + w.y > a.slots) return;
+  auto slot = [&](int k) { return ((int64_t)(w.x + k) * c.heads + head) * R + w.z; };
   float top = -__builtin_inff();
-  for (int k = tid; k < w.z; k += 256) top = fmaxf(top, a.stat[2 * slot(k)]);
+  for (int k = tid; k < w.y; k += 256) top = fmaxf(top, a.stat[2 * slot(k)]);
 #pragma unroll
   for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
   if ((tid & 63) == 0) tops[tid >> 6] = top;
@@ -754,7 +874,7 @@ __global__ __launch_bounds__(256) void cache_attention_join_kernel(const CacheAr
     f32x4 o = {0, 0, 0, 0};
     float sum = 0.0f;
 #pragma unroll 4
-    for (int k = group; k < w.z; k += GROUPS) {
+    for (int k = group; k < w.y; k += GROUPS) {
       const int64_t s = slot(k);
       const float f = __builtin_amdgcn_exp2f(a.stat[2 * s] - base);
       sum += a.stat[2 * s + 1] * f;
@@ -841,8 +961,8 @@ constexpr int step_tokens(int dim) { return dim <= 128 ? 64 : 32; }
 
 struct AttentionPlan {
   int wr;          // row tiles of a workgroup
-  int target;      // chunks wanted for each head, beside one for each item
-  int64_t units;   // workgroups for each head, at most
+  int64_t units;   // workgroups for each head
+  int64_t slots;   // segments of each head, at most
   bool join;
 };
 
@@ -852,11 +972,11 @@ AttentionPlan plan_attention(const CacheArgs& c, const AttentionArgs& a) {
   const int64_t each = c.offsets ? (rows + c.seqs - 1) / c.seqs : a.group;
   p.wr = each <= 16 ? 1 : each <= 32 ? 2 : 4;
   const int64_t items = rows / (16 * p.wr) + c.seqs;
-  const int64_t steps = (c.max_tokens + step_tokens(c.dim) - 1) / step_tokens(c.dim);
-  p.target = (kTarget + c.heads - 1) / c.heads;
+  const int64_t most = (c.max_tokens + step_tokens(c.dim) - 1) / step_tokens(c.dim), steps = most > 0 ? most : 1;
   p.join = steps > 1;
-  p.units = p.join ? p.target + items : items;
-  if (p.join && items * steps < p.units) p.units = items * steps;
+  p.units = (kTarget + c.heads - 1) / c.heads;
+  if (items * steps < p.units) p.units = items * steps;
+  p.slots = p.units + items;
   return p;
 }
 
@@ -866,7 +986,7 @@ struct Attention {
   static void main(const CacheArgs& c, const AttentionArgs& a, const AttentionPlan& p) {
     hipLaunchKernelGGL((cache_attention_kernel<D, FMT, BF16, WR, step_tokens(D)>),
                        dim3((unsigned)p.units, (unsigned)c.heads), dim3(64 * kWaves), 0,
-                       (hipStream_t)a.stream, c, a);
+                       (hipStream_t)a.stream, c, a, c.pages);
   }
   static hipError_t run(const CacheArgs& c, const AttentionArgs& a, const AttentionPlan& p) {
     if (p.wr == 1) main<1>(c, a, p);
@@ -874,13 +994,13 @@ struct Attention {
     else main<4>(c, a, p);
     if (hipError_t e = hipGetLastError(); e != hipSuccess || !p.join) return e;
     hipLaunchKernelGGL((cache_attention_join_kernel<D, BF16>), dim3((unsigned)c.rows, (unsigned)a.heads),
-                       dim3(256), 0, (hipStream_t)a.stream, c, a, 16 * p.wr, (int)p.units);
+                       dim3(256), 0, (hipStream_t)a.stream, c, a, 16 * p.wr);
     return hipGetLastError();
   }
 };
 
 int64_t part_floats(const CacheArgs& c, const AttentionPlan& p) {
-  return p.join ? p.units * c.heads * 16 * p.wr : 0;
+  return p.join ? p.slots * c.heads * 16 * p.wr : 0;
 }
 
 }  // namespace
@@ -895,10 +1015,6 @@ hipError_t mx_launch_cache_read(const CacheArgs& c, const CacheRows& k, const Ca
   return pick<Read>(c, bf16, k, v, pieces(c), stream);
 }
 
-int64_t mx_attention_units(const CacheArgs& c, const AttentionArgs& a) {
-  return plan_attention(c, a).units;
-}
-
 // [where: 16 bytes a row][part: D floats][stat: 2 floats] for each chunk's row
 int64_t mx_attention_workspace_bytes(const CacheArgs& c, const AttentionArgs& a) {
   const AttentionPlan p = plan_attention(c, a);
@@ -907,7 +1023,7 @@ int64_t mx_attention_workspace_bytes(const CacheArgs& c, const AttentionArgs& a)
 
 hipError_t mx_launch_cache_attention(const CacheArgs& c, AttentionArgs a, void* workspace) {
   const AttentionPlan p = plan_attention(c, a);
-  a.target = p.target;
+  a.slots = p.slots;
   a.where = static_cast<int4*>(workspace);
   a.part = reinterpret_cast<float*>(a.where + (int64_t)c.rows * a.group);
   a.stat = a.part + part_floats(c, p) * c.dim;

@@ -539,7 +539,9 @@ mx_status mx_cache_read(const mx_rows* k, const mx_rows* v, int32_t dtype, int64
 
 int64_t mx_cache_attention_workspace(int64_t T, int64_t q_heads, const mx_cache* cache) {
   CacheArgs c{};
-  if (cache_args(cache, T, c) != MX_OK || q_heads < 0 || q_heads > 65535) return -1;
+  if (cache_args(cache, T, c) != MX_OK || q_heads < 0 || q_heads > 65535 ||
+      T * q_heads > kAttentionMaxRows)
+    return -1;
   if (T == 0 || q_heads == 0 || c.seqs == 0) return 0;
   if (c.heads == 0 || q_heads % c.heads) return -1;
   AttentionArgs a{};
@@ -559,6 +561,7 @@ mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, i
   if (q_heads < 0) return MX_ERR_SHAPE;
   if (q_heads > 65535) return MX_ERR_UNSUPPORTED;
   if (c.heads == 0 ? q_heads != 0 : q_heads % c.heads != 0) return MX_ERR_SHAPE;
+  if (T * q_heads > kAttentionMaxRows) return MX_ERR_UNSUPPORTED;
   if (!(scale >= -3.402823466e+38f && scale <= 3.402823466e+38f)) return MX_ERR_ARG;
   if ((s = cache_rows(q, dtype, T, q_heads, c.dim, rq, sq)) != MX_OK) return s;
   if ((s = cache_rows(out, dtype, T, q_heads, c.dim, ro, so)) != MX_OK) return s;
@@ -572,7 +575,6 @@ mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, i
   AttentionArgs a{rq.p, const_cast<void*>(ro.p), lse, rq.token, rq.head, ro.token, ro.head,
                   (int)q_heads, (int)q_heads / c.heads, scale * 1.4426950408889634f,
                   dtype == MX_BF16, stream, 0, nullptr, nullptr, nullptr};
-  if (mx_attention_units(c, a) > 0x7FFFFFFF) return MX_ERR_UNSUPPORTED;
   if (!workspace) return MX_ERR_NULL;
   if (workspace_bytes < mx_attention_workspace_bytes(c, a)) return MX_ERR_ARG;
   return launch_status(mx_launch_cache_attention(c, a, workspace));

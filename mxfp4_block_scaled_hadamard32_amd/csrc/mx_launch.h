@@ -165,6 +165,7 @@ hipError_t mx_launch_cache_write(const CacheArgs& c, const CacheRows& k, const C
 hipError_t mx_launch_cache_read(const CacheArgs& c, const CacheRows& k, const CacheRows& v,
                                 bool bf16, void* stream);
 
+constexpr int64_t kAttentionMaxRows = (int64_t)1 << 30;  // tokens x query heads
 struct AttentionArgs {
   const void* q;
   void* out;
@@ -175,12 +176,11 @@ struct AttentionArgs {
   bool bf16;
   void* stream;
   // set by the launcher
-  int target;
+  int64_t slots;
   int4* where;
   float* part;
   float* stat;
 };
-int64_t mx_attention_units(const CacheArgs& c, const AttentionArgs& a);
 int64_t mx_attention_workspace_bytes(const CacheArgs& c, const AttentionArgs& a);
 hipError_t mx_launch_cache_attention(const CacheArgs& c, AttentionArgs a, void* workspace);
 
