@@ -722,42 +722,65 @@ def mx_lora(x, a, b, index, base=None, scaling=None, out_dtype=None, out=None, w
     (zeros), scaling [E] fp32 or None (ones) -> out [T][N] of out_dtype (base's type when None, x's
     without a base). out may be base itself. workspace: a uint8 buffer of at least
     lib().mx_lora_workspace(T, K, E, rank) bytes, allocated per call when None."""
-    T, K, ldx = _rows(x, "x")
-    dev = x.device
+    try:
+        T, K = x.shape
+        E, rank, _ = a.shape
+        N, at, dtype = b.shape[1], x.get_device(), x.dtype
+        ldx, one = x.stride()
+        good = (dtype in _CODE and at >= 0 and (one == 1 or K <= 1) and a.dtype is dtype
+                and b.dtype is dtype and a.shape == (E, rank, K) and b.shape == (E, N, rank)
+                and a.get_device() == at and b.get_device() == at and a.is_contiguous()
+                and b.is_contiguous() and index.dtype is torch.int32 and index.shape == (T,)
+                and index.get_device() == at and index.is_contiguous()
+                and (scaling is None or scaling.dtype is torch.float32 and scaling.shape == (E,)
+                     and scaling.get_device() == at and scaling.is_contiguous())
+                and (base is None or base.dtype in _CODE and base.shape == (T, N)
+                     and base.get_device() == at and (base.stride(1) == 1 or N <= 1)))
+    except (AttributeError, IndexError, TypeError, ValueError):
+        good = False
+    if not good:
+        _lora_refusal(x, a, b, index, base, scaling)
+    base_code = ldb = 0
+    if base is not None:
+        base_code, ldb = _CODE[base.dtype], base.stride(0) if T > 1 else N
+    if out is None:
+        if out_dtype is None:
+            out_dtype = dtype if base is None else base.dtype
+        if out_dtype not in _CODE:
+            raise TypeError("out_dtype must be bfloat16 or float32")
+        out, code, ldo = torch.empty((T, N), dtype=out_dtype, device=x.device), _CODE[out_dtype], N
+    else:
+        out, code = _out(out, T, N, out.dtype, x.device)
+        ldo = out.stride(0) if T > 1 else N
+    L = _lib.lib()
+    if workspace is not None:
+        size = _workspace(workspace, x.device)
+    else:
+        size = L.mx_lora_workspace(T, K, E, rank)
+        if size:
+            workspace = _scratch(size, x.device, stream)
+    _call(L.mx_lora, at, stream, x.data_ptr(), _CODE[dtype], ldx if T > 1 and K else K, a.data_ptr(),
+          b.data_ptr(), E, rank, index.data_ptr(), _data(scaling), _data(base), base_code, ldb, T, N,
+          K, code, out.data_ptr(), ldo, _data(workspace), size)
+    return out
+
+
+def _lora_refusal(x, a, b, index, base, scaling):
+    """Says what is wrong with the operands of mx_lora."""
+    T, K, _ = _rows(x, "x")
+    dev, same = x.device, (x.dtype,)
     for t, name in ((a, "a"), (b, "b")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dim() != 3:
             raise ValueError(f"{name} must have three dimensions")
     E, rank, N = a.shape[0], a.shape[1], b.shape[1]
-    same = (x.dtype,)
     _buf(a, "a", (E, rank, K), same, dev)
     _buf(b, "b", (E, N, rank), same, dev)
     _buf(index, "index", (T,), _I32, dev)
     if scaling is not None:
         _buf(scaling, "scaling", (E,), _F32, dev)
-    base_code = ldb = 0
-    if base is not None:
-        rows, cols, ldb = _rows(base, "base")
-        if (rows, cols) != (T, N):
-            raise ValueError(f"base has shape {tuple(base.shape)}, expected {(T, N)}")
-        if base.device != dev:
-            raise ValueError(f"base is on {base.device}, expected {dev}")
-        base_code = _CODE[base.dtype]
-    if out is None and out_dtype is None:
-        out_dtype = x.dtype if base is None else base.dtype
-    if out is None and out_dtype in _CODE:
-        out, code, ldo = torch.empty(T, N, dtype=out_dtype, device=dev), _CODE[out_dtype], N
-    else:
-        out, code = _out(out, T, N, out.dtype if out_dtype is None else out_dtype, dev)
-        ldo = out.stride(0) if T > 1 else N
-    if workspace is not None:
-        size = _workspace(workspace, dev)
-    else:
-        size = lib().mx_lora_workspace(T, K, E, rank)
-        if size:
-            workspace = _scratch(size, dev, stream)
-    _launch("mx_lora", dev, stream, x.data_ptr(), _CODE[x.dtype], ldx if K else 0, a.data_ptr(), b.data_ptr(), E,
-            rank, index.data_ptr(), _data(scaling), _data(base), base_code, ldb, T, N, K, code,
-            out.data_ptr(), ldo, _data(workspace), size)
-    return out
+    rows, cols, _ = _rows(base, "base")
+    if (rows, cols) != (T, N):
+        raise ValueError(f"base has shape {tuple(base.shape)}, expected {(T, N)}")
+    raise ValueError(f"base is on {base.device}, expected {dev}")

@@ -3,64 +3,99 @@
 //
 // Two kernels: the first forms h = A x (fp32, in parts over K, in the workspace), the second sums the
 // parts and forms base + s B h with one rounding. Tokens come in any order, so each kernel takes 64 of
-// them at a time (a wave's lanes hold their indexes) and gives every adapter that occurs among them
-// workgroups of its own: a ballot finds its tokens, 16 of which make a matrix product's columns.
-// An adapter's weights are read once for 64 tokens, and a token meets no other adapter's weights.
-// With few tokens the candidates are the tokens (the first of an adapter counts), with few adapters
-// the adapters.
+// them at a time, a wave's lanes with an index each, and finds the adapters that occur among them by
+// ballots: group k of a chunk is the k-th of them, whose tokens are the products' rows or columns,
+// 16 at a time. An adapter's weights are read once for 64 tokens (16 in the first kernel), and a token
+// meets no other adapter's weights. The grid has a group for every adapter that there may be; those
+// that there are not come last in the order of launch, where they leave the others evenly spread (a
+// workgroup for every adapter and chunk, in that order, took 51 us for 8192 tokens, K 4096, 8 adapters
+// of rank 16: the ones with work met on few compute units).
 #include "mx_device.h"
 #include "mx_launch.h"
+
+#include <type_traits>
 
 using namespace mxd;
 
 namespace {
 
-constexpr int kChunk = 64;  // tokens a workgroup looks at
+constexpr int kChunk = 64;      // tokens a workgroup looks at
+constexpr int kMostParts = 16;  // of K
 
-// the tokens of chunk blockIdx.z that the workgroup has
+// tokens of a chunk with one adapter
 struct Members {
   int count, adapter;  // adapter -1: tokens without one
-  int token;           // this lane's: member number `lane` of them
+  int first;           // of the members the workgroup has, the first one's number
+  int token;           // this lane's: member number `lane`
 };
 
-// Candidate c is adapter c, or with by_token the adapter of the chunk's token c if no earlier one
-// has it; c == candidates: the tokens without an adapter.
-__device__ __forceinline__ Members members_of(const LoraArgs& a, int c) {
-  const int lane = threadIdx.x & 63, t = blockIdx.z * kChunk + lane;
-  int e = -2;  // no token
-  if (t < a.T) {
-    e = a.E > 0 ? a.index[t] : -1;
-    if (e < 0 || e >= a.E) e = -1;
+// Group k of a chunk: the k-th SIZE tokens of the adapters that occur, with NONE the tokens without one
+// among them (SIZE 64: an adapter's tokens are one group).
+template <bool NONE, int SIZE>
+__device__ __forceinline__ Members members_of(const LoraArgs& a, int chunk, int k) {
+  const int lane = threadIdx.x & 63, t = chunk * kChunk + lane;
+  int e = a.E;  // none
+  if (t < a.T && a.E > 0) e = a.index[t];
+  if (e < 0 || e > a.E) e = a.E;
+  const bool counts = t < a.T && (NONE || e < a.E);
+  // the lanes with this lane's adapter, from one ballot for each bit of it
+  uint64_t same = __ballot(counts);
+  for (int bits = 32 - __builtin_clz(a.E | 1), i = 0; i < bits; ++i) {
+    const bool bit = (e >> i) & 1;
+    const uint64_t ones = __ballot(bit);
+    same &= bit ? ones : ~ones;
   }
-  Members m;
-  m.adapter = c == a.candidates ? -1 : a.by_token ? __shfl(e, c) : c;
-  m.adapter = __builtin_amdgcn_readfirstlane(m.adapter);
-  const uint64_t mask = __ballot(e == m.adapter);
-  m.count = __popcll(mask);
-  if (c < a.candidates && a.by_token && (m.adapter < 0 || __builtin_ctzll(mask | (1ull << 63)) != c))
-    m.count = 0;
-  // members first, in their order: lane l's place among them, or behind them among the others
   const uint64_t below = (1ull << lane) - 1;
+  // the first lane of an adapter has its groups; those before it are the earlier ones' groups
+  const bool leads = counts && (same & below) == 0;
+  const int size = __popcll(same), groups = (size + SIZE - 1) / SIZE;
+  int before = __popcll(__ballot(leads) & below);
+#pragma unroll
+  for (int n = 2; n <= kChunk / SIZE; ++n)
+    before += __popcll(__ballot(leads && groups >= n) & below);
+  const uint64_t mine = __ballot(leads && before <= k && k < before + groups);
+  Members m;
+  m.count = 0;
+  if (mine == 0) return m;
+  const int from = __builtin_ctzll(mine);
+  m.adapter = __builtin_amdgcn_readlane(e, from);
+  if (m.adapter == a.E) m.adapter = -1;
+  m.first = SIZE * (k - __builtin_amdgcn_readlane(before, from));
+  const uint64_t mask = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)same, from) |
+                        (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(same >> 32), from) << 32;
+  m.count = __popcll(mask);
+  // members first, in their order: lane l's place among them, or behind them among the others
   const int place = (mask >> lane) & 1 ? __popcll(mask & below)
                                        : __popcll(mask) + __popcll(~mask & below);
-  m.token = blockIdx.z * kChunk + __builtin_amdgcn_ds_permute(4 * place, lane);
+  m.token = chunk * kChunk + __builtin_amdgcn_ds_permute(4 * place, lane);
   return m;
 }
 
-// A lane's 16 reduction indexes of 64 (16 g .. 16 g + 15) of one row, zeros from `left` on (a
-// multiple of 8)
+// A lane's 16 reduction indexes of 64 (16 g .. 16 g + 15) of one row
 template <bool BF16>
 struct Piece {
   u32x4 w[BF16 ? 2 : 4];
 };
 
 template <bool BF16>
-__device__ __forceinline__ Piece<BF16> load_piece(const uint8_t* p, int left) {
+__device__ __forceinline__ Piece<BF16> load_piece(const uint8_t* p) {
+  Piece<BF16> o;
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 2 : 4); ++i) o.w[i] = reinterpret_cast<const u32x4*>(p)[i];
+  return o;
+}
+
+// The same where the row has `left` of them (a multiple of 8), zeros from there on; first: its start
+template <bool BF16>
+__device__ __forceinline__ Piece<BF16> load_rest(const uint8_t* first, int64_t at, int left) {
   constexpr int PER = BF16 ? 8 : 4;
   Piece<BF16> o;
 #pragma unroll
-  for (int i = 0; i < (BF16 ? 2 : 4); ++i)
-    o.w[i] = i * PER < left ? reinterpret_cast<const u32x4*>(p)[i] : u32x4{0, 0, 0, 0};
+  for (int i = 0; i < (BF16 ? 2 : 4); ++i) {
+    const bool in = i * PER < left;
+    const u32x4 w = *reinterpret_cast<const u32x4*>(first + (in ? at + 16 * i : 0));
+    o.w[i] = in ? w : u32x4{0, 0, 0, 0};
+  }
   return o;
 }
 
@@ -84,244 +119,327 @@ __device__ __forceinline__ f32x4 multiply(const Piece<BF16>& a, const Piece<BF16
   return acc;
 }
 
-// h = A x. Grid: parts of K, candidates, chunks of tokens. The four waves take every fourth 64 of the
-// part's K; their sums are joined in LDS in the waves' order. RT: 16-row tiles of A.
+// h = A x. Grid: parts of K, chunks of tokens, groups of 16 of their tokens. The four waves take every
+// fourth 64 of the part's K; their sums are joined in LDS in the waves' order. RT: 16-row tiles of A.
+// (Two or four 16s of tokens a workgroup, which read A once for them, are no better: 2048 tokens, K
+// 4096, rank 64: 16.8 us, 17.5 and 15.0; 256 tokens of 64 adapters, K 8192, rank 32: 15.7, 18.4 and 19.8.)
 template <bool BF16, int RT>
 __global__ __launch_bounds__(256) void lora_down_kernel(const LoraArgs a) {
   __shared__ __attribute__((aligned(16))) float sums[4][RT][16][20];
-  const Members m = members_of(a, blockIdx.y);
+  const Members m = members_of<false, 16>(a, blockIdx.y, blockIdx.z);
   if (m.count == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4, wave = tid >> 6;
-  constexpr int E = BF16 ? 2 : 4, TT = kChunk / 16;
+  constexpr int E = BF16 ? 2 : 4;
   const int steps = (a.K + 63) / 64;
-  const int from = (int)((int64_t)steps * blockIdx.x / gridDim.x);
-  const int to = (int)((int64_t)steps * (blockIdx.x + 1) / gridDim.x);
-  const int tiles = (m.count + 15) / 16;
+  const int from = steps * blockIdx.x / gridDim.x, to = steps * (blockIdx.x + 1) / gridDim.x;
   const uint8_t* rows[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
     rows[r] = static_cast<const uint8_t*>(a.a) +
               ((int64_t)m.adapter * a.r + min(16 * r + i, a.r - 1)) * a.K * E;
-  const uint8_t* tokens[TT];
+  const uint8_t* x = static_cast<const uint8_t*>(a.x) +
+                     (int64_t)__shfl(m.token, min(m.first + i, m.count - 1)) * a.ldx * E;
+  f32x4 acc[RT];
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
-    tokens[t] = static_cast<const uint8_t*>(a.x) +
-                (int64_t)__shfl(m.token, min(16 * t + i, m.count - 1)) * a.ldx * E;
-  f32x4 acc[TT][RT];
+  for (int r = 0; r < RT; ++r) acc[r] = f32x4{0, 0, 0, 0};
+  // whole steps, the next one's weights and values on their way
+  const int whole = min(to, a.K / 64);
+  int s = from + wave;
+  if (s < whole) {
+    auto load = [&](int step, Piece<BF16>& v, Piece<BF16>(&w)[RT]) {
+      const int64_t k = (64 * (int64_t)step + 16 * g) * E;
+      v = load_piece<BF16>(x + k);
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
+      for (int r = 0; r < RT; ++r) w[r] = load_piece<BF16>(rows[r] + k);
+    };
+    Piece<BF16> v, w[RT];
+    load(s, v, w);
+    for (; s < whole; s += 4) {
+      Piece<BF16> v2, w2[RT];
+      load(s + 4 < whole ? s + 4 : s, v2, w2);
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[t][r] = f32x4{0, 0, 0, 0};
-  for (int s = from + wave; s < to; s += 4) {
+      for (int r = 0; r < RT; ++r) acc[r] = multiply<BF16>(w[r], v, acc[r]);
+      v = v2;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) w[r] = w2[r];
+    }
+  }
+  if (s < to) {  // the last, K % 64 of it
     const int k = 64 * s + 16 * g, left = a.K - k;
-    Piece<BF16> w[RT];
+    const Piece<BF16> v = load_rest<BF16>(x, (int64_t)k * E, left);
 #pragma unroll
-    for (int r = 0; r < RT; ++r) w[r] = load_piece<BF16>(rows[r] + (int64_t)k * E, left);
-#pragma unroll
-    for (int t = 0; t < TT; ++t)
-      if (t < tiles) {
-        const Piece<BF16> x = load_piece<BF16>(tokens[t] + (int64_t)k * E, left);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) acc[t][r] = multiply<BF16>(w[r], x, acc[t][r]);
-      }
+    for (int r = 0; r < RT; ++r)
+      acc[r] = multiply<BF16>(load_rest<BF16>(rows[r], (int64_t)k * E, left), v, acc[r]);
   }
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
-    if (t < tiles) {
-      __syncthreads();
+  for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(&sums[wave][r][i][4 * g]) = acc[r];
+  __syncthreads();
+  for (int e = tid; e < RT * 256; e += 256) {
+    const int col = e / (16 * RT), row = e % (16 * RT);  // a token's r values in a row
+    const int token = __shfl(m.token, min(m.first + col, 63));
+    if (m.first + col < m.count && row < a.r) {
+      float v = 0.0f;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(&sums[wave][r][i][4 * g]) = acc[t][r];
-      __syncthreads();
-      for (int e = tid; e < RT * 256; e += 256) {
-        const int col = e / (16 * RT), row = e % (16 * RT);  // a token's r values in a row
-        const int token = __shfl(m.token, min(16 * t + col, 63));
-        if (16 * t + col < m.count && row < a.r) {
-          float v = 0.0f;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) v += sums[w][row / 16][col][row % 16];
-          a.h[((int64_t)blockIdx.x * a.T + token) * a.r + row] = v;
-        }
-      }
+      for (int w = 0; w < 4; ++w) v += sums[w][row / 16][col][row % 16];
+      a.h[((int64_t)blockIdx.x * a.T + token) * a.r + row] = v;
     }
+  }
+}
+
+// Four values of a row from `at` on, `n` of them inside it, as they are in memory (bf16: two words);
+// WIDE: all four, at an address for one load
+template <bool BF16, bool WIDE>
+__device__ __forceinline__ u32x4 load4(const void* p, int64_t at, int n) {
+  if constexpr (WIDE) {
+    if constexpr (!BF16) return *reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + at);
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+    return u32x4{w.x, w.y, 0, 0};
+  } else {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) {
+        if constexpr (BF16) w[i / 2] |= (uint32_t)static_cast<const uint16_t*>(p)[at + i] << (16 * (i % 2));
+        else w[i] = static_cast<const uint32_t*>(p)[at + i];
+      }
+    return u32x4{w[0], w[1], w[2], w[3]};
+  }
 }
 
 template <bool BF16>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  if constexpr (BF16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-  return static_cast<const float*>(p)[i];
+__device__ __forceinline__ f32x4 values4(const u32x4& w) {
+  if constexpr (!BF16) return __builtin_bit_cast(f32x4, w);
+  return f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u),
+               __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xFFFF0000u)};
 }
 
-__device__ __forceinline__ void store1(void* p, bool bf16, int64_t i, float v) {
-  if (bf16) {
-    const __bf16 b = (__bf16)v;
-    static_cast<uint16_t*>(p)[i] = __builtin_bit_cast(uint16_t, b);
+template <bool BF16, bool WIDE>
+__device__ __forceinline__ void store4(void* p, int64_t at, int n, const f32x4& v) {
+  const bf16x2_t lo = {(__bf16)v[0], (__bf16)v[1]}, hi = {(__bf16)v[2], (__bf16)v[3]};
+  const uint32_t w[2] = {__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+  if constexpr (WIDE) {
+    if constexpr (BF16) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<f32x4*>(static_cast<float*>(p) + at) = v;
   } else {
-    static_cast<float*>(p)[i] = v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) {
+        if constexpr (BF16) static_cast<uint16_t*>(p)[at + i] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+        else static_cast<float*>(p)[at + i] = v[i];
+      }
   }
 }
 
-// 16 values of a row: n from `at` on, `n` of them inside it; whole and aligned rows by 16 bytes
-__device__ __forceinline__ void load16(const void* p, bool bf16, bool wide, int64_t at, int n, float (&v)[16]) {
-  if (wide && n >= 16) {
-    if (bf16) {
-      const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at);
-      float t[8];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        widen_bf16x8(q[i], t);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[8 * i + j] = t[j];
-      }
-    } else {
-      const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 t = q[i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[4 * i + j] = t[j];
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i < n ? bf16 ? load1<true>(p, at + i) : load1<false>(p, at + i) : 0.0f;
-  }
-}
-
-__device__ __forceinline__ void store16(void* p, bool bf16, bool wide, int64_t at, int n, const float (&v)[16]) {
-  if (wide && n >= 16) {
-    if (bf16) {
-      uint32_t w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bf16x2_t t = {(__bf16)v[2 * i], (__bf16)v[2 * i + 1]};
-        w[i] = __builtin_bit_cast(uint32_t, t);
-      }
-      u32x4* q = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + at);
-      q[0] = u32x4{w[0], w[1], w[2], w[3]};
-      q[1] = u32x4{w[4], w[5], w[6], w[7]};
-    } else {
-      f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p) + at);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) store1(p, bf16, at + i, v[i]);
-  }
-}
-
-// out = base + s B h. Grid: slabs of 256 rows of B, candidates and the tokens without an adapter,
-// chunks of tokens. A wave has 64 rows: tile q's row i is row 16 (i / 4) + 4 q + i % 4 of them, so that
-// a lane ends up with 16 neighbours of a token's output. h goes in as three bf16 terms that add up
-// to the fp32 value (fp32 weights: as it is).
+// out = base + s B h. Grid: slabs of B's rows, chunks of tokens, adapters of a chunk and its tokens without one. A wave has 64 rows at a time: tile q's column i is row 4 i + q of them, so that a lane has
+// four neighbours of an output row and 16 lanes 64 of them, and the tokens are the products' rows. h goes in
+// as three bf16 terms that add up to the fp32 value (fp32 weights: as it is). base and B are on their way
+// while h is summed.
 template <bool BF16, int RT>
-__global__ __launch_bounds__(256) void lora_up_kernel(const LoraArgs a) {
-  constexpr int TT = kChunk / 16, PAD = 16 * RT + 4, JS = BF16 ? 32 : 16;
-  __shared__ __attribute__((aligned(16))) float h[kChunk][PAD];
-  const Members m = members_of(a, blockIdx.y);
-  if (m.count == 0) return;
-  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 256 + (tid >> 6) * 64;
-  const int tiles = (m.count + 15) / 16;
-  f32x4 acc[TT][4];
+struct Up {
+  static constexpr int JS = BF16 ? 32 : 16;                         // of the rank in a product
+  static constexpr int W = BF16 && RT == 1 ? 32 : 16 * RT;          // the rank, filled up with zeros
+  static constexpr int JT = W / JS, NT = BF16 ? 3 : 1;
+  typedef typename std::conditional<BF16, uint16_t, float>::type term_t;
+  struct Shared {
+    term_t h[NT][kChunk][W + (BF16 ? 8 : 4)];
+  };
+
+  // h of the members, as the products take it: zeros from r to W; rows behind the members' are not set, a
+  // product's other rows do not depend on them. Four lanes have four of a token's r values, each every
+  // fourth part of K, and join them as (0 + 1) + (2 + 3); a wave has 16 such values a turn, and the loads of
+  // TURNS turns and ROUNDS times 4 parts are under way at once.
+  template <int ROUNDS, int TURNS>
+  static __device__ __forceinline__ void sum_parts(const LoraArgs& a, const Members& m, float scale,
+                                                   Shared& sh) {
+    const int tid = threadIdx.x, part = tid & 3, fours = a.r / 4, all = m.count * fours;
+    const int64_t stride = (int64_t)a.T * a.r;
+    for (int e0 = 0; e0 < all; e0 += 64 * TURNS) {
+      f32x4 v[TURNS][ROUNDS];
+      int col[TURNS], j[TURNS];
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
+      for (int k = 0; k < TURNS; ++k) {
+        const int e = min(e0 + 64 * k + tid / 4, all - 1);
+        col[k] = e / fours;
+        j[k] = 4 * (e - col[k] * fours);
+        const float* p = a.h + (int64_t)__shfl(m.token, col[k]) * a.r + j[k];
+        if (k == 0 || e0 + 64 * k < all) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc[t][q] = f32x4{0, 0, 0, 0};
-  if (m.adapter >= 0) {
-    const float scale = a.scaling ? a.scaling[m.adapter] : 1.0f;
-    for (int e0 = 0; e0 < 16 * tiles * 16 * RT; e0 += 256) {
-      const int e = e0 + tid, col = e / (16 * RT), j = e % (16 * RT);
-      const int token = __shfl(m.token, min(col, m.count - 1));
-      float v = 0.0f;
-      if (col < m.count && j < a.r)
-        for (int s = 0; s < a.parts; ++s) v += a.h[((int64_t)s * a.T + token) * a.r + j];
-      if (col < kChunk) h[col][j] = v * scale;
+          for (int s = 0; s < ROUNDS; ++s)
+            v[k][s] = *reinterpret_cast<const f32x4*>(p + min(4 * s + part, a.parts - 1) * stride);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < TURNS; ++k) {
+        if (k > 0 && e0 + 64 * k >= all) break;
+        float one = 0.0f;  // this lane's of the four
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          float own = 0.0f;
+#pragma unroll
+          for (int s = 0; s < ROUNDS; ++s) own += 4 * s + part < a.parts ? v[k][s][x] : 0.0f;
+          const float pair = own + dpp_f32<kQuadXor1>(own);
+          const float sum = pair + dpp_f32<kQuadXor2>(pair);
+          if (x == part) one = sum * scale;
+        }
+        put(sh, col[k], j[k] + part, one);
+      }
     }
-    __syncthreads();
-    if (n0 >= a.N) return;
-    const uint8_t* rows[4];
+    const int rest = W - a.r;
+    for (int e = tid; e < m.count * rest; e += 256) put(sh, e / rest, a.r + e % rest, 0.0f);
+  }
+
+  static __device__ __forceinline__ void put(Shared& sh, int col, int j, float v) {
+    if constexpr (BF16) {
+      uint32_t o[3];
+      split_pair<3>(v, 0.0f, o);
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      rows[q] = static_cast<const uint8_t*>(a.b) +
-                ((int64_t)m.adapter * a.N + min(n0 + 16 * (i >> 2) + 4 * q + (i & 3), a.N - 1)) * a.r *
-                    (BF16 ? 2 : 4);
-    for (int j0 = 0; j0 < a.r; j0 += JS) {
-      const int j = j0 + (BF16 ? 8 : 4) * g;
-      u32x4 w[4];
+      for (int n = 0; n < 3; ++n) sh.h[n][col][j] = (uint16_t)o[n];
+    } else {
+      sh.h[0][col][j] = v;
+    }
+  }
+
+  // Four neighbours of base's rows of tile `tile`'s tokens 4 g .., at n. BASE: 0 none, 1 fp32, 2 bf16; WIDE:
+  // all inside the row, at an address for one load.
+  template <int BASE, bool WIDE>
+  static __device__ __forceinline__ void load_base(const LoraArgs& a, const Members& m, int tile, int n,
+                                                   u32x4 (&base)[4]) {
+    const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        w[q] = j < a.r ? *reinterpret_cast<const u32x4*>(rows[q] + j * (BF16 ? 2 : 4)) : u32x4{0, 0, 0, 0};
+    for (int r = 0; r < 4; ++r) {
+      const int64_t token = __shfl(m.token, min(16 * tile + 4 * g + r, m.count - 1));
+      base[r] = BASE == 0 ? u32x4{0, 0, 0, 0} : load4<BASE == 2, WIDE>(a.base, token * a.ldb + n, a.N - n);
+    }
+  }
+  static __device__ __forceinline__ void first_base(const LoraArgs& a, const Members& m, bool wide, int n,
+                                                    u32x4 (&base)[4]) {
+    if (!a.base) load_base<0, false>(a, m, 0, n, base);
+    else if (a.base_bf16) wide ? load_base<2, true>(a, m, 0, n, base) : load_base<2, false>(a, m, 0, n, base);
+    else wide ? load_base<1, true>(a, m, 0, n, base) : load_base<1, false>(a, m, 0, n, base);
+  }
+
+  // 64 rows of B (those at n = n0 + 4 i ..), all members; base holds the first tile's
+  template <int BASE, bool OUT, bool WIDE>
+  static __device__ __forceinline__ void slab(const LoraArgs& a, const Members& m, const Shared& sh, int n,
+                                              const u32x4 (&w)[JT][4], u32x4 (&base)[4]) {
+    const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, tiles = (m.count + 15) / 16;
+    for (int t = 0; t < tiles; ++t) {
+      f32x4 v[4], acc[4];
 #pragma unroll
-      for (int t = 0; t < TT; ++t)
-        if (t < tiles) {
+      for (int r = 0; r < 4; ++r) {
+        v[r] = values4<BASE == 2>(base[r]);
+        acc[r] = f32x4{0, 0, 0, 0};
+      }
+      if (t + 1 < tiles) load_base<BASE, WIDE>(a, m, t + 1, n, base);
+      if (m.adapter >= 0) {
+#pragma unroll
+        for (int k = 0; k < JT; ++k) {
+          const int j = k * JS + (BF16 ? 8 : 4) * g;
           if constexpr (BF16) {
-            float v[8];
-            // columns past r were never written beyond the tile's width
-            if (j < 16 * RT) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = h[16 * t + i][j + e];
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-            }
-            uint32_t o[4][3];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) split_pair<3>(v[2 * e], v[2 * e + 1], o[e]);
-#pragma unroll
-            for (int n = 2; n >= 0; --n) {
-              const bf16x8_t x = __builtin_bit_cast(bf16x8_t, u32x4{o[0][n], o[1][n], o[2][n], o[3][n]});
+            for (int e = 2; e >= 0; --e) {
+              const bf16x8_t x = *reinterpret_cast<const bf16x8_t*>(&sh.h[e][16 * t + i][j]);
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w[q]), x,
-                                                                    acc[t][q], 0, 0, 0);
+                acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    x, __builtin_bit_cast(bf16x8_t, w[k][q]), acc[q], 0, 0, 0);
             }
           } else {
-            const f32x4 v = *reinterpret_cast<const f32x4*>(&h[16 * t + i][j]);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(&sh.h[0][16 * t + i][j]);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[q][e]), v[e], acc[t][q],
-                                                                 0, 0, 0);
+                acc[q] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], __uint_as_float(w[k][q][e]), acc[q],
+                                                              0, 0, 0);
           }
         }
-    }
-  } else if (n0 >= a.N || a.in_place) {
-    return;
-  }
-  const int n = n0 + 16 * g, left = a.N - n;
+      }
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
-    if (t < tiles) {
-      const int64_t token = __shfl(m.token, min(16 * t + i, m.count - 1));
-      if (16 * t + i < m.count && left > 0) {
-        float v[16];
-        if (a.base)
-          load16(a.base, a.base_bf16, a.base_wide, token * a.ldb + n, left, v);
-        else
+      for (int r = 0; r < 4; ++r) {
+        const int at = 16 * t + 4 * g + r;
+        const int64_t token = __shfl(m.token, min(at, 63));
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = 0.0f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * q + e] += acc[t][q][e];
-        store16(a.out, a.out_bf16, a.out_wide, token * a.ldo + n, left, v);
+        for (int q = 0; q < 4; ++q) v[r][q] += acc[q][r];
+        if (at < m.count) store4<OUT, WIDE>(a.out, token * a.ldo + n, a.N - n, v[r]);
       }
     }
+  }
+
+  template <bool WIDE>
+  static __device__ __forceinline__ void any_slab(const LoraArgs& a, const Members& m, const Shared& sh,
+                                                  int n, const u32x4 (&w)[JT][4], u32x4 (&v)[4]) {
+    const int base = !a.base ? 0 : a.base_bf16 ? 2 : 1;
+    if (a.out_bf16) {
+      if (base == 1) slab<1, true, WIDE>(a, m, sh, n, w, v);
+      else if (base == 2) slab<2, true, WIDE>(a, m, sh, n, w, v);
+      else slab<0, true, WIDE>(a, m, sh, n, w, v);
+    } else {
+      if (base == 1) slab<1, false, WIDE>(a, m, sh, n, w, v);
+      else if (base == 2) slab<2, false, WIDE>(a, m, sh, n, w, v);
+      else slab<0, false, WIDE>(a, m, sh, n, w, v);
+    }
+  }
+};
+
+template <bool BF16, int RT>
+__global__ __launch_bounds__(256) void lora_up_kernel(const LoraArgs a) {
+  typedef Up<BF16, RT> U;
+  __shared__ __attribute__((aligned(16))) typename U::Shared sh;
+  const Members m = members_of<true, kChunk>(a, blockIdx.y, blockIdx.z);
+  if (m.count == 0 || (m.adapter < 0 && a.in_place)) return;
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
+  int n0 = (blockIdx.x * a.slabs * 4 + (tid >> 6)) * 64;
+  u32x4 w[U::JT][4];
+  auto load_weights = [&](int n) {
+#pragma unroll
+    for (int k = 0; k < U::JT; ++k) {
+      const int j = k * U::JS + (BF16 ? 8 : 4) * g;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t row = (int64_t)m.adapter * a.N + min(n + q, a.N - 1);
+        const u32x4 t = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.b) +
+                                                        (row * a.r + (j < a.r ? j : 0)) * (BF16 ? 2 : 4));
+        w[k][q] = j < a.r ? t : u32x4{0, 0, 0, 0};
+      }
+    }
+  };
+  const bool rows_wide = a.out_wide && (!a.base || a.base_wide);
+  u32x4 base[4];
+  if (n0 < a.N) U::first_base(a, m, rows_wide && n0 + 64 <= a.N, n0 + 4 * i, base);
+  if (m.adapter >= 0) {
+    if (n0 < a.N) load_weights(n0 + 4 * i);
+    const float scale = a.scaling ? a.scaling[m.adapter] : 1.0f;
+    if (a.parts <= 4) U::template sum_parts<1, (RT >= 4 ? 8 : 4)>(a, m, scale, sh);
+    else U::template sum_parts<kMostParts / 4, 2>(a, m, scale, sh);
+    __syncthreads();
+  }
+  for (int slab = 0; slab < a.slabs && n0 < a.N; ++slab, n0 += 256) {
+    const int n = n0 + 4 * i;
+    const bool wide = rows_wide && n0 + 64 <= a.N;
+    if (slab > 0) {
+      U::first_base(a, m, wide, n, base);
+      if (m.adapter >= 0) load_weights(n);
+    }
+    if (wide) U::template any_slab<true>(a, m, sh, n, w, base);
+    else U::template any_slab<false>(a, m, sh, n, w, base);
+  }
 }
 
 template <bool BF16, int RT>
 hipError_t launch(const LoraArgs& a) {
   const unsigned chunks = (unsigned)((a.T + kChunk - 1) / kChunk);
   if (a.K > 0 && a.E > 0) {
-    hipLaunchKernelGGL((lora_down_kernel<BF16, RT>), dim3(a.parts, a.candidates, chunks), dim3(256), 0,
+    // adapters that a chunk may have, and their 16s of tokens
+    const int tokens = a.T < kChunk ? a.T : kChunk, most = a.E < tokens ? a.E : tokens;
+    const int groups = most + (tokens - most) / 16;
+    hipLaunchKernelGGL((lora_down_kernel<BF16, RT>), dim3(a.parts, chunks, groups), dim3(256), 0,
                        (hipStream_t)a.stream, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
+  const int slab = 256 * a.slabs;
   hipLaunchKernelGGL((lora_up_kernel<BF16, RT>),
-                     dim3((unsigned)((a.N + 255) / 256), a.candidates + 1, chunks), dim3(256), 0,
+                     dim3((unsigned)((a.N + slab - 1) / slab), chunks, a.groups), dim3(256), 0,
                      (hipStream_t)a.stream, a);
   return hipGetLastError();
 }
@@ -334,15 +452,11 @@ hipError_t pick(const LoraArgs& a) {
   return launch<BF16, 8>(a);
 }
 
-// workgroups that look for members: the adapters, or the tokens of a chunk if they are fewer
-int candidates(int64_t T, int64_t E) {
-  const int64_t tokens = T < kChunk ? T : kChunk;
-  return (int)(E <= tokens ? E : tokens);
-}
-
+// Parts of K, so that the groups of up to 16 tokens with one adapter that there may be make about 512
+// workgroups; a part has 4 steps of 64 at least, one for each wave.
 int parts_of(int64_t T, int64_t K, int64_t E) {
-  const int64_t groups = candidates(T, E) * ((T + kChunk - 1) / kChunk);
-  const int64_t steps = (K + 63) / 64, most = steps / 4 > 0 ? steps / 4 : 1;
+  const int64_t tiles = (T + 15) / 16, apart = E < T ? E : T, groups = tiles > apart ? tiles : apart;
+  const int64_t steps = (K + 63) / 64, most = steps < 8 ? 1 : steps < 4 * kMostParts ? steps / 4 : kMostParts;
   const int64_t want = groups > 0 ? (512 + groups - 1) / groups : 1;
   return (int)(want < most ? want : most);
 }
@@ -354,8 +468,15 @@ int64_t mx_lora_workspace_bytes(int64_t T, int64_t K, int64_t E, int64_t r) {
 }
 
 hipError_t mx_launch_lora(LoraArgs a) {
-  a.candidates = candidates(a.T, a.E);
-  a.by_token = a.candidates < a.E;
   a.parts = a.K > 0 ? parts_of(a.T, a.K, a.E) : 0;
+  const int tokens = a.T < kChunk ? a.T : kChunk;
+  a.groups = a.E < tokens ? a.E + 1 : tokens;  // adapters of a chunk, and its tokens without one
+  // A workgroup sums h once for 256, 512 or 1024 outputs: as many as leave 448 workgroups, if every
+  // eighth adapter occurs in a chunk (2048 tokens, N 14336, rank 64, 4 adapters: 49, 48 and 44 us; 1024
+  // tokens, N 4096, rank 128: 27, 30 and 42; 2048 tokens of 64 adapters, N 4096, rank 16: 105, 84 and 72).
+  const int64_t chunks = (a.T + kChunk - 1) / kChunk, slabs = (a.N + 255) / 256;
+  const int64_t apart = a.E < 16 ? 1 : a.E < kChunk ? a.E / 8 : kChunk / 8;
+  a.slabs = 1;
+  while (a.slabs < 4 && chunks * slabs * apart >= 448 * 2 * a.slabs) a.slabs *= 2;
   return a.bf16 ? pick<true>(a) : pick<false>(a);
 }

@@ -622,7 +622,7 @@ mx_status mx_lora(const void* x, int32_t dtype, int64_t ldx, const void* a, cons
   LoraArgs l{x, a, b, index, scaling, base, out, static_cast<float*>(workspace), ldx, ldb, ldo,
              (int)T, (int)N, any ? (int)K : 0, any ? (int)adapters : 0, any ? (int)rank : 8,
              dtype == MX_BF16, base_dtype == MX_BF16, out_dtype == MX_BF16, wide(base, ldb, bsize),
-             wide(out, ldo, osize), in_place, stream, 0, 0, false};
+             wide(out, ldo, osize), in_place, stream, 0, 0, 0};
   return launch_status(mx_launch_lora(l));
 }
 

@@ -200,8 +200,7 @@ struct LoraArgs {
   bool bf16, base_bf16, out_bf16, base_wide, out_wide;  // wide: rows at 16-byte addresses
   bool in_place;         // out is base
   void* stream;
-  int candidates, parts;  // set by the launcher, as by_token
-  bool by_token;
+  int parts, groups, slabs;  // set by the launcher
 };
 int64_t mx_lora_workspace_bytes(int64_t T, int64_t K, int64_t E, int64_t r);
 hipError_t mx_launch_lora(LoraArgs a);
