@@ -13,6 +13,8 @@
 #include "mx_device.h"
 #include "mx_launch.h"
 
+#include <type_traits>
+
 using namespace mxd;
 
 namespace {
@@ -398,29 +400,66 @@ __device__ __forceinline__ int steps_of(const CacheArgs& c, const Sequence& s) {
   return max((min(s.length, c.max_tokens) + TS - 1) / TS, 1);
 }
 
+// the value that a lane has, as a scalar
+__device__ __forceinline__ int64_t lane64(int64_t v, int from) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)v, from) |
+                   (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), from) << 32);
+}
+
+// The call's sequences. Up to 64 of them are in the lanes of every wave, and nothing is read again or
+// exchanged between waves.
+struct Sequences {
+  Sequence own;  // of sequence `lane`, where there are 64 at most
+  bool few;
+  __device__ __forceinline__ Sequence get(const CacheArgs& c, int b) const {
+    if (!few) return sequence_of(c, b, c.rows);
+    return Sequence{__builtin_amdgcn_readlane(own.row0, b), __builtin_amdgcn_readlane(own.n, b),
+                    __builtin_amdgcn_readlane(own.length, b)};
+  }
+};
+
+// the workgroup's steps, once the line's length is known; false: none
+__device__ __forceinline__ bool bounds_of(Line& o, int unit) {
+  o.units = (int)min((int64_t)gridDim.x, o.all);
+  if (unit >= o.units) return false;
+  o.at = bound_of(o, unit);
+  o.end = bound_of(o, unit + 1);
+  return true;
+}
+
 template <int R, int TS>
-__device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs& a, int unit, Line& o) {
+__device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs& a, int unit, Line& o,
+                                        Sequences& seqs) {
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  seqs.few = c.seqs <= 64;
+  if (seqs.few) {
+    const bool is = lane < c.seqs;
+    seqs.own = sequence_of(c, is ? lane : 0, c.rows);
+    const int n = is ? items_of<R>(seqs.own, a.group) : 0, st = steps_of<TS>(c, seqs.own);
+    int64_t end = (int64_t)n * st;
+    int items = n;
+    for (int i = 1; i < c.seqs; i *= 2) {
+      const int64_t t = __shfl_up(end, i);
+      const int k = __shfl_up(items, i);
+      if (lane >= i) {
+        end += t;
+        items += k;
+      }
+    }
+    o.all = lane64(end, c.seqs - 1);
+    if (o.all == 0 || !bounds_of(o, unit)) return false;
+    const int64_t begin = end - (int64_t)n * st;
+    o.b = __builtin_ctzll(__ballot(is && o.at >= begin && o.at < end));
+    const int64_t first = lane64(begin, o.b);
+    const int steps = __builtin_amdgcn_readlane(st, o.b);
+    o.tile = (int)((o.at - first) / steps);
+    o.item = __builtin_amdgcn_readlane(items - n, o.b) + o.tile;
+    o.first = first + (int64_t)o.tile * steps;
+    return true;
+  }
   __shared__ int64_t sums[kWaves];
   __shared__ int64_t got_first;
   __shared__ int got_b, got_item, counts[kWaves];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  auto bounds = [&]() {
-    o.units = (int)min((int64_t)gridDim.x, o.all);
-    if (unit >= o.units) return false;
-    o.at = bound_of(o, unit);
-    o.end = bound_of(o, unit + 1);
-    return true;
-  };
-  if (c.seqs == 1) {
-    const Sequence s = sequence_of(c, 0, c.rows);
-    const int st = steps_of<TS>(c, s);
-    o.all = (int64_t)items_of<R>(s, a.group) * st;
-    if (o.all == 0 || !bounds()) return false;
-    o.b = 0;
-    o.tile = o.item = (int)(o.at / st);
-    o.first = (int64_t)o.item * st;
-    return true;
-  }
   int64_t all = 0;
   for (int b = tid; b < c.seqs; b += 64 * kWaves) {
     const Sequence s = sequence_of(c, b, c.rows);
@@ -433,7 +472,7 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
   o.all = 0;
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) o.all += sums[i];
-  if (o.all == 0 || !bounds()) return false;
+  if (o.all == 0 || !bounds_of(o, unit)) return false;
   int64_t before = 0;
   int items_before = 0;
   for (int b0 = 0; b0 < c.seqs; b0 += 64 * kWaves) {  // the same turns in every wave
@@ -670,9 +709,10 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
   }
   // The next step's keys are on their way while this one's softmax and values are worked on, and its
   // values during its scores, in the registers that have just become free.
-  for (; step < end; step += TW) {
+  auto take = [&](auto follows) {
+    constexpr bool more = decltype(follows)::value;
     int page[NB];
-    look(step + 2 * TW, page);
+    if constexpr (more) look(step + 2 * TW, page);
     f32x4 sc[KT];
     const uint32_t kscale = k.scale;
     const bool nan_k = kscale == 0xFFu;
@@ -691,7 +731,7 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
         }
       }
     }
-    load_keys(next, k);
+    if constexpr (more) load_keys(next, k);
     bool whole = (step + 1) * TS <= least;
 #pragma unroll
     for (int n = 0; n < NB; ++n) whole = whole && here.has[n];
@@ -772,10 +812,14 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
           acc[d] = mfma(x, __builtin_bit_cast(bf16x8_t, u32x4{w[0][n], w[1][n], w[2][n], w[3][n]}), acc[d]);
       }
     }
-    load_values(next, v);
-    here = next;
-    next = find(step + 2 * TW, page);
-  }
+    if constexpr (more) {
+      load_values(next, v);
+      here = next;
+      next = find(step + 2 * TW, page);
+    }
+  };
+  for (; step + TW < end; step += TW) take(std::true_type());
+  if (step < end) take(std::false_type());
 
   // the waves' parts of a row, joined in the waves' order
   l = row_sum(l);
@@ -827,11 +871,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_kernel(
     const CacheArgs c, const AttentionArgs a, const int32_t* __restrict__ pages) {
   __shared__ __attribute__((aligned(16))) AttentionShared<D> sh;
   Line line;
-  if (!line_of<16 * WR, TS>(c, a, blockIdx.x, line)) return;
+  Sequences seqs;
+  if (!line_of<16 * WR, TS>(c, a, blockIdx.x, line, seqs)) return;
   for (;;) {
     // offsets that fall may make more items than the workspace has slots
     if ((int64_t)blockIdx.x + line.item >= a.slots) return;
-    const Sequence s = sequence_of(c, line.b, c.rows);
+    const Sequence s = seqs.get(c, line.b);
     attend<D, FMT, BF16, WR, TS>(c, a, pages, line, s, sh);
     line.at = line.first + steps_of<TS>(c, s);
     if (line.at >= line.end) return;
@@ -841,59 +886,66 @@ __global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_kernel(
       line.tile = 0;
       do {
         if (++line.b >= c.seqs) return;
-      } while (sequence_of(c, line.b, c.rows).n == 0);
+      } while (seqs.get(c, line.b).n == 0);
     }
     __syncthreads();  // what the waves read of sh is written again
   }
 }
 
-// The segments of a row joined: a workgroup for each token and query head, 4 channels a thread, the
-// segments among its groups of D / 4 threads.
-template <int D, bool BF16>
+// The segments of a row joined. THREADS for each token and query head: 256 where the rows are few and
+// may have many segments, a wave where there are many rows. A thread has 4 channels; groups of D / 4
+// threads take every GROUPS-th segment.
+template <int D, bool BF16, int THREADS>
 __global__ __launch_bounds__(256) void cache_attention_join_kernel(const CacheArgs c,
                                                                    const AttentionArgs a, int R) {
-  constexpr int PER = D / 4, GROUPS = 256 / PER;
-  __shared__ __attribute__((aligned(16))) float sums[GROUPS][D];
-  __shared__ float tops[4], all[GROUPS];
-  const int t = blockIdx.x, qhead = blockIdx.y, head = qhead / a.group, tid = threadIdx.x;
-  if (c.offsets && (t < c.offsets[0] || t >= c.offsets[c.seqs])) return;
-  const int4 w = a.where[(int64_t)t * a.group + qhead % a.group];
+  constexpr int PER = D / 4, GROUPS = THREADS / PER, ROWS = 256 / THREADS;
+  __shared__ __attribute__((aligned(16))) float sums[ROWS][GROUPS][D];
+  __shared__ float tops[ROWS][GROUPS], all[ROWS][GROUPS];
+  const int which = threadIdx.x / THREADS, tid = threadIdx.x % THREADS;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + which;
+  const int t = (int)(row / a.heads), qhead = (int)(row - (int64_t)t * a.heads), head = qhead / a.group;
+  bool is = t < c.rows;
+  if (is && c.offsets) is = t >= c.offsets[0] && t < c.offsets[c.seqs];
+  int4 w = make_int4(0, 0, 0, 0);
+  if (is) w = a.where[(int64_t)t * a.group + qhead - head * a.group];
   // one part: written already; and tables that are none (offsets that fall) end here
-  if (w.y <= 1 || w.x < 0 || w.z < 0 || w.z >= R || (int64_t)w.x + w.y > a.slots) return;
-  auto slot = [&](int k) { return ((int64_t)(w.x + k) * c.heads + head) * R + w.z; };
-  float top = -__builtin_inff();
-  for (int k = tid; k < w.y; k += 256) top = fmaxf(top, a.stat[2 * slot(k)]);
-#pragma unroll
-  for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
-  if ((tid & 63) == 0) tops[tid >> 6] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-  const float base = top == -__builtin_inff() ? 0.0f : top;
+  if (w.y <= 1 || w.x < 0 || w.z < 0 || w.z >= R || (int64_t)w.x + w.y > a.slots) is = false;
   const int group = tid / PER, ch = 4 * (tid % PER);
-  if (group < GROUPS) {
+  if (is && group < GROUPS) {
     f32x4 o = {0, 0, 0, 0};
-    float sum = 0.0f;
+    float top = -__builtin_inff(), sum = 0.0f;
 #pragma unroll 4
     for (int k = group; k < w.y; k += GROUPS) {
-      const int64_t s = slot(k);
-      const float f = __builtin_amdgcn_exp2f(a.stat[2 * s] - base);
-      sum += a.stat[2 * s + 1] * f;
+      const int64_t s = ((int64_t)(w.x + k) * c.heads + head) * R + w.z;
+      const float m = a.stat[2 * s], l = a.stat[2 * s + 1];
       const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + s * D + ch);
+      const float next = fmaxf(top, m), base = next == -__builtin_inff() ? 0.0f : next;
+      const float f = __builtin_amdgcn_exp2f(top - base), h = __builtin_amdgcn_exp2f(m - base);
+      sum = sum * f + l * h;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) o[x] += v[x] * f;
+      for (int x = 0; x < 4; ++x) o[x] = o[x] * f + v[x] * h;
+      top = next;
     }
-    *reinterpret_cast<f32x4*>(&sums[group][ch]) = o;
-    if (ch == 0) all[group] = sum;
+    *reinterpret_cast<f32x4*>(&sums[which][group][ch]) = o;
+    if (ch == 0) {
+      tops[which][group] = top;
+      all[which][group] = sum;
+    }
   }
   __syncthreads();
-  if (tid < PER) {
+  if (is && tid < PER) {
+    float top = tops[which][0];
+#pragma unroll
+    for (int k = 1; k < GROUPS; ++k) top = fmaxf(top, tops[which][k]);
+    const float base = top == -__builtin_inff() ? 0.0f : top;
     f32x4 o = {0, 0, 0, 0};
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < GROUPS; ++k) {
-      sum += all[k];
+      const float f = __builtin_amdgcn_exp2f(tops[which][k] - base);
+      sum += all[which][k] * f;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) o[x] += sums[k][4 * tid + x];
+      for (int x = 0; x < 4; ++x) o[x] += sums[which][k][4 * tid + x] * f;
     }
     store_row<BF16>(a, t, qhead, 4 * tid, o, base, sum);
   }
@@ -993,8 +1045,14 @@ struct Attention {
     else if (p.wr == 2) main<2>(c, a, p);
     else main<4>(c, a, p);
     if (hipError_t e = hipGetLastError(); e != hipSuccess || !p.join) return e;
-    hipLaunchKernelGGL((cache_attention_join_kernel<D, BF16>), dim3((unsigned)c.rows, (unsigned)a.heads),
-                       dim3(256), 0, (hipStream_t)a.stream, c, a, 16 * p.wr);
+    const int64_t rows = (int64_t)c.rows * a.heads;
+    // 4096 rows: 5.4 us with a wave each, 7.0 with a workgroup; 32 rows of 64 parts: 5.6 and 4.2
+    if (rows < 2048)
+      hipLaunchKernelGGL((cache_attention_join_kernel<D, BF16, 256>), dim3((unsigned)rows), dim3(256), 0,
+                         (hipStream_t)a.stream, c, a, 16 * p.wr);
+    else
+      hipLaunchKernelGGL((cache_attention_join_kernel<D, BF16, 64>), dim3((unsigned)((rows + 3) / 4)),
+                         dim3(256), 0, (hipStream_t)a.stream, c, a, 16 * p.wr);
     return hipGetLastError();
   }
 };
