@@ -25,18 +25,16 @@ struct Sequence {
 };
 
 // Tables are device data: whatever they hold, rows stay inside [0, T) and pages inside the cache.
-__device__ __forceinline__ Sequence sequence_of(const CacheArgs& c, int b, int rows) {
+__device__ __forceinline__ Sequence sequence_from(int from, int to, int length, int rows) {
   Sequence s;
-  if (c.offsets) {
-    const int from = c.offsets[b], to = c.offsets[b + 1];
-    s.row0 = min(max(from, 0), rows);
-    s.n = max(min(to, rows) - s.row0, 0);
-  } else {
-    s.row0 = b;
-    s.n = b < rows ? 1 : 0;
-  }
-  s.length = max(c.lengths[b], 0);
+  s.row0 = min(max(from, 0), rows);
+  s.n = max(min(to, rows) - s.row0, 0);
+  s.length = max(length, 0);
   return s;
+}
+__device__ __forceinline__ Sequence sequence_of(const CacheArgs& c, int b, int rows) {
+  return c.offsets ? sequence_from(c.offsets[b], c.offsets[b + 1], c.lengths[b], rows)
+                   : sequence_from(b, b + 1, c.lengths[b], rows);
 }
 
 // the place in a page table of the page that holds positions 32 bn ..: bn / page_blocks by a product,
@@ -64,21 +62,31 @@ struct Piece {
 };
 
 __device__ __forceinline__ bool piece_of(const CacheArgs& c, int unit, int rows, Piece& o) {
-  __shared__ int found;
+  __shared__ int found[4];
   int b = unit, j = 0;
+  Sequence s;
   if (c.offsets) {
-    if (threadIdx.x == 0) found = -1;
+    if (threadIdx.x == 0) found[0] = -1;
     __syncthreads();
     for (int i = threadIdx.x; i < c.seqs; i += blockDim.x) {
-      const int first = (c.offsets[i] >> 5) + 2 * i, next = (c.offsets[i + 1] >> 5) + 2 * i + 2;
-      if (first <= unit && unit < next) found = i;
+      const int from = c.offsets[i], to = c.offsets[i + 1], length = c.lengths[i];
+      if ((from >> 5) + 2 * i <= unit && unit < (to >> 5) + 2 * i + 2) {
+        found[0] = i;
+        found[1] = from;
+        found[2] = to;
+        found[3] = length;
+      }
     }
     __syncthreads();
-    b = __builtin_amdgcn_readfirstlane(found);
+    b = __builtin_amdgcn_readfirstlane(found[0]);
     if (b < 0) return false;
-    j = unit - ((c.offsets[b] >> 5) + 2 * b);
+    const int from = __builtin_amdgcn_readfirstlane(found[1]);
+    j = unit - ((from >> 5) + 2 * b);
+    s = sequence_from(from, __builtin_amdgcn_readfirstlane(found[2]),
+                      __builtin_amdgcn_readfirstlane(found[3]), rows);
+  } else {
+    s = sequence_of(c, b, rows);
   }
-  const Sequence s = sequence_of(c, b, rows);
   const int start = s.length - s.n;  // negative with more rows than tokens
   o.b = b;
   o.bn = (start >> 5) + j;
@@ -170,31 +178,30 @@ __global__ __launch_bounds__(D) void cache_write_kernel(const CacheArgs c, const
   if (!piece_of(c, blockIdx.x, c.rows, p)) return;
   const int head = blockIdx.y;
   const bool values = blockIdx.z != 0;
-  const int64_t block = block_of(c, c.pages, p.b, p.bn, head);
-  if (block < 0) return;
   const CacheRows src = values ? v : k;
   const int esize = BF16 ? 2 : 4;
   const uint8_t* rows = static_cast<const uint8_t*>(src.p) + (int64_t)head * src.head * esize;
-  uint8_t* codes = (values ? c.vq : c.kq) + block * (32 * D);
-  uint8_t* scale = (values ? c.vs : c.ks) + block;
   const int tid = threadIdx.x;
   // token slot of run i, and its first channel
   auto slot = [&](int i) { return values ? 4 * (tid & 7) + i : (tid + i * D) / (D / 8); };
   auto channel = [&](int i) { return 8 * (values ? tid >> 3 : (tid + i * D) % (D / 8)); };
+  // Slots that the call does not fill read a row that it has (a load under a condition would wait for
+  // the one before).
   float w[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    load8<BF16>(rows + ((int64_t)(p.row + min(max(slot(i), p.lo), p.hi - 1)) * src.token + channel(i)) * esize,
+                w[i]);
+  const int64_t block = block_of(c, c.pages, p.b, p.bn, head);  // while the rows are on their way
+  if (block < 0) return;
+  uint8_t* codes = (values ? c.vq : c.kq) + block * (32 * D);
+  uint8_t* scale = (values ? c.vs : c.ks) + block;
+  const uint32_t was = p.lo > 0 ? *scale : 0u;
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int s = slot(i);
-    if (s >= p.lo && s < p.hi)
-      load8<BF16>(rows + ((int64_t)(p.row + s) * src.token + channel(i)) * esize, w[i]);
-    else
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[i][j] = 0.0f;
+  for (int i = 0; i < 4; ++i)  // the row read twice changes no maximum
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = max(m, abs_bits(w[i][j]));
-  }
-  const uint32_t was = p.lo > 0 ? *scale : 0u;
   m = workgroup_max<D / 64>(m);
   const uint32_t sb = max(scale_byte_fp8<CEIL, FMT>(m), was);
   const bool bad = sb == 0xFFu;  // every code is zero
