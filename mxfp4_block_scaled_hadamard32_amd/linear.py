@@ -20,8 +20,10 @@ Two variants from the same page:
   * fmt = "mxfp8": the query / key projections in MXFP8, X and W in E4M3 and dY in E5M2.
 
 Around the layer: MXRMSNorm (the norm before it, with the residual's addition), MXNormLinear (both
-in one, the norm's kernel writing the Fprop operand's codes) and MXDecodeLinear (the layer's
-product for a few tokens against weights quantized once).
+in one, the norm's kernel writing the Fprop operand's codes) and, for decoding, MXDecodeLinear (the
+layer's product for a few tokens against weights quantized once, with MXAdapters beside them where
+requests have low-rank adapters of their own) and MXCache (keys and values in 8 bits, and the
+attention over them).
 """
 from __future__ import annotations
 
@@ -30,10 +32,10 @@ from dataclasses import dataclass, field
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (MX_E4M3, MX_E5M2, MX_ROUND_RNE, MX_SCALE_FLOOR, mx_gemm_dgrad, mx_gemm_fprop,
-               mx_gemm_mxfp8, mx_gemm_wgrad, mx_gemv, mx_quantize, mx_quantize_2d_blocks,
-               mx_quantize_mxfp8, mx_rmsnorm, mx_rmsnorm_backward, mx_rmsnorm_quant,
-               mx_rmsnorm_quant_mxfp8)
+from . import (MX_E4M3, MX_E5M2, MX_ROUND_RNE, MX_SCALE_FLOOR, mx_cache_attention, mx_cache_read,
+               mx_cache_write, mx_gemm_dgrad, mx_gemm_fprop, mx_gemm_mxfp8, mx_gemm_wgrad, mx_gemv,
+               mx_lora, mx_quantize, mx_quantize_2d_blocks, mx_quantize_mxfp8, mx_rmsnorm,
+               mx_rmsnorm_backward, mx_rmsnorm_quant, mx_rmsnorm_quant_mxfp8)
 
 
 @dataclass
@@ -346,7 +348,93 @@ class MXDecodeLinear(torch.nn.Module):
         return cls(layer.weight, layer.cfg.fprop_q, layer.cfg.w_block)
 
     @torch.no_grad()
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
-        y = mx_gemv(_readable(_flat(x)), self.codes, self.scales, self.w_block, hadamard=self.spec.hadamard,
-                    sign_mask=self.spec.sign_mask, alpha_exp=_alpha(self.spec), out_dtype=x.dtype)
+    def forward(self, x: torch.Tensor, adapters: "MXAdapters | None" = None,
+                index: torch.Tensor | None = None) -> torch.Tensor:
+        """adapters, index: token i of x (flattened) also goes through adapter index[i] of them, int32,
+        none where it is outside their number; the sum is rounded once."""
+        if (adapters is None) != (index is None):
+            raise ValueError("adapters and the tokens' indexes are given together")
+        flat = _readable(_flat(x))
+        y = mx_gemv(flat, self.codes, self.scales, self.w_block, hadamard=self.spec.hadamard,
+                    sign_mask=self.spec.sign_mask, alpha_exp=_alpha(self.spec),
+                    out_dtype=x.dtype if adapters is None else torch.float32)
+        if adapters is not None:
+            y = mx_lora(flat, adapters.a, adapters.b, index.reshape(-1), base=y,
+                        scaling=adapters.scaling, out_dtype=x.dtype)
         return y.view(*x.shape[:-1], y.shape[1])
+
+
+class MXAdapters(torch.nn.Module):
+    """Low-rank adapters of one layer, B A of each: a [E][rank][K], b [E][N][rank] of the activations'
+    type (K and rank multiples of 8, rank at most 128), scaling [E] (ones when None)."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, scaling: torch.Tensor | None = None):
+        super().__init__()
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise ValueError("adapters are a [E][rank][K] and b [E][N][rank]")
+        self.register_buffer("a", a.detach().clone(memory_format=torch.contiguous_format))
+        self.register_buffer("b", b.detach().clone(memory_format=torch.contiguous_format))
+        self.register_buffer("scaling", None if scaling is None else
+                             scaling.detach().to(torch.float32, copy=True).contiguous())
+
+
+def _readable_heads(t):
+    """t [T][heads][dim] (the binding refuses others) in a layout that the kernels read, a copy where it
+    has to be."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        return t
+    size, d = t.element_size(), t.shape[2]
+    token, head, one = t.stride()
+    fits = lambda n, s: n <= 1 or (s >= d and s * size % 16 == 0)  # noqa: E731
+    if ((one == 1 or d <= 1) and t.data_ptr() % 16 == 0 and fits(t.shape[0], token)
+            and fits(t.shape[1], head)
+            and (t.shape[0] <= 1 or t.shape[1] <= 1 or token >= (t.shape[1] - 1) * head + d
+                 or head >= (t.shape[0] - 1) * token + d)):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+class MXCache(torch.nn.Module):
+    """Keys and values of one layer in 8-bit codes with one scale for 32 tokens of a head, in pages.
+    cache(q, k, v, pages, lengths, offsets) writes the new tokens and returns their attention: q [T]
+    [query heads][dim], k and v [T][heads][dim], bf16 or fp32; pages [B][..] the page table, lengths
+    [B] the sequences' tokens with the new ones, offsets [B + 1] which rows are whose (None: row b is
+    sequence b's), all int32. Which pages a sequence gets is the caller's."""
+
+    def __init__(self, pages: int, heads: int, dim: int, page_size: int = 64, fmt: int = MX_E4M3,
+                 scale_rule: int = MX_SCALE_FLOOR, device="cuda"):
+        super().__init__()
+        if page_size % 32:
+            raise ValueError("a page holds a multiple of 32 tokens")
+        if dim not in (64, 128, 192, 256):
+            raise ValueError("dim must be 64, 128, 192 or 256")
+        self.fmt, self.scale_rule = fmt, scale_rule
+        byte = dict(dtype=torch.uint8, device=device)
+        blocks = page_size // 32
+        self.register_buffer("kq", torch.zeros((pages, heads, page_size, dim), **byte))
+        self.register_buffer("vq", torch.zeros((pages, heads, blocks, dim, 32), **byte))
+        self.register_buffer("ks", torch.zeros((pages, heads, blocks), **byte))
+        self.register_buffer("vs", torch.zeros((pages, heads, blocks), **byte))
+
+    def _tensors(self):
+        return self.kq, self.ks, self.vq, self.vs
+
+    @torch.no_grad()
+    def write(self, k, v, pages, lengths, offsets=None) -> None:
+        mx_cache_write(_readable_heads(k), _readable_heads(v), *self._tensors(), pages, lengths,
+                       offsets=offsets, fmt=self.fmt, scale_rule=self.scale_rule)
+
+    @torch.no_grad()
+    def read(self, pages, lengths, offsets=None, rows=None, out_dtype=torch.bfloat16):
+        """(k, v) of the sequences' newest tokens, [rows][heads][dim]."""
+        return mx_cache_read(*self._tensors(), pages, lengths, offsets=offsets, rows=rows,
+                             fmt=self.fmt, out_dtype=out_dtype)
+
+    @torch.no_grad()
+    def attend(self, q, pages, lengths, offsets=None, scale=None) -> torch.Tensor:
+        return mx_cache_attention(_readable_heads(q), *self._tensors(), pages, lengths,
+                                  offsets=offsets, scale=scale, fmt=self.fmt)
+
+    def forward(self, q, k, v, pages, lengths, offsets=None, scale=None) -> torch.Tensor:
+        self.write(k, v, pages, lengths, offsets)
+        return self.attend(q, pages, lengths, offsets, scale)
