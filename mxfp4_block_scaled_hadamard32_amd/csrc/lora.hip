@@ -71,33 +71,43 @@ __device__ __forceinline__ Members members_of(const LoraArgs& a, int chunk, int 
   return m;
 }
 
-// A lane's 16 reduction indexes of 64 (16 g .. 16 g + 15) of one row
+// 64 reduction indexes of 16 rows, in a wave. As operands of a product (a lane has 16 g .. 16 g + 15 of
+// row i) lanes that follow one another have different rows: read that way each of a load's 16 bytes is
+// a look into the cache of its own. Rows are read whole instead, 8 or 16 lanes each, and put in order
+// through LDS, in an area of the wave's own.
 template <bool BF16>
 struct Piece {
   u32x4 w[BF16 ? 2 : 4];
 };
 
 template <bool BF16>
-__device__ __forceinline__ Piece<BF16> load_piece(const uint8_t* p) {
-  Piece<BF16> o;
-#pragma unroll
-  for (int i = 0; i < (BF16 ? 2 : 4); ++i) o.w[i] = reinterpret_cast<const u32x4*>(p)[i];
-  return o;
-}
+struct Exchange {
+  static constexpr int E = BF16 ? 2 : 4, WORDS = BF16 ? 2 : 4, PER = 4 * E, ROWS = 64 / PER;
+  static constexpr int PITCH = 64 * E + 16;
+  typedef uint8_t Area[16 * PITCH];
+  // the row of word w that this lane reads, and its byte in the 64 indexes
+  static __device__ __forceinline__ int row(int w) { return ROWS * w + (threadIdx.x & 63) / PER; }
+  static __device__ __forceinline__ int byte() { return 16 * (threadIdx.x & (PER - 1)); }
 
-// The same where the row has `left` of them (a multiple of 8), zeros from there on; first: its start
-template <bool BF16>
-__device__ __forceinline__ Piece<BF16> load_rest(const uint8_t* first, int64_t at, int left) {
-  constexpr int PER = BF16 ? 8 : 4;
-  Piece<BF16> o;
+  static __device__ __forceinline__ Piece<BF16> operand(const Piece<BF16>& rows, uint8_t* area) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int i = 0; i < (BF16 ? 2 : 4); ++i) {
-    const bool in = i * PER < left;
-    const u32x4 w = *reinterpret_cast<const u32x4*>(first + (in ? at + 16 * i : 0));
-    o.w[i] = in ? w : u32x4{0, 0, 0, 0};
+    for (int w = 0; w < WORDS; ++w) *reinterpret_cast<u32x4*>(area + row(w) * PITCH + byte()) = rows.w[w];
+    order();
+    Piece<BF16> o;
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w)
+      o.w[w] = *reinterpret_cast<const u32x4*>(area + (lane & 15) * PITCH + (lane >> 4) * 16 * E + 16 * w);
+    order();
+    return o;
   }
-  return o;
-}
+  // a wave's LDS accesses complete in order; the compiler keeps them so
+  static __device__ __forceinline__ void order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+};
 
 // acc += a b^T over a piece: bf16 two products of 32, fp32 sixteen of 4 (lane group g's value e of
 // word w is index 16 g + 4 w + e on either side)
@@ -129,47 +139,71 @@ __global__ __launch_bounds__(256) void lora_down_kernel(const LoraArgs a) {
   const Members m = members_of<false, 16>(a, blockIdx.y, blockIdx.z);
   if (m.count == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4, wave = tid >> 6;
-  constexpr int E = BF16 ? 2 : 4;
+  typedef Exchange<BF16> X;
+  __shared__ __attribute__((aligned(16))) typename X::Area area[4];
+  constexpr int E = X::E;
   const int steps = (a.K + 63) / 64;
   const int from = steps * blockIdx.x / gridDim.x, to = steps * (blockIdx.x + 1) / gridDim.x;
-  const uint8_t* rows[RT];
+  constexpr int WORDS = X::WORDS;
+  const uint8_t* rows[RT][WORDS];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
-    rows[r] = static_cast<const uint8_t*>(a.a) +
-              ((int64_t)m.adapter * a.r + min(16 * r + i, a.r - 1)) * a.K * E;
-  const uint8_t* x = static_cast<const uint8_t*>(a.x) +
-                     (int64_t)__shfl(m.token, min(m.first + i, m.count - 1)) * a.ldx * E;
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w)
+      rows[r][w] = static_cast<const uint8_t*>(a.a) + X::byte() +
+                   ((int64_t)m.adapter * a.r + min(16 * r + X::row(w), a.r - 1)) * a.K * E;
+  const uint8_t* x[WORDS];
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w)
+    x[w] = static_cast<const uint8_t*>(a.x) + X::byte() +
+           (int64_t)__shfl(m.token, min(m.first + X::row(w), m.count - 1)) * a.ldx * E;
   f32x4 acc[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) acc[r] = f32x4{0, 0, 0, 0};
+  auto take = [&](const Piece<BF16>& v, const Piece<BF16>(&w)[RT]) {
+    const Piece<BF16> right = X::operand(v, area[wave]);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = multiply<BF16>(X::operand(w[r], area[wave]), right, acc[r]);
+  };
   // whole steps, the next one's weights and values on their way
   const int whole = min(to, a.K / 64);
   int s = from + wave;
+  Piece<BF16> v, w[RT];
   if (s < whole) {
     auto load = [&](int step, Piece<BF16>& v, Piece<BF16>(&w)[RT]) {
-      const int64_t k = (64 * (int64_t)step + 16 * g) * E;
-      v = load_piece<BF16>(x + k);
+      const int64_t k = 64 * E * (int64_t)step;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) w[r] = load_piece<BF16>(rows[r] + k);
+      for (int n = 0; n < WORDS; ++n) v.w[n] = *reinterpret_cast<const u32x4*>(x[n] + k);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int n = 0; n < WORDS; ++n) w[r].w[n] = *reinterpret_cast<const u32x4*>(rows[r][n] + k);
     };
-    Piece<BF16> v, w[RT];
     load(s, v, w);
     for (; s < whole; s += 4) {
       Piece<BF16> v2, w2[RT];
       load(s + 4 < whole ? s + 4 : s, v2, w2);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) acc[r] = multiply<BF16>(w[r], v, acc[r]);
+      take(v, w);
       v = v2;
 #pragma unroll
       for (int r = 0; r < RT; ++r) w[r] = w2[r];
     }
   }
-  if (s < to) {  // the last, K % 64 of it
-    const int k = 64 * s + 16 * g, left = a.K - k;
-    const Piece<BF16> v = load_rest<BF16>(x, (int64_t)k * E, left);
+  if (s < to) {  // the last, K % 64 of it: zeros from there on
+    const bool in = X::byte() < (a.K - 64 * s) * E;
+    const int64_t k = in ? 64 * E * (int64_t)s : -X::byte();
+    const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-      acc[r] = multiply<BF16>(load_rest<BF16>(rows[r], (int64_t)k * E, left), v, acc[r]);
+    for (int n = 0; n < WORDS; ++n) {
+      const u32x4 t = *reinterpret_cast<const u32x4*>(x[n] + k);
+      v.w[n] = in ? t : zero;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const u32x4 y = *reinterpret_cast<const u32x4*>(rows[r][n] + k);
+        w[r].w[n] = in ? y : zero;
+      }
+    }
+    take(v, w);
   }
 #pragma unroll
   for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(&sums[wave][r][i][4 * g]) = acc[r];
