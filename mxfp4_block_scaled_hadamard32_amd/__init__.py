@@ -721,7 +721,7 @@ def mx_lora(x, a, b, index, base=None, scaling=None, out_dtype=None, out=None, w
     at most 128), index [T] int32 (outside [0, E): base alone), base [T][N] bf16 or fp32 or None
     (zeros), scaling [E] fp32 or None (ones) -> out [T][N] of out_dtype (base's type when None, x's
     without a base). out may be base itself. workspace: a uint8 buffer of at least
-    lib().mx_lora_workspace(T, K, E, rank) bytes, allocated per call when None."""
+    lib().mx_lora_workspace(...) bytes, allocated per call when None and wanted."""
     try:
         T, K = x.shape
         E, rank, _ = a.shape
@@ -756,7 +756,7 @@ def mx_lora(x, a, b, index, base=None, scaling=None, out_dtype=None, out=None, w
     if workspace is not None:
         size = _workspace(workspace, x.device)
     else:
-        size = L.mx_lora_workspace(T, K, E, rank)
+        size = L.mx_lora_workspace(_CODE[dtype], T, N, K, E, rank)
         if size:
             workspace = _scratch(size, x.device, stream)
     _call(L.mx_lora, at, stream, x.data_ptr(), _CODE[dtype], ldx if T > 1 and K else K, a.data_ptr(),

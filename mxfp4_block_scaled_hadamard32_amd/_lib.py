@@ -91,7 +91,7 @@ def lib() -> ctypes.CDLL:
     L.mx_cache_attention_workspace.restype = i64
     L.mx_lora.argtypes = [vp, i32, i64, vp, vp, i64, i64, vp, vp, vp, i32, i64, i64, i64, i64, i32,
                           vp, i64, vp, i64, vp]
-    L.mx_lora_workspace.argtypes = [i64, i64, i64, i64]
+    L.mx_lora_workspace.argtypes = [i32, i64, i64, i64, i64, i64]
     L.mx_lora_workspace.restype = i64
     for name in ("mx_quantize", "mx_quantize_2d", "mx_dequantize", "mx_gemm_fprop",
                  "mx_gemm_dgrad", "mx_gemm_wgrad", "mx_gemm_fprop_quant", "mx_quantize_mxfp8",

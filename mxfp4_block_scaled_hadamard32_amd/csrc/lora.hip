@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kChunk = 64;      // tokens a workgroup looks at
 constexpr int kMostParts = 16;  // of K
+constexpr int kSmallWaves = 16;
 
 // tokens of a chunk with one adapter
 struct Members {
@@ -129,22 +130,13 @@ __device__ __forceinline__ f32x4 multiply(const Piece<BF16>& a, const Piece<BF16
   return acc;
 }
 
-// h = A x. Grid: parts of K, chunks of tokens, groups of 16 of their tokens. The four waves take every
-// fourth 64 of the part's K; their sums are joined in LDS in the waves' order. RT: 16-row tiles of A.
-// (Two or four 16s of tokens a workgroup, which read A once for them, are no better: 2048 tokens, K
-// 4096, rank 64: 16.8 us, 17.5 and 15.0; 256 tokens of 64 adapters, K 8192, rank 32: 15.7, 18.4 and 19.8.)
+// A x of 16 members (m.first ..), steps from + wave, from + wave + waves, .. of 64 up to `to`. RT: 16-row
+// tiles of A; area: the wave's own.
 template <bool BF16, int RT>
-__global__ __launch_bounds__(256) void lora_down_kernel(const LoraArgs a) {
-  __shared__ __attribute__((aligned(16))) float sums[4][RT][16][20];
-  const Members m = members_of<false, 16>(a, blockIdx.y, blockIdx.z);
-  if (m.count == 0) return;
-  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4, wave = tid >> 6;
+__device__ __forceinline__ void accumulate(const LoraArgs& a, const Members& m, int first, int from, int to,
+                                           int wave, int waves, uint8_t* area, f32x4 (&acc)[RT]) {
   typedef Exchange<BF16> X;
-  __shared__ __attribute__((aligned(16))) typename X::Area area[4];
-  constexpr int E = X::E;
-  const int steps = (a.K + 63) / 64;
-  const int from = steps * blockIdx.x / gridDim.x, to = steps * (blockIdx.x + 1) / gridDim.x;
-  constexpr int WORDS = X::WORDS;
+  constexpr int E = X::E, WORDS = X::WORDS;
   const uint8_t* rows[RT][WORDS];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
@@ -156,14 +148,13 @@ __global__ __launch_bounds__(256) void lora_down_kernel(const LoraArgs a) {
 #pragma unroll
   for (int w = 0; w < WORDS; ++w)
     x[w] = static_cast<const uint8_t*>(a.x) + X::byte() +
-           (int64_t)__shfl(m.token, min(m.first + X::row(w), m.count - 1)) * a.ldx * E;
-  f32x4 acc[RT];
+           (int64_t)__shfl(m.token, min(first + X::row(w), m.count - 1)) * a.ldx * E;
 #pragma unroll
   for (int r = 0; r < RT; ++r) acc[r] = f32x4{0, 0, 0, 0};
   auto take = [&](const Piece<BF16>& v, const Piece<BF16>(&w)[RT]) {
-    const Piece<BF16> right = X::operand(v, area[wave]);
+    const Piece<BF16> right = X::operand(v, area);
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[r] = multiply<BF16>(X::operand(w[r], area[wave]), right, acc[r]);
+    for (int r = 0; r < RT; ++r) acc[r] = multiply<BF16>(X::operand(w[r], area), right, acc[r]);
   };
   // whole steps, the next one's weights and values on their way
   const int whole = min(to, a.K / 64);
@@ -180,9 +171,9 @@ __global__ __launch_bounds__(256) void lora_down_kernel(const LoraArgs a) {
         for (int n = 0; n < WORDS; ++n) w[r].w[n] = *reinterpret_cast<const u32x4*>(rows[r][n] + k);
     };
     load(s, v, w);
-    for (; s < whole; s += 4) {
+    for (; s < whole; s += waves) {
       Piece<BF16> v2, w2[RT];
-      load(s + 4 < whole ? s + 4 : s, v2, w2);
+      load(s + waves < whole ? s + waves : s, v2, w2);
       take(v, w);
       v = v2;
 #pragma unroll
@@ -205,6 +196,24 @@ __global__ __launch_bounds__(256) void lora_down_kernel(const LoraArgs a) {
     }
     take(v, w);
   }
+}
+
+// h = A x. Grid: parts of K, chunks of tokens, groups of 16 of their tokens. The four waves take every
+// fourth 64 of the part's K; their sums are joined in LDS in the waves' order.
+// (Two or four 16s of tokens a workgroup, which read A once for them, are no better: 2048 tokens, K
+// 4096, rank 64: 16.8 us, 17.5 and 15.0; 256 tokens of 64 adapters, K 8192, rank 32: 15.7, 18.4 and 19.8;
+// nor are workgroups of 8 or 16 waves.)
+template <bool BF16, int RT>
+__global__ __launch_bounds__(256) void lora_down_kernel(const LoraArgs a) {
+  __shared__ __attribute__((aligned(16))) float sums[4][RT][16][20];
+  __shared__ __attribute__((aligned(16))) typename Exchange<BF16>::Area area[4];
+  const Members m = members_of<false, 16>(a, blockIdx.y, blockIdx.z);
+  if (m.count == 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4, wave = tid >> 6;
+  const int steps = (a.K + 63) / 64;
+  const int from = steps * blockIdx.x / gridDim.x, to = steps * (blockIdx.x + 1) / gridDim.x;
+  f32x4 acc[RT];
+  accumulate<BF16, RT>(a, m, m.first, from, to, wave, 4, area[wave], acc);
 #pragma unroll
   for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(&sums[wave][r][i][4 * g]) = acc[r];
   __syncthreads();
@@ -352,6 +361,22 @@ struct Up {
     else wide ? load_base<1, true>(a, m, 0, n, base) : load_base<1, false>(a, m, 0, n, base);
   }
 
+  static __device__ __forceinline__ void load_weights(const LoraArgs& a, const Members& m, int n,
+                                                      u32x4 (&w)[JT][4]) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int k = 0; k < JT; ++k) {
+      const int j = k * JS + (BF16 ? 8 : 4) * g;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t row = (int64_t)m.adapter * a.N + min(n + q, a.N - 1);
+        const u32x4 t = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.b) +
+                                                        (row * a.r + (j < a.r ? j : 0)) * (BF16 ? 2 : 4));
+        w[k][q] = j < a.r ? t : u32x4{0, 0, 0, 0};
+      }
+    }
+  }
+
   // 64 rows of B (those at n = n0 + 4 i ..), all members; base holds the first tile's
   template <int BASE, bool OUT, bool WIDE>
   static __device__ __forceinline__ void slab(const LoraArgs& a, const Members& m, const Shared& sh, int n,
@@ -422,27 +447,14 @@ __global__ __launch_bounds__(256) void lora_up_kernel(const LoraArgs a) {
   __shared__ __attribute__((aligned(16))) typename U::Shared sh;
   const Members m = members_of<true, kChunk>(a, blockIdx.y, blockIdx.z);
   if (m.count == 0 || (m.adapter < 0 && a.in_place)) return;
-  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, i = tid & 15;
   int n0 = (blockIdx.x * a.slabs * 4 + (tid >> 6)) * 64;
   u32x4 w[U::JT][4];
-  auto load_weights = [&](int n) {
-#pragma unroll
-    for (int k = 0; k < U::JT; ++k) {
-      const int j = k * U::JS + (BF16 ? 8 : 4) * g;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t row = (int64_t)m.adapter * a.N + min(n + q, a.N - 1);
-        const u32x4 t = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.b) +
-                                                        (row * a.r + (j < a.r ? j : 0)) * (BF16 ? 2 : 4));
-        w[k][q] = j < a.r ? t : u32x4{0, 0, 0, 0};
-      }
-    }
-  };
   const bool rows_wide = a.out_wide && (!a.base || a.base_wide);
   u32x4 base[4];
   if (n0 < a.N) U::first_base(a, m, rows_wide && n0 + 64 <= a.N, n0 + 4 * i, base);
   if (m.adapter >= 0) {
-    if (n0 < a.N) load_weights(n0 + 4 * i);
+    if (n0 < a.N) U::load_weights(a, m, n0 + 4 * i, w);
     const float scale = a.scaling ? a.scaling[m.adapter] : 1.0f;
     if (a.parts <= 4) U::template sum_parts<1, (RT >= 4 ? 8 : 4)>(a, m, scale, sh);
     else U::template sum_parts<kMostParts / 4, 2>(a, m, scale, sh);
@@ -453,11 +465,54 @@ __global__ __launch_bounds__(256) void lora_up_kernel(const LoraArgs a) {
     const bool wide = rows_wide && n0 + 64 <= a.N;
     if (slab > 0) {
       U::first_base(a, m, wide, n, base);
-      if (m.adapter >= 0) load_weights(n);
+      if (m.adapter >= 0) U::load_weights(a, m, n, w);
     }
     if (wide) U::template any_slab<true>(a, m, sh, n, w, base);
     else U::template any_slab<false>(a, m, sh, n, w, base);
   }
+}
+
+// Both in one launch, without a workspace, for a few tokens (see small_call): a workgroup of 16 waves
+// forms h of its adapter's tokens for itself and then 1024 outputs.
+__global__ __launch_bounds__(64 * kSmallWaves) void lora_small_kernel(const LoraArgs a) {
+  constexpr bool BF16 = true;
+  constexpr int RT = 1;
+  typedef Up<BF16, RT> U;
+  __shared__ __attribute__((aligned(16))) typename U::Shared sh;
+  // exchanged rows, then the waves' sums
+  __shared__ __attribute__((aligned(16))) union {
+    typename Exchange<BF16>::Area area[kSmallWaves];
+    float sums[kSmallWaves][16][20];
+  } part;
+  const Members m = members_of<true, kChunk>(a, 0, blockIdx.y);
+  if (m.count == 0 || (m.adapter < 0 && a.in_place)) return;
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4, wave = tid >> 6;
+  const int n0 = (blockIdx.x * kSmallWaves + wave) * 64, n = n0 + 4 * i;
+  const bool wide = a.out_wide && (!a.base || a.base_wide) && n0 + 64 <= a.N;
+  u32x4 base[4], w[U::JT][4];
+  if (n0 < a.N) U::first_base(a, m, wide, n, base);
+  if (m.adapter >= 0) {
+    if (n0 < a.N) U::load_weights(a, m, n, w);
+    const float scale = a.scaling ? a.scaling[m.adapter] : 1.0f;
+    f32x4 acc[RT];
+    accumulate<BF16, RT>(a, m, 0, 0, (a.K + 63) / 64, wave, kSmallWaves, part.area[wave], acc);
+    __syncthreads();
+    *reinterpret_cast<f32x4*>(&part.sums[wave][i][4 * g]) = acc[0];
+    __syncthreads();
+    for (int e = tid; e < 16 * U::W; e += 64 * kSmallWaves) {
+      const int col = e / U::W, row = e % U::W;
+      float v = 0.0f;
+      if (row < a.r) {
+#pragma unroll
+        for (int k = 0; k < kSmallWaves; ++k) v += part.sums[k][col][row];
+      }
+      U::put(sh, col, row, v * scale);
+    }
+    __syncthreads();
+  }
+  if (n0 >= a.N) return;
+  if (wide) U::template any_slab<true>(a, m, sh, n, w, base);
+  else U::template any_slab<false>(a, m, sh, n, w, base);
 }
 
 template <bool BF16, int RT>
@@ -478,6 +533,13 @@ hipError_t launch(const LoraArgs& a) {
   return hipGetLastError();
 }
 
+hipError_t launch_small(const LoraArgs& a) {
+  const int slab = 64 * kSmallWaves;
+  hipLaunchKernelGGL(lora_small_kernel, dim3((unsigned)((a.N + slab - 1) / slab), a.groups),
+                     dim3(64 * kSmallWaves), 0, (hipStream_t)a.stream, a);
+  return hipGetLastError();
+}
+
 template <bool BF16>
 hipError_t pick(const LoraArgs& a) {
   if (a.r <= 16) return launch<BF16, 1>(a);
@@ -495,14 +557,26 @@ int parts_of(int64_t T, int64_t K, int64_t E) {
   return (int)(want < most ? want : most);
 }
 
+// One launch: up to 16 bf16 tokens, rank 16 at most, K up to 4096, and no more workgroups than compute
+// units. It has the device for as long as the two kernels (one token, N 14336, K 4096: 8.4 us, 7.8;
+// 16 tokens of 16 adapters: 9.0, 9.9; K 2048, N 512: 5.8, 7.5) and spares the host a launch and a workspace
+// (13.7 us a call, 9 so). Beyond, each workgroup's own h costs more than the second launch (K 8192,
+// N 8192: 10.7 us, 7.9; 64 tokens of 64 adapters, N 14336, K 4096: 25, 20; rank 32: 11.0, 8.2; fp32, rank
+// 16: 14.8, 8.3).
+bool small_call(bool bf16, int64_t T, int64_t N, int64_t K, int64_t E, int64_t r) {
+  return bf16 && T <= 16 && r <= 16 && K <= 4096 && (E < T ? E : T) * ((N + 1023) / 1024) <= 256;
+}
+
 }  // namespace
 
-int64_t mx_lora_workspace_bytes(int64_t T, int64_t K, int64_t E, int64_t r) {
+int64_t mx_lora_workspace_bytes(bool bf16, int64_t T, int64_t N, int64_t K, int64_t E, int64_t r) {
+  if (small_call(bf16, T, N, K, E, r)) return 0;
   return parts_of(T, K, E) * T * r * (int64_t)sizeof(float);
 }
 
 hipError_t mx_launch_lora(LoraArgs a) {
   a.parts = a.K > 0 ? parts_of(a.T, a.K, a.E) : 0;
+  a.small = a.K > 0 && a.E > 0 && small_call(a.bf16, a.T, a.N, a.K, a.E, a.r);
   const int tokens = a.T < kChunk ? a.T : kChunk;
   a.groups = a.E < tokens ? a.E + 1 : tokens;  // adapters of a chunk, and its tokens without one
   // A workgroup sums h once for 256, 512 or 1024 outputs: as many as leave 448 workgroups, if every
@@ -512,5 +586,6 @@ hipError_t mx_launch_lora(LoraArgs a) {
   const int64_t apart = a.E < 16 ? 1 : a.E < kChunk ? a.E / 8 : kChunk / 8;
   a.slabs = 1;
   while (a.slabs < 4 && chunks * slabs * apart >= 448 * 2 * a.slabs) a.slabs *= 2;
+  if (a.small) return launch_small(a);
   return a.bf16 ? pick<true>(a) : pick<false>(a);
 }

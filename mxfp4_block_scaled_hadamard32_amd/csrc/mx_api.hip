@@ -580,11 +580,12 @@ mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, i
   return launch_status(mx_launch_cache_attention(c, a, workspace));
 }
 
-int64_t mx_lora_workspace(int64_t T, int64_t K, int64_t adapters, int64_t rank) {
-  if (T <= 0 || K <= 0 || adapters <= 0 || rank <= 0 || T > kLoraMaxTokens || K > kLoraMaxSize ||
+int64_t mx_lora_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, int64_t adapters,
+                          int64_t rank) {
+  if (T <= 0 || N <= 0 || N > kLoraMaxSize || K <= 0 || adapters <= 0 || rank <= 0 || T > kLoraMaxTokens || K > kLoraMaxSize ||
       adapters > kLoraMaxSize || rank > kLoraMaxRank)
     return 0;
-  return mx_lora_workspace_bytes(T, K, adapters, rank);
+  return mx_lora_workspace_bytes(dtype == MX_BF16, T, N, K, adapters, rank);
 }
 
 mx_status mx_lora(const void* x, int32_t dtype, int64_t ldx, const void* a, const void* b,
@@ -615,14 +616,14 @@ mx_status mx_lora(const void* x, int32_t dtype, int64_t ldx, const void* a, cons
   const Rows rx{x, ldx * esize, K * esize}, ro{out, ldo * osize, N * osize}, rb{base, ldb * bsize, N * bsize};
   const bool in_place = base == out && base_dtype == out_dtype && (ldb == ldo || T == 1);
   if (meet(rx, ro, T) || (!in_place && meet(rb, ro, T))) return MX_ERR_ARG;
-  const int64_t need = any ? mx_lora_workspace(T, K, adapters, rank) : 0;
+  const int64_t need = any ? mx_lora_workspace(dtype, T, N, K, adapters, rank) : 0;
   if (need > 0 && !workspace) return MX_ERR_NULL;
   if (need > 0 && (workspace_bytes < need || !aligned(workspace, 16))) return MX_ERR_ARG;
   auto wide = [](const void* p, int64_t ld, int64_t size) { return aligned(p, 16) && ld * size % 16 == 0; };
   LoraArgs l{x, a, b, index, scaling, base, out, static_cast<float*>(workspace), ldx, ldb, ldo,
              (int)T, (int)N, any ? (int)K : 0, any ? (int)adapters : 0, any ? (int)rank : 8,
              dtype == MX_BF16, base_dtype == MX_BF16, out_dtype == MX_BF16, wide(base, ldb, bsize),
-             wide(out, ldo, osize), in_place, stream, 0, 0, 0};
+             wide(out, ldo, osize), in_place, stream, 0, 0, 0, false};
   return launch_status(mx_launch_lora(l));
 }
 

@@ -200,7 +200,9 @@ struct LoraArgs {
   bool bf16, base_bf16, out_bf16, base_wide, out_wide;  // wide: rows at 16-byte addresses
   bool in_place;         // out is base
   void* stream;
-  int parts, groups, slabs;  // set by the launcher
+  int parts, groups, slabs;  // set by the launcher, as small
+  bool small;
 };
-int64_t mx_lora_workspace_bytes(int64_t T, int64_t K, int64_t E, int64_t r);
+// 0 where the call is one kernel
+int64_t mx_lora_workspace_bytes(bool bf16, int64_t T, int64_t N, int64_t K, int64_t E, int64_t r);
 hipError_t mx_launch_lora(LoraArgs a);

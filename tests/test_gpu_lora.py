@@ -62,6 +62,9 @@ SIZES = [  # T, N, K, rank, adapters
     (16, 256, 264, 16, 40), (37, 1003, 4128, 40, 5), (64, 512, 2720, 64, 64), (65, 130, 320, 8, 70),
     (130, 64, 1024, 128, 200), (200, 700, 96, 72, 3), (5, 1, 8192, 16, 2), (260, 33, 72, 32, 1),
     (2, 14336, 128, 48, 1),
+    # one kernel for bf16: the largest K, more tokens than adapters, N and K odd multiples
+    (16, 3000, 4096, 16, 16), (7, 1003, 1000, 8, 3), (16, 40, 8, 8, 1), (1, 14336, 4096, 16, 8),
+    (12, 2049, 3528, 16, 30),
 ]
 
 
@@ -79,10 +82,11 @@ def test_against_float64(mx, T, N, K, r, E, dtype):
         check(got, want, size)
 
 
+@pytest.mark.parametrize("T", [150, 15])
 @pytest.mark.parametrize("which", ["none", "one", "runs", "all"])
-def test_orders(mx, which):
-    """Tokens of one adapter, in runs, each its own, and none: the same bits as token by token."""
-    T, N, K, r, E = 150, 320, 512, 16, 150
+def test_orders(mx, which, T):
+    """Tokens of one adapter, in runs, each its own, and none: the same bits in any order."""
+    N, K, r, E = 320, 512, 16, 150
     x, a, b, index, scaling, base = operands(T, N, K, r, E, "bf16", seed=2)
     t = torch.arange(T, dtype=torch.int32)
     index = {"none": torch.full_like(t, -5), "one": torch.full_like(t, 149), "runs": t // 37, "all": t.flip(0)}[which]

@@ -19,7 +19,7 @@ def m():
 
 
 def call(m, **kw):
-    v = dict(dtype=1, ldx=64, adapters=4, rank=16, base_dtype=0, ldb=100, T=3, N=100, K=64, out_dtype=1,
+    v = dict(dtype=1, ldx=64, adapters=4, rank=24, base_dtype=0, ldb=100, T=3, N=100, K=64, out_dtype=1,
              ldo=100, size=1 << 30, **P)
     v.update(kw)
     return m.lib().mx_lora(*(v[k] for k in ("x", "dtype", "ldx", "a", "b", "adapters", "rank", "index",
@@ -40,7 +40,7 @@ def call(m, **kw):
     (dict(K=(1 << 26) + 8, ldx=1 << 27), "UNSUPPORTED"), (dict(adapters=(1 << 26) + 1), "UNSUPPORTED"),
     (dict(x=None), "NULL"), (dict(a=None), "NULL"), (dict(b=None), "NULL"), (dict(index=None), "NULL"),
     (dict(out=None), "NULL"), (dict(workspace=None), "NULL"),
-    (dict(workspace=P["workspace"] + 8), "ARG"), (dict(size=3 * 16 * 4 - 1), "ARG"),
+    (dict(workspace=P["workspace"] + 8), "ARG"), (dict(size=3 * 24 * 4 - 1), "ARG"),
     (dict(out=P["x"]), "ARG"), (dict(out=P["x"] + 3 * 128 - 2), "ARG"),       # on x
     (dict(out=P["base"]), "ARG"), (dict(out=P["base"] + 16, out_dtype=0), "ARG"),  # on base, not it
     (dict(out=P["base"], out_dtype=0, ldo=104), "ARG"),
@@ -52,10 +52,14 @@ def test_refusals(m, bad, status):
 def test_no_ops_and_sizes(m):
     assert call(m, T=0) == m.MX_OK and call(m, N=0) == m.MX_OK
     size = m.lib().mx_lora_workspace
-    assert size(3, 64, 4, 16) == 3 * 16 * 4
-    for none in ((0, 64, 4, 16), (3, 0, 4, 16), (3, 64, 0, 16), (3, 64, 4, 0), (-1, 64, 4, 16), (3, 64, 4, 136)):
-        assert size(*none) == 0
-    assert size(1, 4096, 8, 16) % (16 * 4) == 0
+    assert size(1, 3, 100, 64, 4, 24) == 3 * 24 * 4 and size(0, 3, 100, 64, 4, 16) == 3 * 16 * 4
+    for none in ((0, 100, 64, 4, 24), (3, 0, 64, 4, 24), (3, 100, 0, 4, 24), (3, 100, 64, 0, 24),
+                 (3, 100, 64, 4, 0), (-1, 100, 64, 4, 24), (3, 100, 64, 4, 136)):
+        assert size(1, *none) == 0
+    assert size(1, 1, 14336, 4096, 8, 64) % (64 * 4) == 0
+    assert size(1, 1, 14336, 4096, 8, 16) == 0                      # one kernel
+    assert size(1, 17, 14336, 4096, 8, 16) > 0 and size(1, 1, 64, 4104, 8, 16) > 0
+    assert size(1, 1, 64, 4096, 8, 24) > 0 and size(1, 16, 16385, 4096, 16, 16) > 0
 
 
 def test_binding_refuses_before_the_library():
