@@ -350,6 +350,10 @@ constexpr int kWaves = 4;
 // More of them, or three at a time with fewer registers, read less at once of each page and are slower
 // (64 sequences of 8192 tokens: 170 us with 512, 181 with 768 and 180 with 1024).
 constexpr int kTarget = 512;
+// Short tables: a workgroup of 8 waves for each item and head, no segments and no second kernel, while a
+// wave has a step or two and the workgroups are not many (8 heads of 128, one sequence of 512 tokens: 7.3
+// us, 9.4 divided; 16 of 256: 6.9 and 11.1; one of 1024: 11.4 and 9.9; 256 sequences of 64: 33 and 25).
+constexpr int kWholeWaves = 8, kWholeTokens = 768, kWholeItems = 1024;
 
 // 4 channels of an output row: o / sum rounded to the output's type, and once a row its log sum of
 // exponentials; a row that sees no token is zeros, -inf
@@ -434,15 +438,27 @@ __device__ __forceinline__ bool bounds_of(Line& o, int unit) {
   return true;
 }
 
-template <int R, int TS>
+template <int R, int TS, int WAVES>
 __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs& a, int unit, Line& o,
                                         Sequences& seqs) {
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  auto weight = [&](const Sequence& s) { return WAVES == kWaves ? steps_of<TS>(c, s) : 1; };
   seqs.few = c.seqs <= 64;
+  if (WAVES != kWaves && !c.offsets) {  // as many items for each sequence
+    const int each = (a.group + R - 1) / R;
+    seqs.few = false;
+    o.all = (int64_t)each * c.seqs;
+    if (!bounds_of(o, unit)) return false;
+    o.b = unit / each;
+    o.tile = unit - o.b * each;
+    o.item = unit;
+    o.first = unit;
+    return true;
+  }
   if (seqs.few) {
     const bool is = lane < c.seqs;
     seqs.own = sequence_of(c, is ? lane : 0, c.rows);
-    const int n = is ? items_of<R>(seqs.own, a.group) : 0, st = steps_of<TS>(c, seqs.own);
+    const int n = is ? items_of<R>(seqs.own, a.group) : 0, st = weight(seqs.own);
     int64_t end = (int64_t)n * st;
     int items = n;
     for (int i = 1; i < c.seqs; i *= 2) {
@@ -464,13 +480,13 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
     o.first = first + (int64_t)o.tile * steps;
     return true;
   }
-  __shared__ int64_t sums[kWaves];
+  __shared__ int64_t sums[WAVES];
   __shared__ int64_t got_first;
-  __shared__ int got_b, got_item, counts[kWaves];
+  __shared__ int got_b, got_item, counts[WAVES];
   int64_t all = 0;
-  for (int b = tid; b < c.seqs; b += 64 * kWaves) {
+  for (int b = tid; b < c.seqs; b += 64 * WAVES) {
     const Sequence s = sequence_of(c, b, c.rows);
-    all += (int64_t)items_of<R>(s, a.group) * steps_of<TS>(c, s);
+    all += (int64_t)items_of<R>(s, a.group) * weight(s);
   }
   all = wave_sum(all);
   if (lane == 0) sums[wave] = all;
@@ -478,17 +494,17 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
   __syncthreads();
   o.all = 0;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) o.all += sums[i];
+  for (int i = 0; i < WAVES; ++i) o.all += sums[i];
   if (o.all == 0 || !bounds_of(o, unit)) return false;
   int64_t before = 0;
   int items_before = 0;
-  for (int b0 = 0; b0 < c.seqs; b0 += 64 * kWaves) {  // the same turns in every wave
+  for (int b0 = 0; b0 < c.seqs; b0 += 64 * WAVES) {  // the same turns in every wave
     const int b = b0 + tid;
     int n = 0, st = 0;
     if (b < c.seqs) {
       const Sequence s = sequence_of(c, b, c.rows);
       n = items_of<R>(s, a.group);
-      st = steps_of<TS>(c, s);
+      st = weight(s);
     }
     int64_t end = (int64_t)n * st;
     int items = n;
@@ -510,7 +526,7 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
     int64_t total = 0;
     int total_items = 0;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
+    for (int i = 0; i < WAVES; ++i) {
       if (i < wave) {
         end += sums[i];
         items += counts[i];
@@ -532,7 +548,7 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
   }
   o.b = __builtin_amdgcn_readfirstlane(got_b);
   if (o.b < 0) return false;
-  const int st = steps_of<TS>(c, sequence_of(c, o.b, c.rows));
+  const int st = weight(sequence_of(c, o.b, c.rows));
   o.tile = (int)((o.at - got_first) / st);
   o.item = got_item + o.tile;
   o.first = got_first + (int64_t)o.tile * st;
@@ -598,25 +614,26 @@ struct Blocks {
   bool has[NB];
 };
 
-template <int D>
+template <int D, int WAVES>
 struct AttentionShared {
-  float part[kWaves][16][D + 4];
-  float stat[kWaves][16][2];
+  float part[WAVES][16][D + 4];
+  float stat[WAVES][16][2];
 };
 
 // One segment: the steps of an item that the workgroup has
-template <int D, int FMT, bool BF16, int WR, int TS>
+template <int D, int FMT, bool BF16, int WR, int TS, int WAVES>
 __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& a,
                                        const int32_t* __restrict__ pages, const Line& line,
-                                       const Sequence& s, AttentionShared<D>& sh) {
-  constexpr int R = 16 * WR, TW = kWaves / WR;  // rows a workgroup; waves that share a row's tokens
+                                       const Sequence& s, AttentionShared<D, WAVES>& sh) {
+  constexpr int R = 16 * WR, TW = WAVES / WR;  // rows a workgroup; waves that share a row's tokens
   constexpr int NQ = BF16 ? 1 : 3, NP = BF16 ? 2 : 3, KT = TS / 16, NB = TS / 32, PER = TS / 4;
   const int head = blockIdx.y, unit = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wr = wave % WR, wt = wave / WR;
   const int all_steps = steps_of<TS>(c, s);
-  const int from = (int)(line.at - line.first);
-  const int to = (int)min(line.end - line.first, (int64_t)all_steps);
+  constexpr bool WHOLE = WAVES != kWaves;
+  const int from = WHOLE ? 0 : (int)(line.at - line.first);
+  const int to = WHOLE ? all_steps : (int)min(line.end - line.first, (int64_t)all_steps);
   // the item's segments are those of units first_unit .. last_unit
   const int first_unit = from == 0 ? unit : unit_at(line, line.first);
   const int last_unit = to == all_steps ? unit : unit_at(line, line.first + all_steps - 1);
@@ -839,7 +856,7 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
   for (int d = 0; d < D / 16; ++d)
     *reinterpret_cast<f32x4*>(&sh.part[wave][i][16 * d + 4 * g]) = acc[d];
   __syncthreads();
-  for (int e = tid; e < R * (D / 4); e += 64 * kWaves) {
+  for (int e = tid; e < R * (D / 4); e += 64 * WAVES) {
     const int r = e / (D / 4), ch = 4 * (e % (D / 4)), at = row0 + r;
     if (at >= rows) break;
     const int w0 = r / 16, ri = r % 16;
@@ -867,24 +884,25 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
       }
     }
   }
-  if (from == 0 && head == 0 && tid < R && row0 + tid < rows) {
+  if (!WHOLE && a.where && from == 0 && head == 0 && tid < R && row0 + tid < rows) {
     const int at = row0 + tid;
     a.where[(int64_t)s.row0 * a.group + at] = make_int4(first_unit + line.item, last_unit - first_unit + 1, tid, 0);
   }
 }
 
-template <int D, int FMT, bool BF16, int WR, int TS>
-__global__ __launch_bounds__(64 * kWaves, 2) void cache_attention_kernel(
+template <int D, int FMT, bool BF16, int WR, int TS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(
     const CacheArgs c, const AttentionArgs a, const int32_t* __restrict__ pages) {
-  __shared__ __attribute__((aligned(16))) AttentionShared<D> sh;
+  __shared__ __attribute__((aligned(16))) AttentionShared<D, WAVES> sh;
   Line line;
   Sequences seqs;
-  if (!line_of<16 * WR, TS>(c, a, blockIdx.x, line, seqs)) return;
+  if (!line_of<16 * WR, TS, WAVES>(c, a, blockIdx.x, line, seqs)) return;
   for (;;) {
     // offsets that fall may make more items than the workspace has slots
     if ((int64_t)blockIdx.x + line.item >= a.slots) return;
     const Sequence s = seqs.get(c, line.b);
-    attend<D, FMT, BF16, WR, TS>(c, a, pages, line, s, sh);
+    attend<D, FMT, BF16, WR, TS, WAVES>(c, a, pages, line, s, sh);
+    if (WAVES != kWaves) return;  // the item whole
     line.at = line.first + steps_of<TS>(c, s);
     if (line.at >= line.end) return;
     line.first = line.at;
@@ -1022,6 +1040,7 @@ struct AttentionPlan {
   int wr;          // row tiles of a workgroup
   int64_t units;   // workgroups for each head
   int64_t slots;   // segments of each head, at most
+  bool whole;      // a workgroup for each item and head
   bool join;
 };
 
@@ -1032,28 +1051,31 @@ AttentionPlan plan_attention(const CacheArgs& c, const AttentionArgs& a) {
   p.wr = each <= 16 ? 1 : each <= 32 ? 2 : 4;
   const int64_t items = rows / (16 * p.wr) + c.seqs;
   const int64_t most = (c.max_tokens + step_tokens(c.dim) - 1) / step_tokens(c.dim), steps = most > 0 ? most : 1;
-  p.join = steps > 1;
+  p.whole = p.wr == 1 && c.max_tokens <= kWholeTokens && items * c.heads <= kWholeItems;
+  p.join = !p.whole && steps > 1;
   p.units = (kTarget + c.heads - 1) / c.heads;
-  if (items * steps < p.units) p.units = items * steps;
+  if (p.whole) p.units = items;
+  else if (items * steps < p.units) p.units = items * steps;
   p.slots = p.units + items;
   return p;
 }
 
 template <int D, int FMT, bool BF16>
 struct Attention {
-  template <int WR>
+  template <int WR, int WAVES>
   static void main(const CacheArgs& c, const AttentionArgs& a, const AttentionPlan& p) {
-    hipLaunchKernelGGL((cache_attention_kernel<D, FMT, BF16, WR, step_tokens(D)>),
-                       dim3((unsigned)p.units, (unsigned)c.heads), dim3(64 * kWaves), 0,
+    hipLaunchKernelGGL((cache_attention_kernel<D, FMT, BF16, WR, step_tokens(D), WAVES>),
+                       dim3((unsigned)p.units, (unsigned)c.heads), dim3(64 * WAVES), 0,
                        (hipStream_t)a.stream, c, a, c.pages);
   }
   static hipError_t run(const CacheArgs& c, const AttentionArgs& a, const AttentionPlan& p) {
-    if (p.wr == 1) main<1>(c, a, p);
-    else if (p.wr == 2) main<2>(c, a, p);
-    else main<4>(c, a, p);
+    if (p.whole) main<1, kWholeWaves>(c, a, p);
+    else if (p.wr == 1) main<1, kWaves>(c, a, p);
+    else if (p.wr == 2) main<2, kWaves>(c, a, p);
+    else main<4, kWaves>(c, a, p);
     if (hipError_t e = hipGetLastError(); e != hipSuccess || !p.join) return e;
     const int64_t rows = (int64_t)c.rows * a.heads;
-    // 4096 rows: 5.4 us with a wave each, 7.0 with a workgroup; 32 rows of 64 parts: 5.6 and 4.2
+    // 4096 rows: 4.8 us with a wave each, 6.0 with a workgroup; 32 rows of 32 parts: 5.6 and 4.3
     if (rows < 2048)
       hipLaunchKernelGGL((cache_attention_join_kernel<D, BF16, 256>), dim3((unsigned)rows), dim3(256), 0,
                          (hipStream_t)a.stream, c, a, 16 * p.wr);
@@ -1083,14 +1105,16 @@ hipError_t mx_launch_cache_read(const CacheArgs& c, const CacheRows& k, const Ca
 // [where: 16 bytes a row][part: D floats][stat: 2 floats] for each chunk's row
 int64_t mx_attention_workspace_bytes(const CacheArgs& c, const AttentionArgs& a) {
   const AttentionPlan p = plan_attention(c, a);
-  return 16 * (int64_t)c.rows * a.group + part_floats(c, p) * (c.dim + 2) * 4;
+  return p.join ? 16 * (int64_t)c.rows * a.group + part_floats(c, p) * (c.dim + 2) * 4 : 0;
 }
 
 hipError_t mx_launch_cache_attention(const CacheArgs& c, AttentionArgs a, void* workspace) {
   const AttentionPlan p = plan_attention(c, a);
   a.slots = p.slots;
-  a.where = static_cast<int4*>(workspace);
-  a.part = reinterpret_cast<float*>(a.where + (int64_t)c.rows * a.group);
-  a.stat = a.part + part_floats(c, p) * c.dim;
+  if (p.join) {
+    a.where = static_cast<int4*>(workspace);
+    a.part = reinterpret_cast<float*>(a.where + (int64_t)c.rows * a.group);
+    a.stat = a.part + part_floats(c, p) * c.dim;
+  }
   return pick<Attention>(c, a.bf16, a, p);
 }

@@ -575,8 +575,9 @@ mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, i
   AttentionArgs a{rq.p, const_cast<void*>(ro.p), lse, rq.token, rq.head, ro.token, ro.head,
                   (int)q_heads, (int)q_heads / c.heads, scale * 1.4426950408889634f,
                   dtype == MX_BF16, stream, 0, nullptr, nullptr, nullptr};
-  if (!workspace) return MX_ERR_NULL;
-  if (workspace_bytes < mx_attention_workspace_bytes(c, a)) return MX_ERR_ARG;
+  const int64_t need = mx_attention_workspace_bytes(c, a);
+  if (need > 0 && !workspace) return MX_ERR_NULL;
+  if (workspace_bytes < need) return MX_ERR_ARG;
   return launch_status(mx_launch_cache_attention(c, a, workspace));
 }
 

@@ -93,10 +93,10 @@ def test_attention_refusals(m):
     assert bad(q_heads=65538) == m.MX_ERR_UNSUPPORTED
     for s in (float("nan"), float("inf"), -float("inf")):
         assert bad(scale=s) == m.MX_ERR_ARG
-    assert bad(workspace=None) == m.MX_ERR_NULL
+    assert bad(workspace=None, table_width=40) == m.MX_ERR_NULL
     assert bad(workspace=C + 8) == m.MX_ERR_ARG
-    need = m.lib().mx_cache_attention_workspace(3, 4, ctypes.byref(cache_of(m)))
-    assert need > 0 and bad(size=need - 1) == m.MX_ERR_ARG
+    need = m.lib().mx_cache_attention_workspace(3, 4, ctypes.byref(cache_of(m, table_width=40)))
+    assert need > 0 and bad(size=need - 1, table_width=40) == m.MX_ERR_ARG
     assert bad(lse=0x30000002) == m.MX_ERR_ARG
     for b in (A, A + 64 * 2, 0x20000000, 0x22000000):  # out on q, out in the cache
         assert bad(b=b) == m.MX_ERR_ARG
@@ -120,9 +120,10 @@ def test_workspace_sizes(m):
     for bad in (dict(dim=32), dict(page_size=33), dict(seqs=-1)):
         assert size(3, 4, **bad) == -1
     assert size(3, 5) == -1 and size(3, -2) == -1 and size(2, 4) == -1
-    # room for every row's place, and for each chunk of a row its sums and two statistics
-    assert size(3, 4) >= 3 * 2 * 16
-    assert size(3, 4, table_width=1, page_size=64) == 3 * 2 * 16  # one step: nothing is divided
+    # a short table: nothing is divided; a long one: every row's place, each segment's sums and statistics
+    assert size(3, 4) == 0 and size(3, 4, table_width=12) == 0
+    assert size(3, 4, table_width=13) >= 3 * 2 * 16 + 4 * (64 + 2)
+    assert size(600, 2, seqs=600) > 0  # many workgroups
     assert m.lib().mx_cache_attention_workspace(3, 4, None) == -1
 
 

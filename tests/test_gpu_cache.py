@@ -191,7 +191,9 @@ def filled(lengths, heads, page, dim, fmt, seed=30, spread=0.4, **kw):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("fmt", [0, 1])
-@pytest.mark.parametrize("dim,page", [(64, 32), (128, 64), (192, 96), (256, 2048)])
+@pytest.mark.parametrize("dim,page,wide", [(64, 32, 25), (64, 32, None), (128, 64, 40), (128, 64, None),
+                                           (192, 96, None), (192, 96, 9), (256, 2048, None),
+                                           (256, 160, None)])
 @pytest.mark.parametrize("lengths,new,heads,group", [
     ([1, 31, 32, 33, 63, 64, 65, 200], [1] * 8, 2, 4),           # one token each
     ([0, 5, 300], [1, 1, 1], 1, 17),                             # no token; more than one row tile
@@ -199,10 +201,10 @@ def filled(lengths, heads, page, dim, fmt, seed=30, spread=0.4, **kw):
     ([70, 300], [9, 40], 1, 8),                                  # more rows than a workgroup has
     ([2, 90], [5, 33], 1, 1),                                    # rows before the first token
 ])
-def test_attention(mx, lengths, new, heads, group, dim, page, fmt, dtype):
+def test_attention(mx, lengths, new, heads, group, dim, page, wide, fmt, dtype):
     """Slots behind the tokens, blocks behind them and pages of nobody hold random bytes, NaN codes
-    and scales among them."""
-    cache, table = filled(lengths, heads, page, dim, fmt)
+    and scales among them. A table wider than the tokens: they may be divided among workgroups."""
+    cache, table = filled(lengths, heads, page, dim, fmt, width=wide)
     check_attention(mx, cache, table, lengths, new, group, dtype)
 
 
@@ -230,13 +232,17 @@ def test_attention_many_sequences(mx):
     new = [min(n, b % 3) for b, n in enumerate(lengths)]
     cache, table = filled(lengths, 1, 32, 64, 0, seed=60)
     check_attention(mx, cache, table, lengths, new, 2, "bf16")
+    cache, table = filled(lengths, 1, 32, 64, 0, seed=60, width=30)
+    check_attention(mx, cache, table, lengths, new, 2, "bf16")
+    few = 70  # more than a wave has lanes, few enough for a workgroup each
+    check_attention(mx, cache, table[:few, :4].contiguous(), lengths[:few], new[:few], 2, "bf16")
 
 
 def test_attention_not_finite_block(mx):
     """A block with scale 0xFF makes the rows NaN that see one of its tokens, and no others."""
     lengths, new = [100, 80], [10, 2]
-    for x in "kv":
-        cache, table = filled(lengths, 2, 32, 64, 0, seed=70)
+    for x, wide in (("k", None), ("v", None), ("k", 40), ("v", 40)):
+        cache, table = filled(lengths, 2, 32, 64, 0, seed=70, width=wide)
         at = cache.block(table[0], 96)  # tokens 96 .. 99: seen by the last 4 of 10 rows
         (cache.ks if x == "k" else cache.vs)[at[0], 1, at[1]] = 255
         if x == "k":
@@ -248,10 +254,11 @@ def test_attention_not_finite_block(mx):
         assert not torch.isnan(got[:, :2]).any()
 
 
-def test_attention_missing_pages(mx):
+@pytest.mark.parametrize("width", [None, 30])
+def test_attention_missing_pages(mx, width):
     """Tokens without a page are not attended to; a sequence of nothing else gives zeros."""
     lengths, new = [200, 64, 150], [3, 1, 2]
-    cache, table = filled(lengths, 2, 32, 64, 0, seed=80)
+    cache, table = filled(lengths, 2, 32, 64, 0, seed=80, width=width)
     table[0, 0], table[0, 3], table[0, 6] = -1, -7, cache.kq.shape[0]
     table[1, :] = -1
     check_attention(mx, cache, table, lengths, new, 2, "bf16")
@@ -345,11 +352,12 @@ def test_same_bits_and_streams(mx):
     assert torch.equal(r[0], r2[0]) and torch.equal(r[1], r2[1])
 
 
-def test_graph_with_growing_lengths(mx):
+@pytest.mark.parametrize("width", [None, 40])
+def test_graph_with_growing_lengths(mx, width):
     """One captured step (write, then attend) replayed as the sequences grow, beside eager work."""
     heads, group, dim, page, B = 2, 4, 64, 32, 3
     start, steps = [30, 1, 200], 5
-    table, n_pages = ref.table_of([n + steps for n in start], page, seed=120)
+    table, n_pages = ref.table_of([n + steps for n in start], page, seed=120, width=width)
     cache = ref.Cache(n_pages, heads, page, dim, 0, seed=120)
     for b in range(B):
         cache.random_sequence(table[b], start[b], 120 + b)
