@@ -5,7 +5,8 @@
  * E8M0 power-of-two scale per block of 32 elements, or per 32x32 tile) with an optional
  * 32-point Walsh-Hadamard rotation, and multiplies MXFP4 operands with gfx950's block-scaled
  * matrix cores for the three GEMMs of a linear layer (forward, input gradient, weight
- * gradient).
+ * gradient). For decoding it has the product of a few tokens, adapters beside it, and a cache of
+ * keys and values with the attention over it.
  *
  * Sources (web pages; cited by title and section):
  *  [P1] "Block-Scaled MXFP4 With Stochastic Hadamard Rounding Matches BF16 Convergence on 70B

@@ -750,7 +750,7 @@ def mx_lora(x, a, b, index, base=None, scaling=None, out_dtype=None, out=None, w
             raise TypeError("out_dtype must be bfloat16 or float32")
         out, code, ldo = torch.empty((T, N), dtype=out_dtype, device=x.device), _CODE[out_dtype], N
     else:
-        out, code = _out(out, T, N, out.dtype, x.device)
+        out, code = _out(out, T, N, out_dtype, x.device)
         ldo = out.stride(0) if T > 1 else N
     L = _lib.lib()
     if workspace is not None:
