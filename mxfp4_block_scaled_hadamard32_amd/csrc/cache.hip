@@ -345,9 +345,14 @@ __global__ __launch_bounds__(D) void cache_read_kernel(const CacheArgs c, const 
 //
 // Work is divided where the lengths are known, on the device, and evenly: a sequence's rows, R = 16 WR
 // at a time, are an item, and the steps of all items, one after the other, are cut into as many equal
-// parts as there are workgroups (64 sequences of 500 to 16000 tokens, 64 heads over 8 of 128: 175 us, 6.1
-// TB/s; with a chunk of a sequence for each workgroup 25 us more). An item in one part is finished there; of the others each part goes to
-// the workspace, and a second kernel joins them.
+// parts as there are workgroups (64 sequences of 500 to 16000 tokens, 64 heads over 8 of 128: 174 us, 6.1
+// TB/s; with a chunk of a sequence for each workgroup 25 us more). An item in one part is finished
+// there; of the others each part goes to the workspace, and a second kernel joins them.
+//
+// Value codes are read as the product wants them, 4 lanes to a channel's 32 bytes. Key codes are read
+// as they lie, 64 lanes x 16 bytes, and ordered through LDS: read in the product's order neighbouring
+// lanes have different rows, and each 16 bytes are a line lookup of their own (8 sequences of 4100
+// tokens: 24.3 us, 22.3 so; 64 of 8192: 168.7 and 166.4; 256 of 100 to 2000: 118.7 and 111.9).
 // ---------------------------------------------------------------------------------------------
 constexpr int kWaves = 4;
 // Workgroups over all heads: two for each of 256 compute units, which is what their registers allow.
@@ -380,28 +385,30 @@ __device__ __forceinline__ void store_row(const AttentionArgs& a, int64_t t, int
         sum == 0.0f ? -__builtin_inff() : (base + __builtin_log2f(sum)) * 0.6931471805599453f;
 }
 
-__device__ __forceinline__ int64_t wave_sum(int64_t v) {
+__device__ __forceinline__ int wave_sum(int v) {
 #pragma unroll
   for (int i = 1; i < 64; i *= 2) v += __shfl_xor(v, i);
   return v;
 }
 
-// All steps of all items stand in one line, an item after the other, and workgroup u of a head's U
-// has the steps from all * u / U on. A workgroup's part of an item is a segment. Of a workgroup's segments
-// only the first and the last one may be part of an item: they have the workspace's slots 2 u and 2 u + 1.
+// All steps of all items stand in one line, an item after the other, and each of a head's U workgroups
+// has all / U of them, the first all % U one more. A workgroup's part of an item is a segment. Of a
+// workgroup's segments only the first and the last one may be part of an item: they have the workspace's
+// slots 2 u and 2 u + 1. (The host sees to it that there are fewer than 2^31 steps.)
 struct Line {
-  int64_t all, at, end;  // steps in all; the workgroup's
-  int units;             // U
-  int b, tile;           // the item that step `at` is in: R rows of sequence b from tile * R on
-  int64_t first;         // its first step in the line
+  int all, at, end;  // steps in all; the workgroup's
+  int units;         // U
+  int each, more;    // all / U, all % U
+  int b, tile;       // the item that step `at` is in: R rows of sequence b from tile * R on
+  int first;         // its first step in the line
 };
 
-__device__ __forceinline__ int64_t bound_of(const Line& o, int u) { return o.all * u / o.units; }
+__device__ __forceinline__ int bound_of(const Line& o, int u) { return o.each * u + min(u, o.more); }
 // the workgroup that has step x
-__device__ __forceinline__ int unit_at(const Line& o, int64_t x) {
-  int u = (int)(x * o.units / o.all);
-  while (bound_of(o, u + 1) <= x) ++u;
-  return u;
+__device__ __forceinline__ int unit_at(const Line& o, int x) {
+  const int longer = o.more * (o.each + 1);
+  return x < longer ? (int)((uint32_t)x / (uint32_t)(o.each + 1))
+                    : o.more + (int)((uint32_t)(x - longer) / (uint32_t)o.each);
 }
 
 template <int R>
@@ -412,12 +419,6 @@ __device__ __forceinline__ int items_of(const Sequence& s, int group) {
 template <int TS>
 __device__ __forceinline__ int steps_of(const CacheArgs& c, const Sequence& s) {
   return max((min(s.length, c.max_tokens) + TS - 1) / TS, 1);
-}
-
-// the value that a lane has, as a scalar
-__device__ __forceinline__ int64_t lane64(int64_t v, int from) {
-  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)v, from) |
-                   (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), from) << 32);
 }
 
 // The call's sequences. Up to 64 of them are in the lanes of every wave, and nothing is read again or
@@ -434,8 +435,10 @@ struct Sequences {
 
 // the workgroup's steps, once the line's length is known; false: none
 __device__ __forceinline__ bool bounds_of(Line& o, int unit) {
-  o.units = (int)min((int64_t)gridDim.x, o.all);
+  o.units = min((int)gridDim.x, o.all);
   if (unit >= o.units) return false;
+  o.each = (int)((uint32_t)o.all / (uint32_t)o.units);
+  o.more = o.all - o.each * o.units;
   o.at = bound_of(o, unit);
   o.end = bound_of(o, unit + 1);
   return true;
@@ -450,7 +453,7 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
   if (WAVES != kWaves && !c.offsets) {  // as many items for each sequence
     const int each = (a.group + R - 1) / R;
     seqs.few = false;
-    o.all = (int64_t)each * c.seqs;
+    o.all = each * c.seqs;
     if (!bounds_of(o, unit)) return false;
     o.b = unit / each;
     o.tile = unit - o.b * each;
@@ -461,28 +464,26 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
     const bool is = lane < c.seqs;
     seqs.own = sequence_of(c, is ? lane : 0, c.rows);
     const int n = is ? items_of<R>(seqs.own, a.group) : 0, st = weight(seqs.own);
-    int64_t end = (int64_t)n * st;
+    int end = n * st;
     for (int i = 1; i < c.seqs; i *= 2) {
-      const int64_t t = __shfl_up(end, i);
+      const int t = __shfl_up(end, i);
       if (lane >= i) end += t;
     }
-    o.all = lane64(end, c.seqs - 1);
+    o.all = __builtin_amdgcn_readlane(end, c.seqs - 1);
     if (o.all == 0 || !bounds_of(o, unit)) return false;
-    const int64_t begin = end - (int64_t)n * st;
+    const int begin = end - n * st;
     o.b = __builtin_ctzll(__ballot(is && o.at >= begin && o.at < end));
-    const int64_t first = lane64(begin, o.b);
+    const int first = __builtin_amdgcn_readlane(begin, o.b);
     const int steps = __builtin_amdgcn_readlane(st, o.b);
-    o.tile = (int)((o.at - first) / steps);
-    o.first = first + (int64_t)o.tile * steps;
+    o.tile = (int)((uint32_t)(o.at - first) / (uint32_t)steps);
+    o.first = first + o.tile * steps;
     return true;
   }
-  __shared__ int64_t sums[WAVES];
-  __shared__ int64_t got_first;
-  __shared__ int got_b;
-  int64_t all = 0;
+  __shared__ int sums[WAVES], got_first, got_b;
+  int all = 0;
   for (int b = tid; b < c.seqs; b += 64 * WAVES) {
     const Sequence s = sequence_of(c, b, c.rows);
-    all += (int64_t)items_of<R>(s, a.group) * weight(s);
+    all += items_of<R>(s, a.group) * weight(s);
   }
   all = wave_sum(all);
   if (lane == 0) sums[wave] = all;
@@ -492,7 +493,7 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
 #pragma unroll
   for (int i = 0; i < WAVES; ++i) o.all += sums[i];
   if (o.all == 0 || !bounds_of(o, unit)) return false;
-  int64_t before = 0;
+  int before = 0;
   for (int b0 = 0; b0 < c.seqs; b0 += 64 * WAVES) {  // the same turns in every wave
     const int b = b0 + tid;
     int n = 0, st = 0;
@@ -501,23 +502,23 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
       n = items_of<R>(s, a.group);
       st = weight(s);
     }
-    int64_t end = (int64_t)n * st;
+    int end = n * st;
 #pragma unroll
     for (int i = 1; i < 64; i *= 2) {
-      const int64_t t = __shfl_up(end, i);
+      const int t = __shfl_up(end, i);
       if (lane >= i) end += t;
     }
     __syncthreads();
     if (lane == 63) sums[wave] = end;
     __syncthreads();
-    int64_t total = 0;
+    int total = 0;
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) {
       if (i < wave) end += sums[i];
       total += sums[i];
     }
     end += before;
-    const int64_t begin = end - (int64_t)n * st;
+    const int begin = end - n * st;
     if (o.at >= begin && o.at < end) {
       got_b = b;
       got_first = begin;
@@ -529,8 +530,8 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
   o.b = __builtin_amdgcn_readfirstlane(got_b);
   if (o.b < 0) return false;
   const int st = weight(sequence_of(c, o.b, c.rows));
-  o.tile = (int)((o.at - got_first) / st);
-  o.first = got_first + (int64_t)o.tile * st;
+  o.tile = (int)((uint32_t)(o.at - got_first) / (uint32_t)st);
+  o.first = got_first + o.tile * st;
   return true;
 }
 
@@ -578,7 +579,7 @@ __device__ __forceinline__ T load_codes(const uint8_t* p) {
 // The codes of a step's tokens in a lane, and its block's scale (NB == 1: the lanes have one block)
 template <int D, int TS>
 struct Keys {
-  u32x4 w[TS / 16][D / 64];
+  u32x4 w[TS / 16][D / 64];  // as they lie in the cache
   uint32_t scale;
 };
 template <int D, int TS>
@@ -593,17 +594,30 @@ struct Blocks {
   bool has[NB];
 };
 
-template <int D, int WAVES>
+template <int D, int TS, int WAVES>
 struct AttentionShared {
-  float part[WAVES][16][D + 4];
+  // rows of D code bytes; 16 bytes between them and 16 more after 16 rows spread them over the banks
+  static constexpr int PITCH = D + 16, KEYS = TS * PITCH + TS;
+  union {
+    float part[WAVES][16][D + 4];
+    uint8_t keys[WAVES][KEYS];
+  };
   float stat[WAVES][16][2];
+  static __device__ __forceinline__ int at(int row) { return row * PITCH + (row >> 4) * 16; }
 };
+
+// a wave's LDS accesses complete in order; the compiler keeps them so
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // One segment: the steps of an item that the workgroup has
 template <int D, int FMT, bool BF16, int WR, int TS, int WAVES>
 __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& a,
                                        const int32_t* __restrict__ pages, const Line& line,
-                                       const Sequence& s, AttentionShared<D, WAVES>& sh) {
+                                       const Sequence& s, AttentionShared<D, TS, WAVES>& sh) {
   constexpr int R = 16 * WR, TW = WAVES / WR;  // rows a workgroup; waves that share a row's tokens
   constexpr int NQ = BF16 ? 1 : 3, NP = BF16 ? 2 : 3, KT = TS / 16, NB = TS / 32, PER = TS / 4;
   const int head = blockIdx.y, unit = blockIdx.x;
@@ -611,8 +625,8 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wr = wave % WR, wt = wave / WR;
   const int all_steps = steps_of<TS>(c, s);
   constexpr bool WHOLE = WAVES != kWaves;
-  const int from = WHOLE ? 0 : (int)(line.at - line.first);
-  const int to = WHOLE ? all_steps : (int)min(line.end - line.first, (int64_t)all_steps);
+  const int from = WHOLE ? 0 : line.at - line.first;
+  const int to = WHOLE ? all_steps : min(line.end - line.first, all_steps);
   // the item's segments are those of units first_unit .. last_unit
   const int first_unit = from == 0 ? unit : unit_at(line, line.first);
   const int last_unit = to == all_steps ? unit : unit_at(line, line.first + all_steps - 1);
@@ -678,11 +692,12 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
   auto load_keys = [&](const Blocks<NB>& b, Keys<D, TS>& o) {
     const int64_t at = NB == 1 ? b.at[0] : i >= 8 ? b.at[NB - 1] : b.at[0];
     o.scale = c.ks[at];
-    const uint8_t* p = c.kq + at * (32 * D) + (PER * ((i >> 2) & (NB == 1 ? 3 : 1)) + (i & 3)) * D + 16 * g;
+    // 64 lanes x 16 bytes in a row each: D / 32 of these loads are a block's keys
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j) o.w[t][j] = load_codes<WR == 1, u32x4>(p + 4 * t * D + 64 * j);
+    for (int n = 0; n < KT * (D / 64); ++n) {
+      const int64_t from = b.at[n / (D / 32)] * (32 * D) + (n % (D / 32)) * 1024 + lane * 16;
+      o.w[n / (D / 64)][n % (D / 64)] = load_codes<WR == 1, u32x4>(c.kq + from);
+    }
   };
   auto load_values = [&](const Blocks<NB>& b, Values<D, TS>& o) {
     const int64_t at = NB == 1 ? b.at[0] : g >= 2 ? b.at[NB - 1] : b.at[0];
@@ -716,8 +731,18 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
     constexpr bool more = decltype(follows)::value;
     int page[NB];
     if constexpr (more) look(step + 2 * TW, page);
-    f32x4 sc[KT];
+    // the keys into the order of the product, in LDS of the wave's own
+    uint8_t* keys = sh.keys[wave];
+    wave_order();
+#pragma unroll
+    for (int n = 0; n < KT * (D / 64); ++n) {
+      const int byte = n * 1024 + lane * 16;
+      *reinterpret_cast<u32x4*>(keys + sh.at(byte / D) + byte % D) = k.w[n / (D / 64)][n % (D / 64)];
+    }
+    wave_order();
     const uint32_t kscale = k.scale;
+    if constexpr (more) load_keys(next, k);
+    f32x4 sc[KT];
     const bool nan_k = kscale == 0xFFu;
     const float kf = nan_k ? 1.0f : scale_of(kscale);
 #pragma unroll
@@ -725,8 +750,10 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
       sc[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
-        const bf16x8_t k0 = codes_of<FMT>(k.w[t][j][0], k.w[t][j][1], kf);
-        const bf16x8_t k1 = codes_of<FMT>(k.w[t][j][2], k.w[t][j][3], kf);
+        const u32x4 w = *reinterpret_cast<const u32x4*>(
+            keys + sh.at(PER * (i >> 2) + 4 * t + (i & 3)) + 64 * j + 16 * g);
+        const bf16x8_t k0 = codes_of<FMT>(w[0], w[1], kf);
+        const bf16x8_t k1 = codes_of<FMT>(w[2], w[3], kf);
 #pragma unroll
         for (int n = NQ - 1; n >= 0; --n) {
           sc[t] = mfma(k0, q[n][2 * j], sc[t]);
@@ -734,7 +761,6 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
         }
       }
     }
-    if constexpr (more) load_keys(next, k);
     bool whole = (step + 1) * TS <= least;
 #pragma unroll
     for (int n = 0; n < NB; ++n) whole = whole && here.has[n];
@@ -824,6 +850,7 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
   for (; step + TW < end; step += TW) take(std::true_type());
   if (step < end) take(std::false_type());
 
+  __syncthreads();  // keys and parts share LDS
   // the waves' parts of a row, joined in the waves' order
   l = row_sum(l);
   if (l != l) m = 0.0f;  // a NaN counts, whatever the maximum of the others
@@ -852,7 +879,8 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
 #pragma unroll
       for (int x = 0; x < 4; ++x) o[x] += t[x] * f;
     }
-    const int64_t slot = ((int64_t)(2 * unit + (line.at == bound_of(line, unit) ? 0 : 1)) * c.heads + head) * R + r;
+    const int part = 2 * unit + (line.at == bound_of(line, unit) ? 0 : 1);
+    const int64_t slot = ((int64_t)part * c.heads + head) * R + r;
     if (first_unit == last_unit) {
       store_row<BF16>(a, (int64_t)s.row0 + at / a.group, head * a.group + at % a.group, ch, o, base, sum);
     } else {
@@ -873,7 +901,7 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
 template <int D, int FMT, bool BF16, int WR, int TS, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(
     const CacheArgs c, const AttentionArgs a, const int32_t* __restrict__ pages) {
-  __shared__ __attribute__((aligned(16))) AttentionShared<D, WAVES> sh;
+  __shared__ __attribute__((aligned(16))) AttentionShared<D, TS, WAVES> sh;
   Line line;
   Sequences seqs;
   if (!line_of<16 * WR, TS, WAVES>(c, a, blockIdx.x, line, seqs)) return;
@@ -1064,6 +1092,13 @@ struct Attention {
   }
 };
 
+// steps of all items, at most
+int64_t all_steps(const CacheArgs& c, const AttentionArgs& a) {
+  const AttentionPlan p = plan_attention(c, a);
+  const int ts = step_tokens(c.dim);
+  return ((int64_t)c.rows * a.group / (16 * p.wr) + c.seqs) * ((int64_t)c.max_tokens / ts + 1);
+}
+
 int64_t part_floats(const CacheArgs& c, const AttentionPlan& p) {
   return p.join ? p.slots * c.heads * 16 * p.wr : 0;
 }
@@ -1078,6 +1113,10 @@ hipError_t mx_launch_cache_write(const CacheArgs& c, const CacheRows& k, const C
 hipError_t mx_launch_cache_read(const CacheArgs& c, const CacheRows& k, const CacheRows& v,
                                 bool bf16, void* stream) {
   return pick<Read>(c, bf16, k, v, pieces(c), stream);
+}
+
+bool mx_attention_fits(const CacheArgs& c, const AttentionArgs& a) {
+  return all_steps(c, a) < ((int64_t)1 << 31);
 }
 
 // [where: 16 bytes a row][part: D floats][stat: 2 floats] for each chunk's row

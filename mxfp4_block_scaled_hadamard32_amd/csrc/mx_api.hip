@@ -547,7 +547,7 @@ int64_t mx_cache_attention_workspace(int64_t T, int64_t q_heads, const mx_cache*
   AttentionArgs a{};
   a.heads = (int)q_heads;
   a.group = (int)q_heads / c.heads;
-  return mx_attention_workspace_bytes(c, a);
+  return mx_attention_fits(c, a) ? mx_attention_workspace_bytes(c, a) : -1;
 }
 
 mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, int32_t dtype,
@@ -575,6 +575,7 @@ mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, i
   AttentionArgs a{rq.p, const_cast<void*>(ro.p), lse, rq.token, rq.head, ro.token, ro.head,
                   (int)q_heads, (int)q_heads / c.heads, scale * 1.4426950408889634f,
                   dtype == MX_BF16, stream, 0, nullptr, nullptr, nullptr};
+  if (!mx_attention_fits(c, a)) return MX_ERR_UNSUPPORTED;
   const int64_t need = mx_attention_workspace_bytes(c, a);
   if (need > 0 && !workspace) return MX_ERR_NULL;
   if (workspace_bytes < need) return MX_ERR_ARG;

@@ -181,6 +181,8 @@ struct AttentionArgs {
   float* part;
   float* stat;
 };
+// whether the kernels' 32-bit step numbers reach, if every sequence filled its table
+bool mx_attention_fits(const CacheArgs& c, const AttentionArgs& a);
 int64_t mx_attention_workspace_bytes(const CacheArgs& c, const AttentionArgs& a);
 hipError_t mx_launch_cache_attention(const CacheArgs& c, AttentionArgs a, void* workspace);
 

@@ -91,6 +91,7 @@ def test_attention_refusals(m):
     assert bad(q_heads=-2) == m.MX_ERR_SHAPE
     assert bad(heads=0) == m.MX_ERR_SHAPE
     assert bad(q_heads=65538) == m.MX_ERR_UNSUPPORTED
+    assert bad(table_width=(1 << 31) - 1, page_size=2048, T=3000, seqs=3000) == m.MX_ERR_UNSUPPORTED
     for s in (float("nan"), float("inf"), -float("inf")):
         assert bad(scale=s) == m.MX_ERR_ARG
     assert bad(workspace=None, table_width=40) == m.MX_ERR_NULL
