@@ -361,9 +361,14 @@ struct Up {
     else wide ? load_base<1, true>(a, m, 0, n, base) : load_base<1, false>(a, m, 0, n, base);
   }
 
+  // B's rows n .. n + 63, four neighbouring lanes a row's 64 bytes; then each lane's rows n + 4 i .. by
+  // an exchange of registers. Read in that order directly, neighbouring lanes have different rows and
+  // each 16 bytes are a line lookup of their own (2048 tokens of 64 adapters, N and K 4096, rank 16: 85
+  // us both kernels, 75 so; one token, N 14336: 8.5, 8.0; 2048 tokens of 4 adapters, rank 64: level).
   static __device__ __forceinline__ void load_weights(const LoraArgs& a, const Members& m, int n,
                                                       u32x4 (&w)[JT][4]) {
-    const int g = (threadIdx.x & 63) >> 4;
+    const int lane = threadIdx.x & 63, g = lane & 3;
+    n += 4 * (lane >> 2);
 #pragma unroll
     for (int k = 0; k < JT; ++k) {
       const int j = k * JS + (BF16 ? 8 : 4) * g;
@@ -375,6 +380,17 @@ struct Up {
         w[k][q] = j < a.r ? t : u32x4{0, 0, 0, 0};
       }
     }
+  }
+
+  static __device__ __forceinline__ void order_weights(u32x4 (&w)[JT][4]) {
+    const int lane = threadIdx.x & 63, from = 4 * (4 * (lane & 15) + (lane >> 4));
+#pragma unroll
+    for (int k = 0; k < JT; ++k)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[k][q][e] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)w[k][q][e]);
   }
 
   // 64 rows of B (those at n = n0 + 4 i ..), all members; base holds the first tile's
@@ -454,7 +470,7 @@ __global__ __launch_bounds__(256) void lora_up_kernel(const LoraArgs a) {
   u32x4 base[4];
   if (n0 < a.N) U::first_base(a, m, rows_wide && n0 + 64 <= a.N, n0 + 4 * i, base);
   if (m.adapter >= 0) {
-    if (n0 < a.N) U::load_weights(a, m, n0 + 4 * i, w);
+    if (n0 < a.N) U::load_weights(a, m, n0, w);
     const float scale = a.scaling ? a.scaling[m.adapter] : 1.0f;
     if (a.parts <= 4) U::template sum_parts<1, (RT >= 4 ? 8 : 4)>(a, m, scale, sh);
     else U::template sum_parts<kMostParts / 4, 2>(a, m, scale, sh);
@@ -465,8 +481,9 @@ __global__ __launch_bounds__(256) void lora_up_kernel(const LoraArgs a) {
     const bool wide = rows_wide && n0 + 64 <= a.N;
     if (slab > 0) {
       U::first_base(a, m, wide, n, base);
-      if (m.adapter >= 0) U::load_weights(a, m, n, w);
+      if (m.adapter >= 0) U::load_weights(a, m, n0, w);
     }
+    if (m.adapter >= 0) U::order_weights(w);
     if (wide) U::template any_slab<true>(a, m, sh, n, w, base);
     else U::template any_slab<false>(a, m, sh, n, w, base);
   }
@@ -492,7 +509,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void lora_small_kernel(const Lora
   u32x4 base[4], w[U::JT][4];
   if (n0 < a.N) U::first_base(a, m, wide, n, base);
   if (m.adapter >= 0) {
-    if (n0 < a.N) U::load_weights(a, m, n, w);
+    if (n0 < a.N) U::load_weights(a, m, n0, w);
     const float scale = a.scaling ? a.scaling[m.adapter] : 1.0f;
     f32x4 acc[RT];
     accumulate<BF16, RT>(a, m, 0, 0, (a.K + 63) / 64, wave, kSmallWaves, part.area[wave], acc);
@@ -511,6 +528,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void lora_small_kernel(const Lora
     __syncthreads();
   }
   if (n0 >= a.N) return;
+  if (m.adapter >= 0) U::order_weights(w);
   if (wide) U::template any_slab<true>(a, m, sh, n, w, base);
   else U::template any_slab<false>(a, m, sh, n, w, base);
 }
