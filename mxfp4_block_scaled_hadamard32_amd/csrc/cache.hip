@@ -597,6 +597,7 @@ struct Blocks {
 template <int D, int TS, int WAVES>
 struct AttentionShared {
   // rows of D code bytes; 16 bytes between them and 16 more after 16 rows spread them over the banks
+  // (without the latter 25.9 us for 24.6, 20 sequences of 500 to 2000 tokens, fp32, 4 heads of 192)
   static constexpr int PITCH = D + 16, KEYS = TS * PITCH + TS;
   union {
     float part[WAVES][16][D + 4];
