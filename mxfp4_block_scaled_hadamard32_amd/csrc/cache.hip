@@ -359,10 +359,23 @@ constexpr int kWaves = 4;
 // More of them, or three at a time with fewer registers, read less at once of each page and are slower
 // (64 sequences of 8192 tokens: 170 us with 512, 181 with 768 and 180 with 1024).
 constexpr int kTarget = 512;
-// Short tables: a workgroup of 8 waves for each item and head, no segments and no second kernel, while a
-// wave has a step or two and the workgroups are not many (8 heads of 128, one sequence of 512 tokens: 7.3
-// us, 9.4 divided; 16 of 256: 6.9 and 11.1; one of 1024: 11.4 and 9.9; 256 sequences of 64: 33 and 25).
-constexpr int kWholeWaves = 8, kWholeTokens = 768, kWholeItems = 1024;
+// Long work of single items keeps HBM busier with one workgroup a unit, whose stream is longer, if each
+// has kLongSteps steps and more, and its sequences have kLongItem, so that few begin and end (64
+// sequences of 500 to 16000 tokens, 64 heads over 8 of 128: 176 us with two, 171 with one; 16 of 16000:
+// 86.9 and 84.5; but 256 of 2000: 170 and 180, 4 of 16000: 29.0 and 30.3).
+constexpr int kLongSteps = 48, kLongItem = 100;
+// Short work: where a wave has up to kShort steps, a workgroup's part is of one item alone, since a
+// second segment would cost it the first one's latency again (4 sequences of 4000 tokens, 8 heads of 128:
+// 16.8 us cut evenly, 12.9 so; of 200 to 4000: 16.3 and 12.4; one of 8000: 12.3 and 10.6; up to 2 steps
+// instead of 4: 4 of 8000 21.5 us for 18.4).
+constexpr int kShort = 4;
+// Short tables: a workgroup of 8 waves for each item and head, no segments, no second kernel and no
+// workspace (8 heads of 128, 16 sequences of 1020 tokens: 13.3 us divided, 11.7; 16 of 50 to 1020: 12.1 and
+// 11.0; one of 512: 9.4 and 7.3; one of 1020: 9.5 and 10.5, but 4 us less on the host), as long as the
+// workgroups are not very many (256 sequences of 64: 33 and 25); where they are many enough to fill the
+// chip, for longer ones too (16 of 1270: 15.1 and 12.8; 4 of 1270: 10.0 and 11.8).
+constexpr int kWholeWaves = 8, kWholeItems = 1024;
+constexpr int kWholeTokens = 1088, kWholeMost = 1536, kWholeMany = 128;
 
 // 4 channels of an output row: o / sum rounded to the output's type, and once a row its log sum of
 // exponentials; a row that sees no token is zeros, -inf
@@ -397,8 +410,11 @@ __device__ __forceinline__ int wave_sum(int v) {
 // slots 2 u and 2 u + 1. (The host sees to it that there are fewer than 2^31 steps.)
 struct Line {
   int all, at, end;  // steps in all; the workgroup's
+  int unit, head;    // the workgroup's
   int units;         // U
   int each, more;    // all / U, all % U
+  int part;          // short work: steps of a workgroup, all of one item; else 0
+  bool leads;        // `at` is in the workgroup's first segment
   int b, tile;       // the item that step `at` is in: R rows of sequence b from tile * R on
   int first;         // its first step in the line
 };
@@ -434,27 +450,43 @@ struct Sequences {
 };
 
 // the workgroup's steps, once the line's length is known; false: none
-__device__ __forceinline__ bool bounds_of(Line& o, int unit) {
-  o.units = min((int)gridDim.x, o.all);
-  if (unit >= o.units) return false;
+template <bool SINGLE>
+__device__ __forceinline__ bool bounds_of(const CacheArgs& c, Line& o, int most) {
+  o.units = min(most, o.all);
+  if (SINGLE) {
+    if (o.all / kLongSteps >= o.units && o.all / kLongItem >= c.seqs) {
+      o.units = (o.units + 1) / 2;
+    } else {  // a head's workgroups in a row
+      const int n = o.unit * c.heads + o.head;
+      o.head = (int)((uint32_t)n / (uint32_t)most);
+      o.unit = n - o.head * most;
+    }
+  }
+  if (o.unit >= o.units) return false;
   o.each = (int)((uint32_t)o.all / (uint32_t)o.units);
   o.more = o.all - o.each * o.units;
-  o.at = bound_of(o, unit);
-  o.end = bound_of(o, unit + 1);
+  o.at = bound_of(o, o.unit);
+  o.end = bound_of(o, o.unit + 1);
+  o.leads = true;
   return true;
 }
 
 template <int R, int TS, int WAVES>
-__device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs& a, int unit, Line& o,
+__device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs& a, Line& o,
                                         Sequences& seqs) {
+  constexpr bool DIVIDED = WAVES == kWaves;
+  const int unit = blockIdx.y, most = gridDim.y;
+  o.unit = unit;
+  o.head = blockIdx.x;
+  o.part = 0;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  auto weight = [&](const Sequence& s) { return WAVES == kWaves ? steps_of<TS>(c, s) : 1; };
+  auto weight = [&](const Sequence& s) { return DIVIDED ? steps_of<TS>(c, s) : 1; };
   seqs.few = c.seqs <= 64;
-  if (WAVES != kWaves && !c.offsets) {  // as many items for each sequence
+  if (!DIVIDED && !c.offsets) {  // as many items for each sequence
     const int each = (a.group + R - 1) / R;
     seqs.few = false;
     o.all = each * c.seqs;
-    if (!bounds_of(o, unit)) return false;
+    if (!bounds_of<false>(c, o, most)) return false;
     o.b = unit / each;
     o.tile = unit - o.b * each;
     o.first = unit;
@@ -464,13 +496,36 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
     const bool is = lane < c.seqs;
     seqs.own = sequence_of(c, is ? lane : 0, c.rows);
     const int n = is ? items_of<R>(seqs.own, a.group) : 0, st = weight(seqs.own);
-    int end = n * st;
-    for (int i = 1; i < c.seqs; i *= 2) {
-      const int t = __shfl_up(end, i);
-      if (lane >= i) end += t;
+    auto up_to = [&](int v) {  // the sum of the lanes up to this one
+      for (int i = 1; i < c.seqs; i *= 2) {
+        const int t = __shfl_up(v, i);
+        if (lane >= i) v += t;
+      }
+      return v;
+    };
+    for (int k = 1; DIVIDED && k <= kShort;) {
+      const int part = k * (WAVES / (R / 16)), parts = (st + part - 1) / part, behind = up_to(n * parts);
+      const int total = __builtin_amdgcn_readlane(behind, c.seqs - 1);
+      if (total > most) {
+        k = total / most >= kShort ? kShort + 1 : max(k + 1, k * total / most);
+        continue;
+      }
+      const uint64_t has = __ballot(is && unit >= behind - n * parts && unit < behind);
+      if (has == 0) return false;
+      o.b = __builtin_ctzll(has);
+      o.part = part;
+      const int each = __builtin_amdgcn_readlane(parts, o.b);
+      const int at = unit - __builtin_amdgcn_readlane(behind - n * parts, o.b);
+      o.tile = (int)((uint32_t)at / (uint32_t)each);
+      o.first = 0;
+      o.at = (at - o.tile * each) * part;
+      o.end = min(o.at + part, __builtin_amdgcn_readlane(st, o.b));
+      o.leads = true;
+      return true;
     }
+    const int end = up_to(n * st);
     o.all = __builtin_amdgcn_readlane(end, c.seqs - 1);
-    if (o.all == 0 || !bounds_of(o, unit)) return false;
+    if (o.all == 0 || !bounds_of<DIVIDED && R == 16>(c, o, most)) return false;
     const int begin = end - n * st;
     o.b = __builtin_ctzll(__ballot(is && o.at >= begin && o.at < end));
     const int first = __builtin_amdgcn_readlane(begin, o.b);
@@ -492,7 +547,7 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
   o.all = 0;
 #pragma unroll
   for (int i = 0; i < WAVES; ++i) o.all += sums[i];
-  if (o.all == 0 || !bounds_of(o, unit)) return false;
+  if (o.all == 0 || !bounds_of<DIVIDED && R == 16>(c, o, most)) return false;
   int before = 0;
   for (int b0 = 0; b0 < c.seqs; b0 += 64 * WAVES) {  // the same turns in every wave
     const int b = b0 + tid;
@@ -621,7 +676,7 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
                                        const Sequence& s, AttentionShared<D, TS, WAVES>& sh) {
   constexpr int R = 16 * WR, TW = WAVES / WR;  // rows a workgroup; waves that share a row's tokens
   constexpr int NQ = BF16 ? 1 : 3, NP = BF16 ? 2 : 3, KT = TS / 16, NB = TS / 32, PER = TS / 4;
-  const int head = blockIdx.y, unit = blockIdx.x;
+  const int head = line.head, unit = line.unit;
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wr = wave % WR, wt = wave / WR;
   const int all_steps = steps_of<TS>(c, s);
@@ -629,8 +684,11 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
   const int from = WHOLE ? 0 : line.at - line.first;
   const int to = WHOLE ? all_steps : min(line.end - line.first, all_steps);
   // the item's segments are those of units first_unit .. last_unit
-  const int first_unit = from == 0 ? unit : unit_at(line, line.first);
-  const int last_unit = to == all_steps ? unit : unit_at(line, line.first + all_steps - 1);
+  const bool shorts = !WHOLE && line.part > 0;
+  const int first_unit = from == 0 ? unit : shorts ? unit - from / line.part : unit_at(line, line.first);
+  const int last_unit = to == all_steps ? unit
+                        : shorts        ? first_unit + (all_steps - 1) / line.part
+                                        : unit_at(line, line.first + all_steps - 1);
   const int row0 = line.tile * R;
   const int rows = s.n * a.group;      // of this sequence and head
   const int row = row0 + 16 * wr + i;  // this lane's
@@ -880,7 +938,7 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
 #pragma unroll
       for (int x = 0; x < 4; ++x) o[x] += t[x] * f;
     }
-    const int part = 2 * unit + (line.at == bound_of(line, unit) ? 0 : 1);
+    const int part = 2 * unit + (line.leads ? 0 : 1);
     const int64_t slot = ((int64_t)part * c.heads + head) * R + r;
     if (first_unit == last_unit) {
       store_row<BF16>(a, (int64_t)s.row0 + at / a.group, head * a.group + at % a.group, ch, o, base, sum);
@@ -894,7 +952,7 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
   }
   if (!WHOLE && a.where && from == 0 && head == 0 && tid < R && row0 + tid < rows) {
     const int at = row0 + tid;
-    const int first = 2 * unit + (line.at == bound_of(line, unit) ? 0 : 1);
+    const int first = 2 * unit + (line.leads ? 0 : 1);
     a.where[(int64_t)s.row0 * a.group + at] = make_int4(first, last_unit - first_unit + 1, tid, 0);
   }
 }
@@ -905,7 +963,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(
   __shared__ __attribute__((aligned(16))) AttentionShared<D, TS, WAVES> sh;
   Line line;
   Sequences seqs;
-  if (!line_of<16 * WR, TS, WAVES>(c, a, blockIdx.x, line, seqs)) return;
+  if (!line_of<16 * WR, TS, WAVES>(c, a, line, seqs)) return;
   for (;;) {
     const Sequence s = seqs.get(c, line.b);
     attend<D, FMT, BF16, WR, TS, WAVES>(c, a, pages, line, s, sh);
@@ -913,6 +971,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(
     line.at = line.first + steps_of<TS>(c, s);
     if (line.at >= line.end) return;
     line.first = line.at;
+    line.leads = false;
     if (++line.tile * 16 * WR >= s.n * a.group) {
       line.tile = 0;
       do {
@@ -1058,7 +1117,9 @@ AttentionPlan plan_attention(const CacheArgs& c, const AttentionArgs& a) {
   p.wr = each <= 16 ? 1 : each <= 32 ? 2 : 4;
   const int64_t items = rows / (16 * p.wr) + c.seqs;
   const int64_t most = (c.max_tokens + step_tokens(c.dim) - 1) / step_tokens(c.dim), steps = most > 0 ? most : 1;
-  p.whole = p.wr == 1 && c.max_tokens <= kWholeTokens && items * c.heads <= kWholeItems;
+  const int64_t workgroups = items * c.heads;
+  p.whole = p.wr == 1 && workgroups <= kWholeItems &&
+            c.max_tokens <= (workgroups < kWholeMany ? kWholeTokens : kWholeMost);
   p.join = !p.whole && steps > 1;
   p.units = (kTarget + c.heads - 1) / c.heads;
   if (p.whole) p.units = items;
@@ -1072,7 +1133,7 @@ struct Attention {
   template <int WR, int WAVES>
   static void main(const CacheArgs& c, const AttentionArgs& a, const AttentionPlan& p) {
     hipLaunchKernelGGL((cache_attention_kernel<D, FMT, BF16, WR, step_tokens(D), WAVES>),
-                       dim3((unsigned)p.units, (unsigned)c.heads), dim3(64 * WAVES), 0,
+                       dim3((unsigned)c.heads, (unsigned)p.units), dim3(64 * WAVES), 0,
                        (hipStream_t)a.stream, c, a, c.pages);
   }
   static hipError_t run(const CacheArgs& c, const AttentionArgs& a, const AttentionPlan& p) {

@@ -217,6 +217,62 @@ def test_attention_long(mx, dtype):
     check_attention(mx, cache, table, lengths, [4, 2, 1], 8, dtype, seed=21)
 
 
+@pytest.mark.parametrize("dtype,fmt", [("bf16", 0), ("f32", 1)])
+@pytest.mark.parametrize("dim,page,wide", [(64, 32, 80), (128, 64, 30), (192, 96, 20), (256, 160, 12)])
+@pytest.mark.parametrize("lengths,new,heads,group", [
+    ([1, 700, 33, 0, 65, 1800], [1] * 6, 2, 4),
+    ([700, 90, 1500], [9, 1, 20], 2, 3),
+    ([400, 0, 1100], [40, 0, 3], 1, 8),
+])
+def test_attention_divided(mx, lengths, new, heads, group, dim, page, wide, fmt, dtype):
+    """Tables that are too wide for a workgroup each."""
+    cache, table = filled(lengths, heads, page, dim, fmt, width=wide, seed=41)
+    check_attention(mx, cache, table, lengths, new, group, dtype)
+
+
+@pytest.mark.parametrize("lengths,pages", [
+    ([700, 30, 1500, 900], 40),      # 64 heads leave 8 workgroups each: a part is 2 steps a wave,
+    ([2500, 1500, 900, 30], 40),     # 4 steps,
+    ([6000, 30, 2500, 1500], 100),   # and cut evenly, with parts of several items
+    ([1500, 700], 24),               # many heads, 1536 tokens: a workgroup each
+])
+@pytest.mark.parametrize("new", [1, 2])
+def test_attention_many_heads(mx, lengths, pages, new):
+    heads, page = 64, 64
+    table, n_pages = ref.table_of([min(n, 1024) for n in lengths], page, seed=42, width=pages)
+    cache = ref.Cache(n_pages, heads, page, 64, 0, seed=42)
+    for b, n in enumerate(lengths):
+        cache.random_sequence(table[b], min(n, 1024), 42 + b, 0.4)
+        for i in range(16, -(-n // page)):  # the same pages again
+            table[b, i] = table[b, i % 16]
+    check_attention(mx, cache, table, lengths, [new] * len(lengths), 1, "bf16")
+
+
+@pytest.mark.parametrize("lengths", [[13000], [13000, 9001], [0, 12800, 13000, 12500]])
+@pytest.mark.parametrize("dim,dtype", [(64, "bf16"), (128, "f32")])
+def test_attention_long_many_heads(mx, lengths, dim, dtype):
+    """Long sequences, which half of the workgroups have: 128 heads leave 4 each."""
+    heads, page = 128, 64
+    table, n_pages = ref.table_of([min(n, 512) for n in lengths], page, seed=43, width=210)
+    cache = ref.Cache(n_pages, heads, page, dim, 0, seed=43)
+    for b, n in enumerate(lengths):
+        cache.random_sequence(table[b], min(n, 512), 43 + b, 0.4)
+        for i in range(8, -(-n // page)):
+            table[b, i] = table[b, i % 8]
+    check_attention(mx, cache, table, lengths, [1] * len(lengths), 1, dtype)
+
+
+def test_attention_many_wide_sequences(mx):
+    """More sequences than a wave has lanes or a workgroup has threads, divided."""
+    for count, heads in ((70, 2), (600, 1), (65, 40)):
+        lengths = [(37 * b) % 331 for b in range(count)]
+        new = [min(n, b % 3) for b, n in enumerate(lengths)]
+        cache, table = filled(lengths, heads, 32, 64, 0, seed=61, width=60)
+        check_attention(mx, cache, table, lengths, new, 2, "bf16")
+        one = [1] * count
+        check_attention(mx, cache, table, lengths, one, 2, "bf16", seed=22)
+
+
 @pytest.mark.parametrize("size,scale", [(60.0, None), (1.0, 5.0), (1.0, 0.0), (1.0, -0.3)])
 def test_attention_scores(mx, size, scale):
     """One token that takes all, the mean, and a negative scale."""
