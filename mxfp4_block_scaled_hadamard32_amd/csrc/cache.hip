@@ -345,9 +345,10 @@ __global__ __launch_bounds__(D) void cache_read_kernel(const CacheArgs c, const 
 //
 // Work is divided where the lengths are known, on the device, and evenly: a sequence's rows, R = 16 WR
 // at a time, are an item, and the steps of all items, one after the other, are cut into as many equal
-// parts as there are workgroups (64 sequences of 500 to 16000 tokens, 64 heads over 8 of 128: 174 us, 6.1
-// TB/s; with a chunk of a sequence for each workgroup 25 us more). An item in one part is finished
-// there; of the others each part goes to the workspace, and a second kernel joins them.
+// parts as there are workgroups (64 sequences of 500 to 16000 tokens, 64 heads over 8 of 128: 171 us, 6.2
+// TB/s; with a chunk of a sequence for each workgroup, whatever its length, 25 us more). Short and long
+// work and short tables differ, see the constants below. An item in one part is finished there; of the
+// others each part goes to the workspace, and a second kernel joins them.
 //
 // Value codes are read as the product wants them, 4 lanes to a channel's 32 bytes. Key codes are read
 // as they lie, 64 lanes x 16 bytes, and ordered through LDS: read in the product's order neighbouring
@@ -357,7 +358,7 @@ __global__ __launch_bounds__(D) void cache_read_kernel(const CacheArgs c, const 
 constexpr int kWaves = 4;
 // Workgroups over all heads: two for each of 256 compute units, which is what their registers allow.
 // More of them, or three at a time with fewer registers, read less at once of each page and are slower
-// (64 sequences of 8192 tokens: 170 us with 512, 181 with 768 and 180 with 1024).
+// (64 sequences of 8192 tokens: 167 us with 512, 181 with 768 and 175 with 1024).
 constexpr int kTarget = 512;
 // Long work of single items keeps HBM busier with one workgroup a unit, whose stream is longer, if each
 // has kLongSteps steps and more, and its sequences have kLongItem, so that few begin and end (64
@@ -449,7 +450,10 @@ struct Sequences {
   }
 };
 
-// the workgroup's steps, once the line's length is known; false: none
+// The workgroup's steps, once the line's length is known; false: none. Consecutive workgroups have
+// different heads: items of the same sequence and head, which read the same codes, then meet on one XCD
+// (4 sequences of 8192 tokens, 16 rows of 64 heads over 8: 56.7 us, 59.5 with a head's in a row). Where
+// each sequence and head has one item (SINGLE) its workgroups in a row are 2% faster.
 template <bool SINGLE>
 __device__ __forceinline__ bool bounds_of(const CacheArgs& c, Line& o, int most) {
   o.units = min(most, o.all);
@@ -744,7 +748,8 @@ __device__ __forceinline__ void attend(const CacheArgs& c, const AttentionArgs& 
     for (int n = 0; n < NB; ++n) {
       const int bn = NB * step + n, slot = slot_of(c, bn);
       o.has[n] = step < end && 32 * bn < most && page[n] >= 0 && page[n] < c.n_pages;
-      o.at[n] = o.has[n] ? ((int64_t)page[n] * c.heads + head) * c.page_blocks + (bn - slot * c.page_blocks) : 0;
+      const int64_t at = ((int64_t)page[n] * c.heads + head) * c.page_blocks + (bn - slot * c.page_blocks);
+      o.at[n] = o.has[n] ? at : 0;
     }
     return o;
   };
@@ -1116,7 +1121,8 @@ AttentionPlan plan_attention(const CacheArgs& c, const AttentionArgs& a) {
   const int64_t each = c.offsets ? (rows + c.seqs - 1) / c.seqs : a.group;
   p.wr = each <= 16 ? 1 : each <= 32 ? 2 : 4;
   const int64_t items = rows / (16 * p.wr) + c.seqs;
-  const int64_t most = (c.max_tokens + step_tokens(c.dim) - 1) / step_tokens(c.dim), steps = most > 0 ? most : 1;
+  const int64_t most = (c.max_tokens + step_tokens(c.dim) - 1) / step_tokens(c.dim);
+  const int64_t steps = most > 0 ? most : 1;
   const int64_t workgroups = items * c.heads;
   p.whole = p.wr == 1 && workgroups <= kWholeItems &&
             c.max_tokens <= (workgroups < kWholeMany ? kWholeTokens : kWholeMost);

@@ -273,10 +273,11 @@ __device__ __forceinline__ void store4(void* p, int64_t at, int n, const f32x4& 
   }
 }
 
-// out = base + s B h. Grid: slabs of B's rows, chunks of tokens, adapters of a chunk and its tokens without one. A wave has 64 rows at a time: tile q's column i is row 4 i + q of them, so that a lane has
-// four neighbours of an output row and 16 lanes 64 of them, and the tokens are the products' rows. h goes in
-// as three bf16 terms that add up to the fp32 value (fp32 weights: as it is). base and B are on their way
-// while h is summed. 2048 tokens, N 14336, rank 64: 43 us, 4.1 TB/s (56 from cold memory).
+// out = base + s B h. Grid: slabs of B's rows, chunks of tokens, adapters of a chunk and its tokens
+// without one. A wave has 64 rows at a time: tile q's column i is row 4 i + q of them, so that a lane has
+// four neighbours of an output row and 16 lanes 64 of them, and the tokens are the products' rows. h goes
+// in as three bf16 terms that add up to the fp32 value (fp32 weights: as it is). base and B are on their
+// way while h is summed. 2048 tokens, N 14336, rank 64: 43 us, 4.1 TB/s (56 from cold memory).
 template <bool BF16, int RT>
 struct Up {
   static constexpr int JS = BF16 ? 32 : 16;                         // of the rank in a product
