@@ -531,7 +531,9 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
     o.all = __builtin_amdgcn_readlane(end, c.seqs - 1);
     if (o.all == 0 || !bounds_of<DIVIDED && R == 16>(c, o, most)) return false;
     const int begin = end - n * st;
-    o.b = __builtin_ctzll(__ballot(is && o.at >= begin && o.at < end));
+    const uint64_t has = __ballot(is && o.at >= begin && o.at < end);
+    if (has == 0) return false;  // offsets that fall may give more than 2^31 steps
+    o.b = __builtin_ctzll(has);
     const int first = __builtin_amdgcn_readlane(begin, o.b);
     const int steps = __builtin_amdgcn_readlane(st, o.b);
     o.tile = (int)((uint32_t)(o.at - first) / (uint32_t)steps);

@@ -122,8 +122,8 @@ def test_workspace_sizes(m):
         assert size(3, 4, **bad) == -1
     assert size(3, 5) == -1 and size(3, -2) == -1 and size(2, 4) == -1
     # a short table: nothing is divided; a long one: every row's place, each segment's sums and statistics
-    assert size(3, 4) == 0 and size(3, 4, table_width=12) == 0
-    assert size(3, 4, table_width=13) >= 3 * 2 * 16 + 4 * (64 + 2)
+    assert size(3, 4) == 0 and size(3, 4, table_width=17) == 0
+    assert size(3, 4, table_width=18) >= 3 * 2 * 16 + 4 * (64 + 2)
     assert size(600, 2, seqs=600) > 0  # many workgroups
     assert m.lib().mx_cache_attention_workspace(3, 4, None) == -1
 
