@@ -540,7 +540,9 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
     o.first = first + o.tile * steps;
     return true;
   }
-  __shared__ int sums[WAVES], got_first, got_b;
+  __shared__ int sums[WAVES];
+  __shared__ unsigned long long got;  // the sequence and its first step
+  constexpr unsigned long long none = ~0ull;
   int all = 0;
   for (int b = tid; b < c.seqs; b += 64 * WAVES) {
     const Sequence s = sequence_of(c, b, c.rows);
@@ -548,7 +550,7 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
   }
   all = wave_sum(all);
   if (lane == 0) sums[wave] = all;
-  if (tid == 0) got_b = -1;
+  if (tid == 0) got = none;
   __syncthreads();
   o.all = 0;
 #pragma unroll
@@ -580,19 +582,19 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
     }
     end += before;
     const int begin = end - n * st;
-    if (o.at >= begin && o.at < end) {
-      got_b = b;
-      got_first = begin;
-    }
+    // Offsets that fall may give so many steps that the sums wrap and several sequences have this one:
+    // the first of them, with its own start (its steps are fewer than 2^31, so the tile is one of it).
+    if (o.at >= begin && o.at < end) atomicMin(&got, (unsigned long long)b << 32 | (uint32_t)begin);
     before += total;
     __syncthreads();
-    if (got_b >= 0) break;
+    if (got != none) break;
   }
-  o.b = __builtin_amdgcn_readfirstlane(got_b);
-  if (o.b < 0) return false;
+  if (got == none) return false;
+  o.b = __builtin_amdgcn_readfirstlane((int)(got >> 32));
+  const int first = __builtin_amdgcn_readfirstlane((int)(uint32_t)got);
   const int st = weight(sequence_of(c, o.b, c.rows));
-  o.tile = (int)((uint32_t)(o.at - got_first) / (uint32_t)st);
-  o.first = got_first + o.tile * st;
+  o.tile = (int)((uint32_t)(o.at - first) / (uint32_t)st);
+  o.first = first + o.tile * st;
   return true;
 }
 
