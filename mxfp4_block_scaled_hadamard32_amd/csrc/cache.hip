@@ -1001,7 +1001,7 @@ __global__ __launch_bounds__(256) void cache_attention_join_kernel(const CacheAr
   __shared__ __attribute__((aligned(16))) float sums[ROWS][GROUPS][D];
   __shared__ float tops[ROWS][GROUPS], all[ROWS][GROUPS];
   const int which = threadIdx.x / THREADS, tid = threadIdx.x % THREADS;
-  const int64_t row = (int64_t)blockIdx.x * ROWS + which;
+  const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * ROWS + which;
   const int t = (int)(row / a.heads), qhead = (int)(row - (int64_t)t * a.heads), head = qhead / a.group;
   bool is = t < c.rows;
   if (is && c.offsets) is = t >= c.offsets[0] && t < c.offsets[c.seqs];
@@ -1154,12 +1154,17 @@ struct Attention {
     if (hipError_t e = hipGetLastError(); e != hipSuccess || !p.join) return e;
     const int64_t rows = (int64_t)c.rows * a.heads;
     // 4096 rows: 4.8 us with a wave each, 6.0 with a workgroup; 32 rows of 32 parts: 5.6 and 4.3
-    if (rows < 2048)
+    if (rows < 2048) {
       hipLaunchKernelGGL((cache_attention_join_kernel<D, BF16, 256>), dim3((unsigned)rows), dim3(256), 0,
                          (hipStream_t)a.stream, c, a, 16 * p.wr);
-    else
-      hipLaunchKernelGGL((cache_attention_join_kernel<D, BF16, 64>), dim3((unsigned)((rows + 3) / 4)),
-                         dim3(256), 0, (hipStream_t)a.stream, c, a, 16 * p.wr);
+    } else {
+      // up to 2^28 workgroups: a dimension of a grid holds fewer than 2^32 threads
+      const int64_t workgroups = (rows + 3) / 4, most = (int64_t)1 << 22;
+      const int64_t x = workgroups < most ? workgroups : most;
+      hipLaunchKernelGGL((cache_attention_join_kernel<D, BF16, 64>),
+                         dim3((unsigned)x, (unsigned)((workgroups + x - 1) / x)), dim3(256), 0,
+                         (hipStream_t)a.stream, c, a, 16 * p.wr);
+    }
     return hipGetLastError();
   }
 };

@@ -479,3 +479,31 @@ def test_far_pages(mx):
     dev = [t.to(DEV) for t in cache.tensors()]
     assert torch.equal(mx.mx_cache_attention(q, *args),
                        mx.mx_cache_attention(q, *dev, near.to(DEV), i32(lengths)))
+
+
+def test_attention_most_joined_rows(mx):
+    """More rows than one dimension of the join's grid has threads for: 2^26 and a few, of one sequence
+    whose table holds few tokens. Each of a head's 64 workgroups has many items and parts of two."""
+    heads, group, dim, page, T = 8, 8, 64, 32, (1 << 20) + 3
+    lengths = [1 << 20, 190]
+    cache, table = filled([1920, 190], heads, page, dim, 0, seed=140)
+    dev = [t.to(DEV) for t in cache.tensors()]
+    few = T - (1 << 20)
+    g = torch.Generator().manual_seed(141)
+    one = torch.randn((1, heads * group, dim), generator=g).bfloat16()
+    q = one.to(DEV).expand(T, -1, -1).contiguous()
+    # the table has the first 1920 tokens of the first sequence: the rows from there on see the same
+    got, lse = mx.mx_cache_attention(q, *dev, table.to(DEV), i32(lengths), offsets=i32([0, 1 << 20, T]),
+                                     with_lse=True)
+    seen = page * 60
+    want, want_lse, tol = ref.attention(cache, one, table[0], seen, dim ** -0.5, P_EPS["bf16"])
+    half = torch.finfo(torch.bfloat16).eps / 2
+    limit = (tol + half * (want.abs() + tol))[0].to(DEV)
+    lo, hi = want[0].to(DEV) - limit, want[0].to(DEV) + limit
+    for first in range(seen - 1, 1 << 20, 1 << 16):
+        part = got[first:min(first + (1 << 16), 1 << 20)].double()
+        assert ((part >= lo) & (part <= hi)).all(), first
+    assert ((lse[seen - 1:1 << 20].double() - want_lse[0].to(DEV)).abs() <= 1e-4 + 2.0 ** -20 * 8).all()
+    want, _, tol = ref.attention(cache, one.expand(few, -1, -1), table[1], 190, dim ** -0.5, P_EPS["bf16"])
+    err = (got[1 << 20:].cpu().double() - want).abs()
+    assert (err <= tol + half * (want.abs() + tol)).all()
