@@ -441,9 +441,9 @@ mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, i
  * workspace: mx_lora_workspace(...) bytes (0 for a few tokens), 16-byte aligned, scratch: calls that
  * may run at the same time need one each.
  * Errors (nothing is launched): MX_ERR_SHAPE, MX_ERR_ARG (types, alignment, a workspace that is too
- * small, an out that overlaps x or, without being it, base), MX_ERR_NULL, MX_ERR_UNSUPPORTED (rank
- * above 128, T above 2^21, N, K or adapters above 2^26). T == 0 or N == 0 is a no-op; no adapters, or
- * K == 0 or rank == 0, leave base alone. */
+ * small, an out that overlaps x, a, b, index, scaling or, without being it, base), MX_ERR_NULL,
+ * MX_ERR_UNSUPPORTED (rank above 128, T above 2^21, N, K or adapters above 2^26). T == 0 or N == 0 is
+ * a no-op; no adapters, or K == 0 or rank == 0, leave base alone. */
 int64_t mx_lora_workspace(int32_t dtype, int64_t T, int64_t N, int64_t K, int64_t adapters,
                           int64_t rank);
 mx_status mx_lora(const void* x, int32_t dtype, int64_t ldx, const void* a, const void* b,

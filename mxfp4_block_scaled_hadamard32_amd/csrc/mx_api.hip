@@ -97,6 +97,15 @@ bool meet(const Rows& a, const Rows& b, int64_t rows) {
   return false;
 }
 
+// whether `rows` rows have a byte in common with `size` bytes at p
+bool meet_block(const Rows& a, const void* p, int64_t size, int64_t rows) {
+  if (!a.p || !p || rows <= 0 || a.width <= 0 || size <= 0) return false;
+  typedef __int128 wide;
+  const wide d = (wide)reinterpret_cast<uintptr_t>(p) - (wide)reinterpret_cast<uintptr_t>(a.p);
+  const wide i = d < a.width ? 0 : (d - a.width) / a.pitch + 1;  // the first row that ends behind p
+  return i < rows && i * a.pitch < d + size;
+}
+
 // an output may be an input itself, or share nothing with it
 bool clash(const Rows& out, const Rows& in, int64_t rows) {
   const bool same = out.p == in.p && (out.pitch == in.pitch || rows == 1);
@@ -618,6 +627,10 @@ mx_status mx_lora(const void* x, int32_t dtype, int64_t ldx, const void* a, cons
   const Rows rx{x, ldx * esize, K * esize}, ro{out, ldo * osize, N * osize}, rb{base, ldb * bsize, N * bsize};
   const bool in_place = base == out && base_dtype == out_dtype && (ldb == ldo || T == 1);
   if (meet(rx, ro, T) || (!in_place && meet(rb, ro, T))) return MX_ERR_ARG;
+  if (any && (meet_block(ro, a, adapters * rank * K * esize, T) ||
+              meet_block(ro, b, adapters * rank * N * esize, T) || meet_block(ro, index, T * 4, T) ||
+              meet_block(ro, scaling, adapters * 4, T)))
+    return MX_ERR_ARG;
   const int64_t need = any ? mx_lora_workspace(dtype, T, N, K, adapters, rank) : 0;
   if (need > 0 && !workspace) return MX_ERR_NULL;
   if (need > 0 && (workspace_bytes < need || !aligned(workspace, 16))) return MX_ERR_ARG;

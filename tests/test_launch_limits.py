@@ -102,7 +102,7 @@ CALLS = [  # and how many launches
     ("write", [16 * M], {"seqs": M, "dim": 256, "heads": 65535}, 1),
     ("read", [16 * M], {"seqs": M, "dim": 256, "heads": 65535}, 1),
     ("write", [M], {"offsets": False, "seqs": M, "dim": 256}, 1),
-    ("lora", [2 * M, 64 * M, 4096, 64 * M, 128, 0], {}, 2), ("lora", [2 * M, 64 * M, 64 * M, 64, 128, 1], {}, 2),
+    ("lora", [2 * M, 64 * M, 4096, 1024, 128, 0], {}, 2), ("lora", [2 * M, 64 * M, 64 * M, 64, 128, 1], {}, 2),
     ("lora", [16, 16384, 4096, 16, 16, 1], {}, 1), ("lora", [1, 64 * M, 4096, 1, 16, 1], {}, 2),
 ]
 

@@ -71,3 +71,23 @@ def test_binding_refuses_before_the_library():
         mx.mx_lora(x, a, b, i)  # not on a GPU
     with pytest.raises(TypeError):
         mx.mx_lora(None, a, b, i)
+
+
+def test_out_on_weights_and_tables(m):
+    """An out that shares a byte with a, b, index or scaling would be read while it is written. T, N of
+    3 x 100 bf16 in rows of 200 bytes; a has 4 x 24 x 64 values, b 4 x 100 x 24."""
+    bytes_of = {"a": 4 * 24 * 64 * 2, "b": 4 * 100 * 24 * 2, "index": 3 * 4, "scaling": 4 * 4}
+    for name, size in bytes_of.items():
+        for at in (P[name], P[name] + size - 2, P[name] - 3 * 200 + 2):
+            assert call(m, out=at) == m.MX_ERR_ARG, (name, at)
+        for row in range(3):  # rows of 200 bytes, 1 MiB apart
+            for at in (P[name] - 198, P[name] + size - 2):
+                assert call(m, out=at - (row << 20), ldo=1 << 19) == m.MX_ERR_ARG, (name, row, at)
+        # beside them and between the rows: not refused (without a GPU the launch is)
+        for at in (P[name] - 3 * 200, P[name] + size):
+            assert call(m, out=at) != m.MX_ERR_ARG, (name, at)
+        for at in (P[name] - 200, P[name] + size - (1 << 20), P[name] + size - (2 << 20)):
+            assert call(m, out=at, ldo=1 << 19) != m.MX_ERR_ARG, (name, at)
+    # in place is no way round it, and nothing is read without adapters
+    assert call(m, out=P["b"], base=P["b"], out_dtype=0, base_dtype=0) == m.MX_ERR_ARG
+    assert call(m, out=P["b"], adapters=0) != m.MX_ERR_ARG
