@@ -400,7 +400,8 @@ mx_status mx_cache_write(const mx_rows* k, const mx_rows* v, int32_t dtype, int6
 
 /* The T newest tokens' keys and values back as code * 2^(scale - 127), rounded to dtype once; NaN
  * where the scale is 0xFF, zeros where there is no page, or no token (more rows than the sequence
- * has). Errors as for mx_cache_write, and MX_ERR_ARG for k and v that overlap. */
+ * has). Errors as for mx_cache_write, and MX_ERR_ARG for k and v that overlap each other or the
+ * tables. */
 mx_status mx_cache_read(const mx_rows* k, const mx_rows* v, int32_t dtype, int64_t T,
                         const mx_cache* cache, void* stream);
 
@@ -419,8 +420,8 @@ mx_status mx_cache_read(const mx_rows* k, const mx_rows* v, int32_t dtype, int64
  * workspace: mx_cache_attention_workspace(...) bytes, 16-byte aligned, scratch: calls that may run at
  * the same time need one each (or -1 for arguments that the call refuses).
  * Errors as for mx_cache_write; MX_ERR_SHAPE for q_heads that is no multiple of heads; MX_ERR_ARG for
- * a scale that is not finite, a workspace that is too small, and an out or lse that overlaps q or the
- * other; MX_ERR_UNSUPPORTED for more than 65535 query heads, 2^30 rows of all of them, or 2^31
+ * a scale that is not finite, a workspace that is too small, and an out or lse that overlaps q, the
+ * other or the tables; MX_ERR_UNSUPPORTED for more than 65535 query heads, 2^30 rows of all of them, or 2^31
  * steps (16 rows by 32 tokens) if every sequence filled its table. */
 int64_t mx_cache_attention_workspace(int64_t T, int64_t q_heads, const mx_cache* cache);
 mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, int32_t dtype,

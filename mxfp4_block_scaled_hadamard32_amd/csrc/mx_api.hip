@@ -245,6 +245,21 @@ bool meets_cache(const Rows& span, const CacheArgs& c) {
          meet(span, Rows{c.ks, 1, blocks}, 1) || meet(span, Rows{c.vs, 1, blocks}, 1);
 }
 
+// `rows` rows on the tables of the cache
+bool meets_tables(const Rows& r, int64_t rows, const CacheArgs& c) {
+  return meet_block(r, c.pages, (int64_t)c.seqs * c.table_width * 4, rows) ||
+         meet_block(r, c.lengths, (int64_t)c.seqs * 4, rows) ||
+         meet_block(r, c.offsets, ((int64_t)c.seqs + 1) * 4, rows);
+}
+// the T tokens' rows of an output on the tables: token by token, or all that lies between them where
+// tokens are closer than their heads
+bool meets_tables(const CacheRows& o, const Rows& span, int64_t T, int64_t heads, int64_t esize,
+                  const CacheArgs& c) {
+  const int64_t width = ((heads - 1) * o.head + c.dim) * esize;
+  return T > 1 && width <= o.token * esize ? meets_tables(Rows{o.p, o.token * esize, width}, T, c)
+                                           : meets_tables(span, 1, c);
+}
+
 }  // namespace
 
 extern "C" {
@@ -543,6 +558,8 @@ mx_status mx_cache_read(const mx_rows* k, const mx_rows* v, int32_t dtype, int64
       rows_meet(rk, sk, c.heads, rv, sv, c.heads, T, c.dim, esize))
     return MX_ERR_ARG;
   if (T == 0 || c.seqs == 0 || c.heads == 0) return MX_OK;
+  if (meets_tables(rk, sk, T, c.heads, esize, c) || meets_tables(rv, sv, T, c.heads, esize, c))
+    return MX_ERR_ARG;
   return launch_status(mx_launch_cache_read(c, rk, rv, dtype == MX_BF16, stream));
 }
 
@@ -579,7 +596,8 @@ mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, i
   const int64_t esize = dtype == MX_BF16 ? 2 : 4;
   const Rows sl{lse, 1, T * q_heads * 4};
   if (rows_meet(rq, sq, q_heads, ro, so, q_heads, T, c.dim, esize) || meets_cache(so, c) ||
-      meets_cache(sl, c) || meet(sl, so, 1) || meet(sl, sq, 1))
+      meets_cache(sl, c) || meet(sl, so, 1) || meet(sl, sq, 1) ||
+      meets_tables(ro, so, T, q_heads, esize, c) || meets_tables(sl, 1, c))
     return MX_ERR_ARG;
   AttentionArgs a{rq.p, const_cast<void*>(ro.p), lse, rq.token, rq.head, ro.token, ro.head,
                   (int)q_heads, (int)q_heads / c.heads, scale * 1.4426950408889634f,

@@ -150,3 +150,31 @@ def test_binding_refuses_before_the_library():
         mx.mx_cache_attention(x[0], kq, ks, vq, vs, pages, lengths)
     with pytest.raises(ValueError):  # offsets without a number of rows
         mx.mx_cache_read(kq, ks, vq, vs, pages, lengths, offsets=z(4, dtype=torch.int32))
+
+
+def test_outputs_on_tables(m):
+    """Outputs that share a byte with the page table, the lengths or the offsets, which other workgroups
+    still read; beside them and between the rows of a strided output they are not refused (without a GPU
+    the launch is)."""
+    tables = {"pages": (0x24000000, 3 * 2 * 4), "lengths": (0x25000000, 3 * 4), "offsets": (0x26000000, 4 * 4)}
+    rows = {"mx_cache_read": 2, "mx_cache_attention": 4}
+    for where, size in tables.values():
+        for name, heads in rows.items():
+            row = heads * 64 * 2
+            for out in "ab" if name == "mx_cache_read" else "b":
+                kw = dict(offsets=0x26000000)
+                for at in (where, where - 3 * row + 16, where - 16 + (size + 15) // 16 * 16):
+                    assert call(m, name, **{out: at}, **kw) == m.MX_ERR_ARG, (name, out, at)
+                for i in range(3):
+                    assert call(m, name, token=1 << 15, **{out: where - (i << 16)}, **kw) == m.MX_ERR_ARG
+                for at in (where - 3 * row, where + (size + 15) // 16 * 16):
+                    assert call(m, name, **{out: at}, **kw) != m.MX_ERR_ARG, (name, out, at)
+                assert call(m, name, token=1 << 15, **{out: where - row - (1 << 16)}, **kw) != m.MX_ERR_ARG
+        for at in (where, where - 3 * 4 * 4 + 4, where + size - 4):
+            assert call(m, "mx_cache_attention", lse=at, offsets=0x26000000) == m.MX_ERR_ARG
+        for at in (where - 3 * 4 * 4, where + size):
+            assert call(m, "mx_cache_attention", lse=at, offsets=0x26000000) != m.MX_ERR_ARG
+    # heads before tokens: the whole extent counts
+    kw = dict(token=64, head=64 * 3, offsets=0x26000000)
+    for where, size in tables.values():
+        assert call(m, "mx_cache_read", b=where - 128, **kw) == m.MX_ERR_ARG
