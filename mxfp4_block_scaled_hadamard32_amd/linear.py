@@ -366,7 +366,7 @@ class MXDecodeLinear(torch.nn.Module):
 
 class MXAdapters(torch.nn.Module):
     """Low-rank adapters of one layer, B A of each: a [E][rank][K], b [E][N][rank] of the activations'
-    type (K and rank multiples of 8, rank at most 128), scaling [E] (ones when None)."""
+    type (K and rank multiples of 8, rank at most 128), scaling [E], kept in fp32 (ones when None)."""
 
     def __init__(self, a: torch.Tensor, b: torch.Tensor, scaling: torch.Tensor | None = None):
         super().__init__()
@@ -376,6 +376,14 @@ class MXAdapters(torch.nn.Module):
         self.register_buffer("b", b.detach().clone(memory_format=torch.contiguous_format))
         self.register_buffer("scaling", None if scaling is None else
                              scaling.detach().to(torch.float32, copy=True).contiguous())
+
+    def _apply(self, fn, recurse=True):
+        """Moves and changes of type (to, bfloat16, ..): the factors are fp32 whatever the weights are."""
+        scaling = self.scaling
+        super()._apply(fn, recurse)
+        if scaling is not None and self.scaling.dtype != torch.float32:
+            self.scaling = scaling.to(self.scaling.device)
+        return self
 
 
 def _readable_heads(t):

@@ -91,3 +91,20 @@ def test_out_on_weights_and_tables(m):
     # in place is no way round it, and nothing is read without adapters
     assert call(m, out=P["b"], base=P["b"], out_dtype=0, base_dtype=0) == m.MX_ERR_ARG
     assert call(m, out=P["b"], adapters=0) != m.MX_ERR_ARG
+
+
+def test_scaling_stays_fp32():
+    """A module's change of type takes the weights along, not the factors, which mx_lora has in fp32."""
+    from mxfp4_block_scaled_hadamard32_amd.linear import MXAdapters
+    a, b = torch.randn((2, 8, 64)), torch.randn((2, 32, 8))
+    s = torch.tensor([1.0 / 3.0, 1e30])
+    for change in (lambda m: m.to(torch.bfloat16), lambda m: m.bfloat16(), lambda m: m.double().float(),
+                   lambda m: torch.nn.Sequential(m).bfloat16()[0], lambda m: m.to("cpu", torch.bfloat16),
+                   lambda m: m.half()):
+        ad = MXAdapters(a, b, s)
+        got = change(ad)
+        assert got.scaling.dtype == torch.float32 and torch.equal(got.scaling, s)
+        assert got.a.dtype == got.b.dtype
+    assert MXAdapters(a, b).bfloat16().scaling is None and MXAdapters(a, b).bfloat16().a.dtype == torch.bfloat16
+    meta = MXAdapters(a, b, s).to("meta")
+    assert meta.scaling.device.type == "meta" and meta.a.device.type == "meta"
