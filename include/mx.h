@@ -389,8 +389,10 @@ typedef struct {
  * sequence and that is larger; where it grows the older codes are rounded again, to code * 2^(old -
  * new). Scales are powers of two, so that changes a code only below the format's least normal. A
  * token with an infinity or NaN makes its block's scale 0xFF and its tokens' codes zero, for good.
- * Slots of a block behind its last token keep what they hold. Two rows of a call must not fall into
- * one block from two sequences.
+ * Slots of a block behind its last token keep what they hold. Tokens that a later call writes over
+ * (drafts that were refused: lengths may shrink) leave the scale that they made to a block that holds
+ * older tokens too, and those the rounding to it, or the zeros of a 0xFF; a block that is written from its
+ * first slot on starts anew. Two rows of a call must not fall into one block from two sequences.
  * Errors (nothing is launched): MX_ERR_NULL; MX_ERR_SHAPE (negative sizes, T != seqs without
  * offsets, a distance below the rules); MX_ERR_ARG (dtype, fmt, scale_rule, page_size, alignment,
  * rows inside the cache); MX_ERR_UNSUPPORTED (dim, more than 2^20 sequences, 2^24 rows, 65535 heads

@@ -652,7 +652,8 @@ def mx_cache_write(k, v, kq, ks, vq, vs, pages, lengths, offsets=None, fmt: int 
     [pages][heads][page / 32] scales, all uint8. pages [B][..] int32 is the page table, lengths [B]
     int32 counts the sequences' tokens with these; rows offsets[b] .. offsets[b + 1] (int32, [B + 1])
     are the newest of sequence b, without offsets row b is. A block of 32 tokens whose scale has to
-    grow rounds its older codes again."""
+    grow rounds its older codes again; it keeps that scale when the tokens that needed it are written
+    over (refused drafts), unless it is written from its first slot on."""
     T = _row_count(k, "k")[0]
     c, H, D, at = _cache(kq, ks, vq, vs, pages, lengths, offsets, T, fmt)
     rk = _heads(k, "k", H, D, at)

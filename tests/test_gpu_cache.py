@@ -507,3 +507,35 @@ def test_attention_most_joined_rows(mx):
     want, _, tol = ref.attention(cache, one.expand(few, -1, -1), table[1], 190, dim ** -0.5, P_EPS["bf16"])
     err = (got[1 << 20:].cpu().double() - want).abs()
     assert (err <= tol + half * (want.abs() + tol)).all()
+
+
+@pytest.mark.parametrize("bad", [1e4, math.inf])
+def test_refused_drafts(mx, bad):
+    """A draft that is written over: the block keeps the scale that it made where older tokens stay, and
+    they what that scale left of them; written from the first slot on, it starts anew."""
+    heads, dim, page = 1, 64, 32
+    table, n_pages = ref.table_of([70], page)
+    cache = ref.Cache(n_pages, heads, page, dim, 0, seed=150)
+    dev = [t.to(DEV) for t in cache.tensors()]
+    k, v = rows(70, heads, dim, "bf16", 151, 0.5), rows(70, heads, dim, "bf16", 152, 0.5)
+
+    def write(first, count, kk=k, vv=v):
+        kk, vv = kk[first:first + count], vv[first:first + count]
+        off, n = i32([0, count]), first + count
+        mx.mx_cache_write(kk.to(DEV), vv.to(DEV), *dev, table.to(DEV), i32([n]), offsets=off)
+        cache.write(kk, vv, table[0], n)
+        for name, got, want in zip(("kq", "ks", "vq", "vs"), dev, cache.tensors()):
+            assert torch.equal(got.cpu(), want), (name, first, count)
+
+    first, second = cache.block(table[0], 32), cache.block(table[0], 64)
+    write(0, 40)
+    before = int(cache.ks[first[0], 0, first[1]])
+    draft = k.clone()
+    draft[41], draft[66] = bad, bad
+    write(40, 28, draft, v)     # in the block of tokens 32 .. and at the start of the next one
+    large = int(cache.ks[first[0], 0, first[1]])
+    assert large > before and (large == 255) == math.isinf(bad)
+    write(40, 24)               # refused: the same positions again
+    assert int(cache.ks[first[0], 0, first[1]]) == large
+    write(64, 3)                # tokens 64 .. from the block's first slot on
+    assert int(cache.ks[second[0], 0, second[1]]) < large
