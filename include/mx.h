@@ -412,7 +412,7 @@ mx_status mx_cache_read(const mx_rows* k, const mx_rows* v, int32_t dtype, int64
  *   out = sum_j p_j v_j,  p = softmax(scale * q . k_j).
  * q and out: dtype, [T][q_heads][dim]; lse (optional, [T][q_heads] fp32, contiguous): the natural
  * logarithm of the sum of exp(scale * q . k_j). A row that sees no token gets zeros and -infinity.
- * Keys and values are exact; q . k is formed in fp32 from exact products (bf16 q, or fp32 q as three
+ * Keys and values are exact (down to bf16's least subnormal, 2^-133); q . k is formed in fp32 from exact products (bf16 q, or fp32 q as three
  * bf16 terms); the statistics and sums are fp32; the probabilities keep 16 bits for a bf16 output and
  * 24 for fp32. Tokens whose scale is 0xFF make the rows that see them NaN (their lse with that of the
  * keys), and only those. Codes of NaN or infinity, which mx_cache_write does not leave, are not provided for.

@@ -139,3 +139,38 @@ def test_two_turns_of_threads(mx):
     lengths = [(53 * b) % 211 for b in range(300)]
     new = [min(n, 40 if b % 20 == 0 else b % 2) for b, n in enumerate(lengths)]
     check(mx, lengths, new, 16, 3, 64, 32, 64, "bf16", 0, seed=400)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("low,high,size", [(0, 13, 2.0 ** 108), (1, 30, 2.0 ** 90), (225, 238, 2.0 ** -100)])
+@pytest.mark.parametrize("dim,width", [(64, None), (128, 60), (256, 30)])
+def test_ends_of_the_scales(mx, low, high, size, fmt, dim, width, dtype):
+    """Scale bytes down to 0, which stands for a subnormal, and up to where sums of the values stay in
+    fp32's range. A code times its scale is exact down to bf16's least subnormal, 2^-133: below, half
+    of that comes to every key and value."""
+    lengths, new, heads, group, page = [90, 33], [3, 1], 2, 2, 32
+    table, n_pages = ref.table_of(lengths, page, width=width, seed=500)
+    cache = ref.Cache(n_pages, heads, page, dim, fmt, seed=500)
+    for b, n in enumerate(lengths):
+        cache.random_sequence(table[b], n, 500 + b, 0.4)
+    g = torch.Generator().manual_seed(501)
+    for s in (cache.ks, cache.vs):
+        s.copy_(torch.randint(low, high, s.shape, generator=g, dtype=torch.uint8))
+    q = (size * torch.randn((4, heads * group, dim), generator=g)).to(DT[dtype])
+    dev = [t.to(DEV) for t in cache.tensors()]
+    f = dim ** -0.5
+    got = mx.mx_cache_attention(q.to(DEV), *dev, table.to(DEV), i32(lengths), offsets=i32([0, 3, 4]),
+                                fmt=fmt).cpu().double()
+    half, least = torch.finfo(DT[dtype]).eps / 2, 2.0 ** -134
+    row = 0
+    for b, (length, n) in enumerate(zip(lengths, new)):
+        x = q[row:row + n]
+        want, _, tol = ref.attention(cache, x, table[b], length, f, P_EPS[dtype])
+        v = cache.tokens("v", table[b], 0, length)[0].abs().amax((0, 2)).repeat_interleave(group)
+        score = 2 * least * x.double().abs().sum(2, keepdim=True) * f
+        tol = tol + 2 * score * v[None, :, None] + 2 * least
+        err = (got[row:row + n] - want).abs()
+        assert torch.isfinite(got[row:row + n]).all()
+        assert (err <= tol + half * (want.abs() + tol) + least).all(), float((err / want.abs().amax()).max())
+        row += n
