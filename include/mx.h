@@ -412,10 +412,11 @@ mx_status mx_cache_read(const mx_rows* k, const mx_rows* v, int32_t dtype, int64
  *   out = sum_j p_j v_j,  p = softmax(scale * q . k_j).
  * q and out: dtype, [T][q_heads][dim]; lse (optional, [T][q_heads] fp32, contiguous): the natural
  * logarithm of the sum of exp(scale * q . k_j). A row that sees no token gets zeros and -infinity.
- * Keys and values are exact (down to bf16's least subnormal, 2^-133); q . k is formed in fp32 from exact products (bf16 q, or fp32 q as three
- * bf16 terms); the statistics and sums are fp32; the probabilities keep 16 bits for a bf16 output and
- * 24 for fp32. Tokens whose scale is 0xFF make the rows that see them NaN (their lse with that of the
- * keys), and only those. Codes of NaN or infinity, which mx_cache_write does not leave, are not provided for.
+ * Keys and values are exact (down to bf16's least subnormal, 2^-133); q . k is formed in fp32 from
+ * exact products (bf16 q, or fp32 q as three bf16 terms); the statistics and sums are fp32; the
+ * probabilities keep 16 bits for a bf16 output and 24 for fp32. Tokens whose scale is 0xFF make the rows
+ * that see them NaN (their lse with that of the keys), and only those. Codes of NaN or infinity, which
+ * mx_cache_write does not leave, are not provided for.
  * Lengths are read on the device, and long contexts are divided there: a call may be captured and
  * replayed with other lengths, pages and offsets. The order of the sums depends on the lengths of all
  * sequences of the call.
@@ -423,8 +424,9 @@ mx_status mx_cache_read(const mx_rows* k, const mx_rows* v, int32_t dtype, int64
  * the same time need one each (or -1 for arguments that the call refuses).
  * Errors as for mx_cache_write; MX_ERR_SHAPE for q_heads that is no multiple of heads; MX_ERR_ARG for
  * a scale that is not finite, a workspace that is too small, and an out or lse that overlaps q, the
- * other or the tables; MX_ERR_UNSUPPORTED for more than 65535 query heads, 2^30 rows of all of them, or 2^31
- * steps (16 rows by 32 tokens) if every sequence filled its table. */
+ * other or the tables; MX_ERR_UNSUPPORTED for more than 65535 query heads, 2^30 rows of all of them, or
+ * 2^31 steps of a head if every sequence filled its table (a step is 64 tokens, 32 for dim above 128, by
+ * 16, 32 or 64 rows: at least the rows that a sequence has of it on average, and 64 from 33 on). */
 int64_t mx_cache_attention_workspace(int64_t T, int64_t q_heads, const mx_cache* cache);
 mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, int32_t dtype,
                              int64_t T, int64_t q_heads, float scale, const mx_cache* cache,

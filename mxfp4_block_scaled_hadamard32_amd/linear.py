@@ -32,8 +32,8 @@ from dataclasses import dataclass, field
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (MX_E4M3, MX_E5M2, MX_ROUND_RNE, MX_SCALE_FLOOR, mx_cache_attention, mx_cache_read,
-               mx_cache_write, mx_gemm_dgrad, mx_gemm_fprop, mx_gemm_mxfp8, mx_gemm_wgrad, mx_gemv,
+from . import (MX_E4M3, MX_E5M2, MX_ROUND_RNE, MX_SCALE_CEIL, MX_SCALE_FLOOR, mx_cache_attention,
+               mx_cache_read, mx_cache_write, mx_gemm_dgrad, mx_gemm_fprop, mx_gemm_mxfp8, mx_gemm_wgrad, mx_gemv,
                mx_lora, mx_quantize, mx_quantize_2d_blocks, mx_quantize_mxfp8, mx_rmsnorm,
                mx_rmsnorm_backward, mx_rmsnorm_quant, mx_rmsnorm_quant_mxfp8)
 
@@ -412,10 +412,12 @@ class MXCache(torch.nn.Module):
     def __init__(self, pages: int, heads: int, dim: int, page_size: int = 64, fmt: int = MX_E4M3,
                  scale_rule: int = MX_SCALE_FLOOR, device="cuda"):
         super().__init__()
-        if page_size % 32:
-            raise ValueError("a page holds a multiple of 32 tokens")
+        if page_size % 32 or not 32 <= page_size <= 2048:
+            raise ValueError("a page holds a multiple of 32 tokens, 2048 at most")
         if dim not in (64, 128, 192, 256):
             raise ValueError("dim must be 64, 128, 192 or 256")
+        if fmt not in (MX_E4M3, MX_E5M2) or scale_rule not in (MX_SCALE_FLOOR, MX_SCALE_CEIL):
+            raise ValueError("fmt is MX_E4M3 or MX_E5M2, scale_rule MX_SCALE_FLOOR or MX_SCALE_CEIL")
         self.fmt, self.scale_rule = fmt, scale_rule
         byte = dict(dtype=torch.uint8, device=device)
         blocks = page_size // 32

@@ -178,3 +178,17 @@ def test_outputs_on_tables(m):
     kw = dict(token=64, head=64 * 3, offsets=0x26000000)
     for where, size in tables.values():
         assert call(m, "mx_cache_read", b=where - 128, **kw) == m.MX_ERR_ARG
+
+
+def test_module_refuses_what_no_call_takes():
+    """A cache that every call would refuse is not allocated."""
+    from mxfp4_block_scaled_hadamard32_amd.linear import MXCache
+    for bad in (dict(page_size=0), dict(page_size=-32), dict(page_size=48), dict(page_size=2080), dict(dim=96),
+                dict(dim=0), dict(fmt=2), dict(fmt=-1), dict(scale_rule=2), dict(scale_rule=-1)):
+        kw = dict(dim=64, page_size=32)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            MXCache(2, 1, device="cpu", **kw)
+    for page in (32, 2048):
+        c = MXCache(2, 3, 128, page, fmt=1, scale_rule=1, device="cpu")
+        assert c.kq.shape == (2, 3, page, 128) and c.vs.shape == (2, 3, page // 32)
