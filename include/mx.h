@@ -425,8 +425,9 @@ mx_status mx_cache_read(const mx_rows* k, const mx_rows* v, int32_t dtype, int64
  * Errors as for mx_cache_write; MX_ERR_SHAPE for q_heads that is no multiple of heads; MX_ERR_ARG for
  * a scale that is not finite, a workspace that is too small, and an out or lse that overlaps q, the
  * other or the tables; MX_ERR_UNSUPPORTED for more than 65535 query heads, 2^30 rows of all of them, or
- * 2^31 steps of a head if every sequence filled its table (a step is 64 tokens, 32 for dim above 128, by
- * 16, 32 or 64 rows: at least the rows that a sequence has of it on average, and 64 from 33 on). */
+ * 2^31 steps of a head if every sequence filled its table (a step is 64 tokens, 32 for dim above 128,
+ * by 16, 32 or 64 rows). One call takes one of these numbers of rows, by the sequences' average:
+ * prompts and single tokens are faster in calls of their own. */
 int64_t mx_cache_attention_workspace(int64_t T, int64_t q_heads, const mx_cache* cache);
 mx_status mx_cache_attention(const mx_rows* q, const mx_rows* out, float* lse, int32_t dtype,
                              int64_t T, int64_t q_heads, float scale, const mx_cache* cache,

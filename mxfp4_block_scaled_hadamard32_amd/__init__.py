@@ -690,7 +690,8 @@ def mx_cache_attention(q, kq, ks, vq, vs, pages, lengths, offsets=None, scale=No
     """Causal attention of each sequence's newest tokens over its cache (as for mx_cache_write): q
     [T][query heads][dim] bf16 or fp32, query head h over head h / (query heads / heads) of the cache,
     each row over the tokens up to its own -> out of q's shape and type, or (out, lse [T][query heads]
-    fp32) with with_lse or an lse buffer. scale: dim ** -0.5 when None. workspace: a uint8 buffer of at
+    fp32) with with_lse or an lse buffer. Prompts and single tokens are faster in calls of their own.
+    scale: dim ** -0.5 when None. workspace: a uint8 buffer of at
     least lib().mx_cache_attention_workspace(...) bytes, allocated per call when None."""
     T, heads = _row_count(q, "q")
     c, _, D, at = _cache(kq, ks, vq, vs, pages, lengths, offsets, T, fmt)

@@ -170,9 +170,9 @@ __device__ __forceinline__ uint32_t workgroup_max(uint32_t m) {
 // Writing. A workgroup of dim threads has the keys or the values of one block; a thread 32 of its
 // elements: of the keys four runs of 8 in a row, of the values 4 tokens x 8 channels, which make 8
 // words of a channel's 4 tokens each: no LDS but for the maximum, whole lines either way.
-// 8192 bf16 tokens, 8 heads of 128: 10.9 us, 4.6 TB/s read and written, what a copy reaches (12.4 with
-// the rows read after the page was known and each under its condition); 64 single tokens: 4.6 us, the
-// chain table - rows - maximum - store.
+// 8192 bf16 tokens, 8 heads of 128: 11.0 us in a row (12.0 by the tracer), 4.6 TB/s read and written, what
+// a copy reaches (1.5 us more with the rows read after the page was known and each under its condition);
+// 64 single tokens: 4.6 us, the chain table - rows - maximum - store.
 // ---------------------------------------------------------------------------------------------
 template <int D, int FMT, bool BF16, bool CEIL>
 __global__ __launch_bounds__(D) void cache_write_kernel(const CacheArgs c, const CacheRows k,
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(D) void cache_write_kernel(const CacheArgs c, const
 
 // ---------------------------------------------------------------------------------------------
 // Reading back: the same pieces. Positions that have no page (before the first token, too) are zeros.
-// 13750 tokens of 8 heads of 128 in bf16: 15.9 us, 5.3 TB/s.
+// 13750 tokens of 8 heads of 128 in bf16: 16.1 us, 5.2 TB/s.
 // ---------------------------------------------------------------------------------------------
 template <int D, int FMT, bool BF16>
 __global__ __launch_bounds__(D) void cache_read_kernel(const CacheArgs c, const CacheRows k,
@@ -340,14 +340,18 @@ __global__ __launch_bounds__(D) void cache_read_kernel(const CacheArgs c, const 
 //
 // Codes become bf16 with their block's scale in the converter (exact: 4 bits and a power of two).
 // q goes in as it is (bf16) or as three bf16 terms that add up to the fp32 value; P as two terms,
-// 16 bits, for a bf16 result (its rounding, 2^-9, would otherwise be felt beside the result's own) and
-// as three for fp32. Sums and the softmax's statistics are fp32, exponentials to the base 2.
+// 16 bits, for a bf16 result (the rounding of one, 2^-9, would be felt beside the result's own; with three
+// the results are as far from the 64-bit ones, 1.649e-3 of them, and drafts take 5 to 8% longer, single
+// tokens up to 2%) and as three for fp32. Sums and the softmax's statistics are fp32, exponentials to the
+// base 2.
 //
 // Work is divided where the lengths are known, on the device, and evenly: a sequence's rows, R = 16 WR
 // at a time, are an item, and the steps of all items, one after the other, are cut into as many equal
 // parts as there are workgroups (64 sequences of 500 to 16000 tokens, 64 heads over 8 of 128: 171 us, 6.2
-// TB/s; with a chunk of a sequence for each workgroup, whatever its length, 25 us more). Short and long
-// work and short tables differ, see the constants below. An item in one part is finished there; of the
+// TB/s; with a chunk of a sequence for each workgroup, whatever its length, 25 us more). An item counts
+// the whole sequence's steps, though its rows may see fewer: where most of a sequence is new, half of the
+// counted steps are empty (4096 tokens of 4096: 1128 us, 244 TFLOP/s; 512 of 2500: 107 us, 351). Short and
+// long work and short tables differ, see the constants below. An item in one part is finished there; of the
 // others each part goes to the workspace, and a second kernel joins them.
 //
 // Value codes are read as the product wants them, 4 lanes to a channel's 32 bytes. Key codes are read
@@ -598,7 +602,7 @@ __device__ __forceinline__ bool line_of(const CacheArgs& c, const AttentionArgs&
   return true;
 }
 
-// 16 codes as bf16 values times the scale
+// 8 codes as bf16 values times the scale
 template <int FMT>
 __device__ __forceinline__ bf16x8_t codes_of(uint32_t lo, uint32_t hi, float f) {
   if constexpr (FMT == 0) {
@@ -1108,11 +1112,15 @@ int64_t pieces(const CacheArgs& c) {
   return c.offsets ? (int64_t)c.rows / 32 + 2 * (int64_t)c.seqs : c.seqs;
 }
 
-// tokens of a step: wider heads take fewer, for their registers
+// tokens of a step: wider heads take fewer, for their registers (fp32 has too many all the same: 64
+// sequences of 3000 to 5000 tokens, 16 heads over 4: dim 128 56 us; 192, 7 registers spilled, 90; 256, 71
+// of them, 183)
 constexpr int step_tokens(int dim) { return dim <= 128 ? 64 : 32; }
 
 struct AttentionPlan {
-  int wr;          // row tiles of a workgroup
+  // Row tiles of a workgroup, from the average of the sequences' rows, which the host knows: an uneven call
+  // is slower than its parts (512 tokens of 2500 and 63 single ones of 8000: 408 us, 107 and 161 apart).
+  int wr;
   int64_t units;   // workgroups for each head
   int64_t slots;   // of the workspace, two for each workgroup
   bool whole;      // a workgroup for each item and head

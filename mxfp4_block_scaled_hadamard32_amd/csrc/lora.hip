@@ -200,9 +200,10 @@ __device__ __forceinline__ void accumulate(const LoraArgs& a, const Members& m, 
 
 // h = A x. Grid: parts of K, chunks of tokens, groups of 16 of their tokens. The four waves take every
 // fourth 64 of the part's K; their sums are joined in LDS in the waves' order.
-// 2048 tokens, K 4096, rank 64: 11.2 us. (Two or four 16s of tokens a workgroup, which read A once for
-// them, were no better while rows were read in the operands' order, 16.8 us to 17.5 and 15.0, 15.7 to
-// 18.4 and 19.8 for 256 tokens of 64 adapters, K 8192, rank 32; nor workgroups of 8 or 16 waves.)
+// 2048 tokens, K 4096, rank 64: 13.1 us by the tracer, 11.2 on one set of inputs again and again. (Two or
+// four 16s of tokens a workgroup, which read A once for them, and workgroups of 8 or 16 waves were tried
+// while rows were read in the operands' order, not since they are read whole: 16.8 us to 17.5 and 15.0, and
+// 15.7 to 18.4 and 19.8 for 256 tokens of 64 adapters, K 8192, rank 32.)
 template <bool BF16, int RT>
 __global__ __launch_bounds__(256) void lora_down_kernel(const LoraArgs a) {
   __shared__ __attribute__((aligned(16))) float sums[4][RT][16][20];
@@ -365,7 +366,7 @@ struct Up {
   // B's rows n .. n + 63, four neighbouring lanes a row's 64 bytes; then each lane's rows n + 4 i .. by
   // an exchange of registers. Read in that order directly, neighbouring lanes have different rows and
   // each 16 bytes are a line lookup of their own (2048 tokens of 64 adapters, N and K 4096, rank 16: 85
-  // us both kernels, 75 so; one token, N 14336: 8.5, 8.0; 2048 tokens of 4 adapters, rank 64: level).
+  // us both kernels, 74.5 so; one token, N 14336: 8.5, 7.8; 2048 tokens of 4 adapters, rank 64: level).
   static __device__ __forceinline__ void load_weights(const LoraArgs& a, const Members& m, int n,
                                                       u32x4 (&w)[JT][4]) {
     const int lane = threadIdx.x & 63, g = lane & 3;
@@ -599,8 +600,9 @@ hipError_t mx_launch_lora(LoraArgs a) {
   const int tokens = a.T < kChunk ? a.T : kChunk;
   a.groups = a.E < tokens ? a.E + 1 : tokens;  // adapters of a chunk, and its tokens without one
   // A workgroup sums h once for 256, 512 or 1024 outputs: as many as leave 448 workgroups, if every
-  // eighth adapter occurs in a chunk (2048 tokens, N 14336, rank 64, 4 adapters: 49, 48 and 44 us; 1024
-  // tokens, N 4096, rank 128: 27, 30 and 42; 2048 tokens of 64 adapters, N 4096, rank 16: 105, 84 and 72).
+  // eighth adapter occurs in a chunk (both kernels, K 4096: 2048 tokens of 64 adapters, N 4096, rank 16: 110,
+  // 86 and 74 us; 1024 tokens of 4, N 4096, rank 128: 40, 44 and 56; 2048 tokens of 4, N 14336, rank 64: 67,
+  // 67 and 69, where the rule takes the last; 8192 of 8, N 4096, rank 16: 68, 73 and 68).
   const int64_t chunks = (a.T + kChunk - 1) / kChunk, slabs = (a.N + 255) / 256;
   const int64_t apart = a.E < 16 ? 1 : a.E < kChunk ? a.E / 8 : kChunk / 8;
   a.slabs = 1;

@@ -33,9 +33,10 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import (MX_E4M3, MX_E5M2, MX_ROUND_RNE, MX_SCALE_CEIL, MX_SCALE_FLOOR, mx_cache_attention,
-               mx_cache_read, mx_cache_write, mx_gemm_dgrad, mx_gemm_fprop, mx_gemm_mxfp8, mx_gemm_wgrad, mx_gemv,
-               mx_lora, mx_quantize, mx_quantize_2d_blocks, mx_quantize_mxfp8, mx_rmsnorm,
-               mx_rmsnorm_backward, mx_rmsnorm_quant, mx_rmsnorm_quant_mxfp8)
+               mx_cache_read, mx_cache_write, mx_gemm_dgrad, mx_gemm_fprop, mx_gemm_mxfp8,
+               mx_gemm_wgrad, mx_gemv, mx_lora, mx_quantize, mx_quantize_2d_blocks,
+               mx_quantize_mxfp8, mx_rmsnorm, mx_rmsnorm_backward, mx_rmsnorm_quant,
+               mx_rmsnorm_quant_mxfp8)
 
 
 @dataclass
